@@ -412,6 +412,154 @@ int32_t moe_store_burst_probe(const moe_burst_params* params, void* dst, size_t 
 int32_t moe_mfma_rate_probe(int32_t format, int32_t blocks, int64_t iters, const void* operands,
                             size_t operand_bytes, int64_t* stamps, float* sink, void* stream);
 
+/* ---- Operators around the expert FFN --------------------------------------
+ * Routed rows in expert order: what the fused kernel does in one launch for
+ * inference, as separate operators with their gradients, for training the
+ * experts, for activations the fused kernel does not have and for dense layers
+ * in the fp8 format. They follow the conventions above and hold no state: no
+ * workspace, no allocation, every launch may be captured, and calls on
+ * different streams are independent.
+ *
+ * `row_offset` is the layout's (device int32 [L+1], row_offset[0] first): rows
+ * row_offset[e] .. row_offset[e+1]-1 belong to expert e. `rows` is the number
+ * of rows the row buffers have room for (at most 2^30). Offsets are read on
+ * the device; they must not decrease, and any past `rows` (or below 0) is
+ * taken as `rows` (0), so no access leaves the buffers. Rows outside
+ * row_offset[0] .. row_offset[L]-1 are neither read nor written. Leading
+ * dimensions (ld_*) count elements between rows, at least the row's length.
+ * Pointers need only their element's alignment; the fast kernels are taken
+ * when pointers are 16-byte aligned and rows (k, n and the leading dimensions)
+ * are whole multiples of 16 bytes, a slower kernel otherwise. */
+
+/* Rows of the local experts from the tokens (the gradient of
+ * moe_combine_rows): out[r] = x[row_pair[r] / top_k] for r < row_offset[L].
+ *   x         [tokens, hidden], elements of elem_bytes (1, 2 or 4) bytes
+ *   row_pair  device int32 [rows], flat pair index of each row (the layout's);
+ *             a row whose pair is not 0 .. tokens*top_k-1 becomes zeros
+ *   out       [rows, hidden] */
+typedef struct {
+  int64_t tokens;        /* N */
+  int64_t rows;          /* rows `out` has room for (dispatch) or `in` holds (combine) */
+  int32_t top_k;         /* 1..16 */
+  int32_t hidden;        /* elements of a row, any size >= 1 */
+  int32_t elem_bytes;    /* dispatch: 1, 2 or 4; combine: 2 (bf16) */
+  int32_t num_experts;   /* dispatch: L, entries of row_offset - 1; combine: ignored */
+  int32_t out_dtype;     /* combine: MOE_Y_FP32 or MOE_Y_BF16; dispatch: ignored */
+  int64_t ld_tokens;     /* row stride of x (dispatch) or y (combine) */
+  int64_t ld_rows;       /* row stride of out (dispatch) or in (combine) */
+} moe_rows_params;
+int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t* row_pair,
+                          const int32_t* row_offset, void* out, void* stream);
+
+/* Sum of each token's rows (the gradient of moe_dispatch_rows):
+ * y[n] = sum over j of in[pair_row[n*top_k + j]], in ascending j, in fp32,
+ * stored as out_dtype says; slots whose pair_row is not 0 .. rows-1 (the
+ * layout writes -1 for an expert that is not local) add nothing, and a token
+ * without any gets zeros. in: bf16 [rows, hidden]; y: [tokens, hidden]. */
+int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row, void* y,
+                         void* stream);
+
+/* Matrix products grouped by expert, bf16 with fp32 accumulation. For every
+ * expert e and its rows r:
+ *   MOE_GROUPED_FORWARD  y[r] = W[e] x[r]                 (writes y)
+ *   MOE_GROUPED_DGRAD    x[r] = W[e]^T y[r]               (writes x: the input gradient from y = dy)
+ *   MOE_GROUPED_WGRAD    W[e] = sum over r of y[r] x[r]^T (writes W: the weight gradient;
+ *                        an expert without rows gets zeros, with accumulate it stays)
+ * with x [rows, k], W [num_experts, n, k] and y [rows, n]. The two operands
+ * read are bf16; the one written is bf16 (rounded once from fp32) or fp32. */
+#define MOE_GROUPED_FORWARD 0
+#define MOE_GROUPED_DGRAD 1
+#define MOE_GROUPED_WGRAD 2
+typedef struct {
+  int32_t op;              /* MOE_GROUPED_* */
+  int32_t num_experts;     /* L, 1..MOE_MAX_LOCAL_EXPERTS */
+  int64_t rows;            /* rows of x and y */
+  int64_t expected_rows;   /* rows expected in all experts together (chooses the tile); 0 = rows */
+  int32_t n, k;            /* output and input features, any size >= 1 */
+  int64_t ld_x, ld_w, ld_y;
+  int64_t expert_stride_w; /* elements between experts' matrices */
+  int32_t out_dtype;       /* MOE_Y_FP32 or MOE_Y_BF16, of the operand written */
+  int32_t accumulate;      /* MOE_GROUPED_WGRAD: add to W instead of overwriting it */
+} moe_grouped_params;
+int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w,
+                           void* y, void* stream);
+
+/* SwiGLU of routed rows: h[r, i] = w_r silu(a[r, i]) a[r, I + i], silu(g) =
+ * g / (1 + e^-g), as the fused kernel's Linear-1 epilogue (w_r there applied
+ * after Linear-2). Computed in fp32, rounded once.
+ *   a           [rows, 2*inter] bf16, gate columns then up columns
+ *   row_weight  device fp32 [rows] or NULL (1)
+ *   row_offset  NULL: every row; else rows row_offset[0] .. row_offset[L]-1
+ *   h           MOE_SWIGLU_BF16: bf16 [rows, inter]; MOE_SWIGLU_FP8: e4m3 [rows,
+ *               inter] with h_scales, as moe_quantize_fp8 with 1 x 128 blocks
+ *               quantises the fp32 values
+ *   h_scales    fp32 [rows, ceil(inter/128)], or NULL */
+#define MOE_SWIGLU_BF16 0
+#define MOE_SWIGLU_FP8 1
+typedef struct {
+  int64_t rows;
+  int32_t inter;           /* I, any size >= 1 */
+  int32_t num_experts;     /* with row_offset */
+  int32_t out_format;      /* forward: MOE_SWIGLU_* */
+  int64_t ld_a, ld_h;      /* row strides of a (and da), and of h (dh) */
+  int64_t ld_scales;       /* row stride of h_scales */
+  int64_t ld_da;           /* backward */
+} moe_swiglu_params;
+int32_t moe_swiglu(const moe_swiglu_params* p, const void* a, const float* row_weight,
+                   const int32_t* row_offset, void* h, float* h_scales, void* stream);
+
+/* Gradients of moe_swiglu (bf16 form) for dh [rows, inter] bf16:
+ *   da           [rows, 2*inter] bf16: dg = dh w u s (1 + g (1 - s)), du = dh w g s,
+ *                s = 1 / (1 + e^-g); may be a itself
+ *   drow_weight  fp32 [rows] or NULL: sum over i of dh silu(g) u, in fp32 */
+int32_t moe_swiglu_backward(const moe_swiglu_params* p, const void* a, const void* dh,
+                            const float* row_weight, const int32_t* row_offset, void* da,
+                            float* drow_weight, void* stream);
+
+/* Quantisation to e4m3 with fp32 block scales, the MOE_FP8_E4M3 operand
+ * format: blocks of block_rows x 128 elements (edge blocks are smaller), scale
+ * = fp32(amax / 448), 1 where that is zero; code = the e4m3 value nearest to
+ * fp32(x / scale), ties to even. A block with an infinity or NaN gets that as
+ * its scale and NaN codes.
+ *   x       [batch, rows, cols] bf16 or fp32
+ *   codes   e4m3 bytes [batch, rows, cols]
+ *   scales  fp32 [batch, ceil(rows/block_rows), ceil(cols/128)], contiguous
+ *   row_offset  NULL, or with batch 1 and block_rows 1: only rows row_offset[0]
+ *           .. row_offset[L]-1 */
+typedef struct {
+  int64_t rows;
+  int32_t batch;           /* matrices, 1..65535 */
+  int32_t cols;            /* any size >= 1 */
+  int32_t block_rows;      /* 1 (activations) or 128 (weights) */
+  int32_t in_dtype;        /* MOE_Y_FP32 or MOE_Y_BF16 */
+  int32_t num_experts;     /* with row_offset */
+  int64_t ld_x, ld_codes;
+  int64_t batch_stride_x, batch_stride_codes;
+} moe_quantize_params;
+int32_t moe_quantize_fp8(const moe_quantize_params* p, const void* x, const int32_t* row_offset,
+                         void* codes, float* scales, void* stream);
+
+/* Matrix product of e4m3 operands with fp32 block scales (the MOE_FP8_E4M3
+ * format), dense (row_offset NULL, num_experts 1) or grouped by expert:
+ *   y[r, n] = sum over 128-wide K blocks b of
+ *             x_scales[r, b] w_scales[e, n/128, b] sum over k in b of x[r, k] W[e, n, k]
+ * with exact products, each block's sum and the sum over blocks in fp32.
+ *   x [rows, k], x_scales [rows, ceil(k/128)]; w [num_experts, n, k], w_scales
+ *   [num_experts, ceil(n/128), ceil(k/128)] (contiguous past ld_xs); y bf16 or
+ *   fp32 [rows, n]. */
+typedef struct {
+  int32_t num_experts;
+  int64_t rows;
+  int64_t expected_rows;   /* 0 = rows */
+  int32_t n, k;            /* any size >= 1 */
+  int64_t ld_x, ld_xs, ld_w, ld_y;
+  int64_t expert_stride_w; /* elements */
+  int32_t out_dtype;       /* MOE_Y_FP32 or MOE_Y_BF16 */
+} moe_fp8_params;
+int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const void* x,
+                       const float* x_scales, const void* w, const float* w_scales, void* y,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

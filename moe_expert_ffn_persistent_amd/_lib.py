@@ -24,18 +24,26 @@ MOE_SCHED_INTERLEAVED = 1
 MOE_MAX_SLICES = 64
 MOE_Y_FP32 = 0
 MOE_Y_BF16 = 1
+MOE_MAX_LOCAL_EXPERTS = 256
+MOE_GROUPED_FORWARD = 0
+MOE_GROUPED_DGRAD = 1
+MOE_GROUPED_WGRAD = 2
+MOE_SWIGLU_BF16 = 0
+MOE_SWIGLU_FP8 = 1
 
 # every symbol include/moe_ffn.h declares
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_layout_scratch_bytes", "moe_ffn_plan",
            "moe_workspace_init", "moe_dispatch_layout", "moe_ffn_forward", "moe_combine_check",
            "moe_store_burst_probe", "moe_predict_schedule", "moe_ffn_forward_noalloc",
-           "moe_mfma_rate_probe")
+           "moe_mfma_rate_probe", "moe_dispatch_rows", "moe_combine_rows", "moe_grouped_matmul",
+           "moe_swiglu", "moe_swiglu_backward", "moe_quantize_fp8", "moe_fp8_matmul")
 MFMA_PROBE_THREADS = 512
 MFMA_PROBE_OPERAND_BYTES = 64 * 64 * 16 * 16
 NOALLOC_WORKSPACE_BYTES = 64 << 20
 NOALLOC_MAX_SCHED_ROWS = 16384
 
 c_i32 = ctypes.c_int32
+c_i64 = ctypes.c_int64
 c_vp = ctypes.c_void_p
 
 
@@ -87,6 +95,35 @@ class MoeBurstParams(ctypes.Structure):
                 ("row_bytes", c_i32), ("control", c_i32), ("gap_ns", ctypes.c_int64)]
 
 
+class MoeRowsParams(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("rows", c_i64), ("top_k", c_i32), ("hidden", c_i32),
+                ("elem_bytes", c_i32), ("num_experts", c_i32), ("out_dtype", c_i32),
+                ("ld_tokens", c_i64), ("ld_rows", c_i64)]
+
+
+class MoeGroupedParams(ctypes.Structure):
+    _fields_ = [("op", c_i32), ("num_experts", c_i32), ("rows", c_i64), ("expected_rows", c_i64),
+                ("n", c_i32), ("k", c_i32), ("ld_x", c_i64), ("ld_w", c_i64), ("ld_y", c_i64),
+                ("expert_stride_w", c_i64), ("out_dtype", c_i32), ("accumulate", c_i32)]
+
+
+class MoeSwigluParams(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("inter", c_i32), ("num_experts", c_i32), ("out_format", c_i32),
+                ("ld_a", c_i64), ("ld_h", c_i64), ("ld_scales", c_i64), ("ld_da", c_i64)]
+
+
+class MoeQuantizeParams(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("batch", c_i32), ("cols", c_i32), ("block_rows", c_i32),
+                ("in_dtype", c_i32), ("num_experts", c_i32), ("ld_x", c_i64), ("ld_codes", c_i64),
+                ("batch_stride_x", c_i64), ("batch_stride_codes", c_i64)]
+
+
+class MoeFp8Params(ctypes.Structure):
+    _fields_ = [("num_experts", c_i32), ("rows", c_i64), ("expected_rows", c_i64), ("n", c_i32),
+                ("k", c_i32), ("ld_x", c_i64), ("ld_xs", c_i64), ("ld_w", c_i64), ("ld_y", c_i64),
+                ("expert_stride_w", c_i64), ("out_dtype", c_i32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} ({status})")
@@ -136,6 +173,16 @@ def load(path: str | None = None):
     lib.moe_predict_schedule.restype = c_i32
     lib.moe_predict_schedule.argtypes = [P(MoeShape), P(MoePlan), P(c_i32), P(MoeSchedParams),
                                          P(MoeSchedulePrediction)]
+    for fn, params, nptr in (("moe_dispatch_rows", MoeRowsParams, 4),
+                             ("moe_combine_rows", MoeRowsParams, 3),
+                             ("moe_grouped_matmul", MoeGroupedParams, 4),
+                             ("moe_swiglu", MoeSwigluParams, 5),
+                             ("moe_swiglu_backward", MoeSwigluParams, 6),
+                             ("moe_quantize_fp8", MoeQuantizeParams, 4),
+                             ("moe_fp8_matmul", MoeFp8Params, 6)):
+        f = getattr(lib, fn)
+        f.restype = c_i32
+        f.argtypes = [P(params)] + [c_vp] * (nptr + 1)
     _lib = lib
     return lib
 

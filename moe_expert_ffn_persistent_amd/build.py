@@ -21,8 +21,8 @@ LIB = os.path.join(PKG, "libmoe_ffn.so")
 ARCH = "gfx950"
 
 SOURCES = ["layout.hip", "ffn_bf16.hip", "ffn_fp8.hip", "ffn_w4a8.hip", "combine.hip", "burst.hip",
-           "mfma_probe.hip",
-           "api.cpp", "planner.cpp"]
+           "mfma_probe.hip", "rows.hip", "swiglu.hip", "gemm_any.hip",
+           "api.cpp", "ops_api.cpp", "planner.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

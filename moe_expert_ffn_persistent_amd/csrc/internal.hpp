@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "moe_ffn.h"
 
 namespace moe {
@@ -109,6 +111,58 @@ struct CheckArgs {
   int32_t* report;
 };
 hipError_t launch_check(const CheckArgs& a, hipStream_t stream);
+
+// Operators around the FFN (rows.hip, swiglu.hip, gemm_any.hip, ...). Leading
+// dimensions of rows are in bytes for RowsArgs, in elements elsewhere.
+struct RowsArgs {
+  const void* in;
+  void* out;
+  const int32_t* index;        // row_pair (dispatch) or pair_row (combine)
+  const int32_t* row_offset;   // dispatch
+  long long rows, pairs;       // capacity; tokens * k
+  long long ld_in, ld_out;
+  int k, hidden, elem, L;
+};
+hipError_t launch_dispatch_rows(const RowsArgs& a, hipStream_t s);
+hipError_t launch_combine_rows(const RowsArgs& a, bool bf16_out, hipStream_t s);
+
+struct SwigluArgs {
+  const void *a, *dh;
+  const float* weight;
+  const int32_t* row_offset;   // nullptr: every row
+  void *h, *da;
+  float *scales, *dweight;
+  long long rows, ld_a, ld_h, ld_scales, ld_da;
+  int inter, L;
+  bool vec;                    // rows are 16-byte aligned (codes: 8-byte)
+};
+hipError_t launch_swiglu(const SwigluArgs& a, bool fp8, hipStream_t s);
+hipError_t launch_swiglu_backward(const SwigluArgs& a, hipStream_t s);
+
+struct QuantArgs {
+  const void* x;
+  const int32_t* row_offset;
+  void* codes;
+  float* scales;
+  long long rows, ld_x, ld_codes, bs_x, bs_codes;
+  int batch, cols, L;
+  bool vec;
+};
+hipError_t launch_quantize(const QuantArgs& a, int block_rows, bool fp32, hipStream_t s);
+
+// Grouped products: x [rows, k], w [L, n, k], y [rows, n], one of them written
+// (op: MOE_GROUPED_*); the block-scaled e4m3 product is the forward form with
+// scales. row_offset nullptr: one expert with every row.
+struct GemmArgs {
+  const int32_t* row_offset;
+  void *x, *w, *y;
+  const float *xs, *ws;
+  long long ld_x, ld_w, ld_y, es_w, ld_xs;
+  int op, L, rows, n, k;
+  bool out_bf16, accumulate;
+  int expected;                // rows expected in all experts together
+};
+hipError_t launch_gemm_any(const GemmArgs& a, bool fp8, hipStream_t s);
 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t stream);
 

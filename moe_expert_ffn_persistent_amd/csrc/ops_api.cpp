@@ -1,0 +1,234 @@
+// Host side of the operators around the expert FFN: argument checks and
+// kernel choice. Nothing here allocates, waits or keeps state.
+#include <hip/hip_runtime.h>
+
+#include "internal.hpp"
+
+using namespace moe;
+
+namespace {
+
+constexpr long long kMaxRows = 1ll << 28;
+constexpr int kMaxCols = 1 << 20;
+
+int32_t done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+bool dtype_ok(int32_t d) { return d == MOE_Y_FP32 || d == MOE_Y_BF16; }
+
+// the tile of a 16-byte kernel by the rows an expert is expected to have
+int expected_rows(int64_t expected, int64_t rows) {
+  return (int)(expected > 0 && expected < rows ? expected : rows);
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t* row_pair,
+                          const int32_t* row_offset, void* out, void* stream) {
+  if (!p || p->tokens < 0 || p->rows < 0 || p->rows > kMaxRows || p->top_k < 1 || p->top_k > 16 || p->hidden < 1 ||
+      p->hidden > kMaxCols || (p->elem_bytes != 1 && p->elem_bytes != 2 && p->elem_bytes != 4) ||
+      p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->ld_tokens < p->hidden ||
+      p->ld_rows < p->hidden || p->tokens * p->top_k > (1ll << 30))
+    return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!row_pair || !row_offset || !out || (p->tokens && !x)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, p->elem_bytes) || !aligned(out, p->elem_bytes)) return MOE_ERR_INVALID_ARG;
+  RowsArgs a{};
+  a.in = x;
+  a.out = out;
+  a.index = row_pair;
+  a.row_offset = row_offset;
+  a.rows = p->rows;
+  a.pairs = p->tokens * p->top_k;
+  a.ld_in = p->ld_tokens * p->elem_bytes;
+  a.ld_out = p->ld_rows * p->elem_bytes;
+  a.k = p->top_k;
+  a.hidden = p->hidden;
+  a.elem = p->elem_bytes;
+  a.L = p->num_experts;
+  return done(launch_dispatch_rows(a, (hipStream_t)stream));
+}
+
+int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row, void* y, void* stream) {
+  if (!p || p->tokens < 0 || p->rows < 0 || p->rows > kMaxRows || p->top_k < 1 || p->top_k > 16 || p->hidden < 1 ||
+      p->hidden > kMaxCols || p->elem_bytes != 2 || !dtype_ok(p->out_dtype) || p->ld_tokens < p->hidden ||
+      p->ld_rows < p->hidden || p->tokens > (1ll << 23))
+    return MOE_ERR_INVALID_ARG;
+  if (p->tokens == 0) return MOE_OK;
+  if (!pair_row || !y || (p->rows && !in)) return MOE_ERR_INVALID_ARG;
+  const size_t out_elem = p->out_dtype == MOE_Y_BF16 ? 2 : 4;
+  if (!aligned(in, 2) || !aligned(y, out_elem)) return MOE_ERR_INVALID_ARG;
+  RowsArgs a{};
+  a.in = in;
+  a.out = y;
+  a.index = pair_row;
+  a.rows = p->rows;
+  a.pairs = p->tokens * p->top_k;
+  a.ld_in = p->ld_rows * 2;
+  a.ld_out = p->ld_tokens * (long long)out_elem;
+  a.k = p->top_k;
+  a.hidden = p->hidden;
+  a.elem = 2;
+  return done(launch_combine_rows(a, p->out_dtype == MOE_Y_BF16, (hipStream_t)stream));
+}
+
+int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w, void* y,
+                           void* stream) {
+  if (!p || p->op < MOE_GROUPED_FORWARD || p->op > MOE_GROUPED_WGRAD || p->num_experts < 1 ||
+      p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows || p->expected_rows < 0 ||
+      p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || p->ld_x < p->k || p->ld_w < p->k ||
+      p->ld_y < p->n || p->expert_stride_w < (p->num_experts > 1 ? (p->n - 1) * p->ld_w + p->k : 0) ||
+      !dtype_ok(p->out_dtype))
+    return MOE_ERR_INVALID_ARG;
+  const bool wgrad = p->op == MOE_GROUPED_WGRAD, fwd = p->op == MOE_GROUPED_FORWARD;
+  if (p->accumulate && !wgrad) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0 && (!wgrad || p->accumulate)) return MOE_OK;
+  if (!row_offset || !w || (p->rows && (!x || !y))) return MOE_ERR_INVALID_ARG;
+  const size_t oe = p->out_dtype == MOE_Y_BF16 ? 2 : 4;
+  if (!aligned(x, !fwd && !wgrad ? oe : 2) || !aligned(y, fwd ? oe : 2) || !aligned(w, wgrad ? oe : 2))
+    return MOE_ERR_INVALID_ARG;
+  GemmArgs a{};
+  a.row_offset = row_offset;
+  a.x = x;
+  a.w = w;
+  a.y = y;
+  a.ld_x = p->ld_x;
+  a.ld_w = p->ld_w;
+  a.ld_y = p->ld_y;
+  a.es_w = p->expert_stride_w;
+  a.op = p->op;
+  a.L = p->num_experts;
+  a.rows = (int)p->rows;
+  a.n = p->n;
+  a.k = p->k;
+  a.out_bf16 = p->out_dtype == MOE_Y_BF16;
+  a.accumulate = p->accumulate != 0;
+  a.expected = expected_rows(p->expected_rows, p->rows);
+  return done(launch_gemm_any(a, false, (hipStream_t)stream));
+}
+
+int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_weight, const int32_t* row_offset,
+                   void* h, float* h_scales, void* stream) {
+  if (!p || p->rows < 0 || p->rows > kMaxRows || p->inter < 1 || p->inter > kMaxCols || p->ld_a < 2ll * p->inter ||
+      p->ld_h < p->inter || (p->out_format != MOE_SWIGLU_BF16 && p->out_format != MOE_SWIGLU_FP8) ||
+      (row_offset && (p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS)))
+    return MOE_ERR_INVALID_ARG;
+  const bool fp8 = p->out_format == MOE_SWIGLU_FP8;
+  if (fp8 && p->ld_scales < (p->inter + 127) / 128) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!a_ || !h || (fp8 && !h_scales) || !aligned(a_, 2) || (!fp8 && !aligned(h, 2))) return MOE_ERR_INVALID_ARG;
+  SwigluArgs a{};
+  a.a = a_;
+  a.weight = row_weight;
+  a.row_offset = row_offset;
+  a.h = h;
+  a.scales = h_scales;
+  a.rows = p->rows;
+  a.ld_a = p->ld_a;
+  a.ld_h = p->ld_h;
+  a.ld_scales = p->ld_scales;
+  a.inter = p->inter;
+  a.L = p->num_experts;
+  a.vec = aligned(a_, 16) && aligned(h, fp8 ? 8 : 16) && p->inter % 8 == 0 && p->ld_a % 8 == 0 && p->ld_h % 8 == 0;
+  return done(launch_swiglu(a, fp8, (hipStream_t)stream));
+}
+
+int32_t moe_swiglu_backward(const moe_swiglu_params* p, const void* a_, const void* dh, const float* row_weight,
+                            const int32_t* row_offset, void* da, float* drow_weight, void* stream) {
+  if (!p || p->rows < 0 || p->rows > kMaxRows || p->inter < 1 || p->inter > kMaxCols || p->ld_a < 2ll * p->inter ||
+      p->ld_da < 2ll * p->inter || p->ld_h < p->inter ||
+      (row_offset && (p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS)))
+    return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!a_ || !dh || !da || !aligned(a_, 2) || !aligned(dh, 2) || !aligned(da, 2)) return MOE_ERR_INVALID_ARG;
+  SwigluArgs a{};
+  a.a = a_;
+  a.dh = dh;
+  a.weight = row_weight;
+  a.row_offset = row_offset;
+  a.da = da;
+  a.dweight = drow_weight;
+  a.rows = p->rows;
+  a.ld_a = p->ld_a;
+  a.ld_h = p->ld_h;
+  a.ld_da = p->ld_da;
+  a.inter = p->inter;
+  a.L = p->num_experts;
+  a.vec = aligned(a_, 16) && aligned(dh, 16) && aligned(da, 16) && p->inter % 8 == 0 && p->ld_a % 8 == 0 &&
+          p->ld_h % 8 == 0 && p->ld_da % 8 == 0;
+  return done(launch_swiglu_backward(a, (hipStream_t)stream));
+}
+
+int32_t moe_quantize_fp8(const moe_quantize_params* p, const void* x, const int32_t* row_offset, void* codes,
+                         float* scales, void* stream) {
+  if (!p || p->rows < 0 || p->rows > kMaxRows || p->batch < 1 || p->batch > 65535 || p->cols < 1 ||
+      p->cols > kMaxCols || (p->block_rows != 1 && p->block_rows != 128) || !dtype_ok(p->in_dtype) ||
+      p->ld_x < p->cols || p->ld_codes < p->cols)
+    return MOE_ERR_INVALID_ARG;
+  if (row_offset && (p->batch != 1 || p->block_rows != 1 || p->num_experts < 1 ||
+                     p->num_experts > MOE_MAX_LOCAL_EXPERTS))
+    return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (p->batch > 1 && (p->batch_stride_x < (p->rows - 1) * p->ld_x + p->cols ||
+                       p->batch_stride_codes < (p->rows - 1) * p->ld_codes + p->cols))
+    return MOE_ERR_INVALID_ARG;
+  if (p->block_rows == 128 && ((p->rows + 127) / 128) * ((p->cols + 127) / 128) > (1ll << 23))
+    return MOE_ERR_UNSUPPORTED;
+  const bool fp32 = p->in_dtype == MOE_Y_FP32;
+  const int xe = fp32 ? 4 : 2;
+  if (!x || !codes || !scales || !aligned(x, xe)) return MOE_ERR_INVALID_ARG;
+  QuantArgs a{};
+  a.x = x;
+  a.row_offset = row_offset;
+  a.codes = codes;
+  a.scales = scales;
+  a.rows = p->rows;
+  a.ld_x = p->ld_x;
+  a.ld_codes = p->ld_codes;
+  a.bs_x = p->batch > 1 ? p->batch_stride_x : 0;
+  a.bs_codes = p->batch > 1 ? p->batch_stride_codes : 0;
+  a.batch = p->batch;
+  a.cols = p->cols;
+  a.L = p->num_experts;
+  a.vec = aligned(x, 16) && aligned(codes, 8) && (a.ld_x * xe) % 16 == 0 && (a.bs_x * xe) % 16 == 0 &&
+          a.ld_codes % 8 == 0 && a.bs_codes % 8 == 0;
+  return done(launch_quantize(a, p->block_rows, fp32, (hipStream_t)stream));
+}
+
+int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const void* x, const float* x_scales,
+                       const void* w, const float* w_scales, void* y, void* stream) {
+  if (!p || p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows ||
+      p->expected_rows < 0 || p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || p->ld_x < p->k ||
+      p->ld_w < p->k || p->ld_y < p->n || p->ld_xs < (p->k + 127) / 128 ||
+      p->expert_stride_w < (p->num_experts > 1 ? (p->n - 1) * p->ld_w + p->k : 0) || !dtype_ok(p->out_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (!row_offset && p->num_experts != 1) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!x || !x_scales || !w || !w_scales || !y || !aligned(y, p->out_dtype == MOE_Y_BF16 ? 2 : 4))
+    return MOE_ERR_INVALID_ARG;
+  GemmArgs a{};
+  a.row_offset = row_offset;
+  a.x = const_cast<void*>(x);
+  a.w = const_cast<void*>(w);
+  a.y = y;
+  a.xs = x_scales;
+  a.ws = w_scales;
+  a.ld_x = p->ld_x;
+  a.ld_w = p->ld_w;
+  a.ld_y = p->ld_y;
+  a.es_w = p->expert_stride_w;
+  a.ld_xs = p->ld_xs;
+  a.op = MOE_GROUPED_FORWARD;
+  a.L = p->num_experts;
+  a.rows = (int)p->rows;
+  a.n = p->n;
+  a.k = p->k;
+  a.out_bf16 = p->out_dtype == MOE_Y_BF16;
+  a.expected = expected_rows(p->expected_rows, p->rows);
+  return done(launch_gemm_any(a, true, (hipStream_t)stream));
+}
+
+}  // extern "C"

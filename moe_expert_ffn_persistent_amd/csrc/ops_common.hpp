@@ -1,0 +1,178 @@
+// Device helpers shared by the operators around the expert FFN.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ffn_common.hpp"
+#include "moe_ffn.h"
+
+namespace moe {
+
+// One expert's rows: rows r0 .. r0+Me-1, and which of its M-blocks this is.
+struct Group {
+  int e, m, r0, Me;
+  bool ok;
+};
+
+// row_offset[i] of L experts, inside 0..rows whatever the array holds
+__device__ __forceinline__ int clamped_offset(const int32_t* off, int L, int rows, int i) {
+  return min(max(off[min(i, L)], 0), rows);
+}
+
+// M-block `p` of the experts' blocks of TM rows: every wavefront finds it by
+// itself, a lane looking at four experts (L <= 256), with one prefix sum over
+// the lanes. Not ok: past the last block.
+template <int TM>
+__device__ __forceinline__ Group find_group(const int32_t* off, int L, int rows, int p) {
+  static_assert(MOE_MAX_LOCAL_EXPERTS <= 256, "four experts a lane");
+  const int lane = threadIdx.x & 63;
+  int o[5], t[4];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) o[j] = clamped_offset(off, L, rows, lane * 4 + j);
+  int sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    t[j] = (max(o[j + 1] - o[j], 0) + TM - 1) / TM;
+    sum += t[j];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += v;
+  }
+  int q = p - (incl - sum);
+  const uint64_t hit = __ballot(q >= 0 && q < sum);
+  Group g{0, 0, 0, 0, hit != 0};
+  if (!g.ok) return g;
+  int e = lane * 4, r0 = o[0], Me = o[1] - o[0];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const bool past = e == lane * 4 + j && q >= t[j];
+    q -= past ? t[j] : 0;
+    e += past;
+    r0 = past ? o[j + 1] : r0;
+    Me = past ? o[j + 2] - o[j + 1] : Me;
+  }
+  const int src = __builtin_ctzll(hit);
+  g.e = __builtin_amdgcn_readlane(e, src);
+  g.m = __builtin_amdgcn_readlane(q, src);
+  g.r0 = __builtin_amdgcn_readlane(r0, src);
+  g.Me = __builtin_amdgcn_readlane(Me, src);
+  return g;
+}
+
+// Rows to work on: all of them, or row_offset[0] .. row_offset[L]-1.
+__device__ __forceinline__ void row_range(const int32_t* off, int L, long long rows, int& lo, int& hi) {
+  lo = off ? clamped_offset(off, L, (int)rows, 0) : 0;
+  hi = off ? clamped_offset(off, L, (int)rows, L) : (int)rows;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+}
+
+// Eight consecutive elements of which the first n exist (the others read as
+// zero, are not written). `vec`: the row is 16-byte aligned and n is 8.
+__device__ __forceinline__ void load8(const __bf16* p, int n, bool vec, float (&x)[8]) {
+  if (vec) {
+    unpack8(*reinterpret_cast<const uint4*>(p), x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void load8(const float* p, int n, bool vec, float (&x)[8]) {
+  if (vec) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? p[i] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store8(__bf16* p, int n, bool vec, const float (&x)[8]) {
+  if (vec) {
+    *reinterpret_cast<uint4*>(p) = pack8(x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (__bf16)x[i];
+  }
+}
+
+// Block scale of values whose largest magnitude has the fp32 bits `amax`
+// (taken as an integer maximum, which carries infinities and NaN along):
+// fp32(amax / 448), 1 for a block of zeros or one whose quotient underflows.
+__device__ __forceinline__ float block_scale(uint32_t amax) {
+  const float s = __builtin_bit_cast(float, amax) / 448.f;
+  return s == 0.f ? 1.f : s;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
+
+// The e4m3 codes of fp32(x[i] / scale), ties to even, exactly as a correctly
+// rounded division gives them, at the cost of a multiplication: x * (1/scale)
+// is within two units in the last place of the quotient, so the code can only
+// differ where that lies as near to a border between two codes (a tie: in the
+// normal range the 20 bits below the code's three mantissa bits are 0x80000);
+// those lanes, values in the code's subnormal range and scales whose reciprocal
+// is not a normal number divide. For normal data that is a few values in 10^4.
+__device__ __forceinline__ uint2 quant8(const float (&x)[8], float scale) {
+  const float inv = 1.f / scale;
+  float y[8];
+  bool near = !(scale > 1e-37f && scale < 1e37f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[i] = x[i] * inv;
+    const uint32_t b = abs_bits(y[i]);
+    near |= ((b - (0x80000u - 4u)) & 0xfffffu) <= 8u;
+    near |= b - 1u < 0x3c800000u - 1u;   // 0 < |y| < 2^-6
+  }
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i] / scale;
+  }
+  const bool finite = abs_bits(scale) < 0x7f800000u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -448.f), 448.f);
+  uint2 q{pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7])};
+  if (!finite) q = uint2{0x7f7f7f7fu, 0x7f7f7f7fu};
+  return q;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, bool vec, uint2 q) {
+  if (vec) {
+    *reinterpret_cast<uint2*>(p) = q;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+  }
+}
+
+// Integer maximum over the 16 lanes of a row of lanes (quantisation: a lane
+// holds 8 of a block's 128 columns).
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d, 64));
+  return v;
+}
+
+}  // namespace moe

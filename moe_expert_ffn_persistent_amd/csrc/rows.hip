@@ -1,0 +1,93 @@
+// Rows of the local experts gathered from the tokens (dispatch) and each
+// token's rows summed (combine): each other's gradients, both one pass over
+// the bytes.
+#include "internal.hpp"
+#include "ops_common.hpp"
+
+namespace moe {
+namespace {
+
+// out[r] = x[row_pair[r] / k]. A wavefront copies whole rows in pieces of V
+// bytes a lane, several in flight. The grid is fixed and strides over the rows
+// that exist: the layout's capacity (every pair local) is several times the
+// rows routed here, and a workgroup for each would mostly start and end.
+template <class V>
+__global__ void __launch_bounds__(256) moe_dispatch_rows_k(const RowsArgs a) {
+  int lo, hi;
+  row_range(a.row_offset, a.L, a.rows, lo, hi);
+  const int wave = uni((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  const int lane = threadIdx.x & 63;
+  const int n = a.hidden * a.elem / (int)sizeof(V);
+  for (int r = lo + wave; r < hi; r += gridDim.x * 4) {
+    const int f = uni(a.index[r]);
+    const bool ok = f >= 0 && f < a.pairs;
+    const V* src = reinterpret_cast<const V*>(static_cast<const char*>(a.in) + (size_t)(ok ? f / a.k : 0) * a.ld_in);
+    V* dst = reinterpret_cast<V*>(static_cast<char*>(a.out) + (size_t)r * a.ld_out);
+    int c = lane;
+    for (; c + 192 < n; c += 256) {
+      V v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = ok ? src[c + 64 * j] : V{};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dst[c + 64 * j] = v[j];
+    }
+    for (; c < n; c += 64) dst[c] = ok ? src[c] : V{};
+  }
+}
+
+// y[n] = sum of the token's rows, ascending slots, fp32. A workgroup of four
+// wavefronts takes a token, a lane eight columns at a time; the slots' row
+// indices are uniform (scalar loads), so slots of other GPUs cost nothing.
+template <bool BF16>
+__global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool vec) {
+  const int n = blockIdx.x;
+  const int32_t* idx = a.index + (size_t)n * a.k;
+  char* yrow = static_cast<char*>(a.out) + (size_t)n * a.ld_out;
+  for (int c = threadIdx.x * 8; c < a.hidden; c += 256 * 8) {
+    const int m = min(8, a.hidden - c);
+    const bool v = vec && m == 8;
+    float s[8] = {};
+    for (int j = 0; j < a.k; ++j) {
+      const int r = uni(idx[j]);
+      if (r < 0 || r >= a.rows) continue;
+      float x[8];
+      load8(reinterpret_cast<const __bf16*>(static_cast<const char*>(a.in) + (size_t)r * a.ld_in) + c, m, v, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += x[i];
+    }
+    if constexpr (BF16) {
+      store8(reinterpret_cast<__bf16*>(yrow) + c, m, v, s);
+    } else {
+      float* y = reinterpret_cast<float*>(yrow) + c;
+      if (v) {
+        reinterpret_cast<float4*>(y)[0] = float4{s[0], s[1], s[2], s[3]};
+        reinterpret_cast<float4*>(y)[1] = float4{s[4], s[5], s[6], s[7]};
+      } else {
+        for (int i = 0; i < m; ++i) y[i] = s[i];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_dispatch_rows(const RowsArgs& a, hipStream_t s) {
+  const uintptr_t bits = (uintptr_t)a.in | (uintptr_t)a.out | (uintptr_t)a.ld_in | (uintptr_t)a.ld_out |
+                         (uintptr_t)((size_t)a.hidden * a.elem);
+  const int grid = (int)std::min<long long>((a.rows + 3) / 4, 2048);
+  if (bits % 16 == 0) moe_dispatch_rows_k<uint4><<<grid, 256, 0, s>>>(a);
+  else if (bits % 4 == 0) moe_dispatch_rows_k<uint32_t><<<grid, 256, 0, s>>>(a);
+  else if (bits % 2 == 0) moe_dispatch_rows_k<uint16_t><<<grid, 256, 0, s>>>(a);
+  else moe_dispatch_rows_k<uint8_t><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_rows(const RowsArgs& a, bool bf16_out, hipStream_t s) {
+  const bool vec = (((uintptr_t)a.in | (uintptr_t)a.out | (uintptr_t)a.ld_in | (uintptr_t)a.ld_out) % 16) == 0;
+  const int tokens = (int)(a.pairs / a.k);
+  if (bf16_out) moe_combine_rows_k<true><<<tokens, 256, 0, s>>>(a, vec);
+  else moe_combine_rows_k<false><<<tokens, 256, 0, s>>>(a, vec);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,468 @@
+"""Operators around the expert FFN (include/moe_ffn.h, "Operators around the
+expert FFN"): rows dispatched to and combined from the local experts, matrix
+products grouped by expert with their gradients, SwiGLU, quantisation to e4m3
+with block scales and the block-scaled e4m3 product.
+
+Every call checks its tensors on the host (ValueError before anything is
+enqueued), enqueues one or a few kernels on ``stream`` (a torch.cuda.Stream;
+default: the current stream of the tensors' device) and returns without waiting. With
+``out`` given nothing is allocated and the call may be captured in a HIP
+graph. ``out`` must not overlap an input unless a function says it may. When a
+call allocates its output, rows that no expert owns hold whatever the memory
+held. Tensors used on a stream other than the one they were allocated on need
+the caller's ``record_stream``, as everywhere in torch.
+
+The functions record nothing for autograd; gradients are the operators named
+so. Given an input that requires grad while grad mode is on they raise, rather
+than return a tensor that silently cuts the graph: call them inside a
+torch.autograd.Function or under torch.no_grad().
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import (MOE_GROUPED_DGRAD, MOE_GROUPED_FORWARD, MOE_GROUPED_WGRAD, MOE_MAX_LOCAL_EXPERTS,
+                   MOE_SWIGLU_BF16, MOE_SWIGLU_FP8, MOE_Y_BF16, MOE_Y_FP32, MoeFp8Params,
+                   MoeGroupedParams, MoeQuantizeParams, MoeRowsParams, MoeSwigluParams)
+
+BLOCK = 128   # columns of one fp32 scale
+_OUT = {torch.bfloat16: MOE_Y_BF16, torch.float32: MOE_Y_FP32}
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _on(device, *named):
+    """Every tensor given is on ``device``, and grad mode would not be cut."""
+    grad = torch.is_grad_enabled()
+    for what, t in named:
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{what}: on {t.device}, need {device}")
+        if grad and t.requires_grad:
+            raise ValueError(f"{what} requires grad, and this operator records nothing for autograd: "
+                             "call it in a torch.autograd.Function or under torch.no_grad()")
+
+
+def _matrix(t, what, dtypes, dims=2):
+    """A tensor of ``dims`` dimensions and one of ``dtypes`` whose rows are
+    contiguous and do not overlap; returns the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what}: need a tensor, got {type(t).__name__}")
+    if t.dim() != dims:
+        raise ValueError(f"{what}: need {dims} dimensions, got shape {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: need dtype {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    rows, cols = t.shape[-2:]
+    if cols < 1:
+        raise ValueError(f"{what}: rows of no elements")
+    st = t.stride()
+    if cols > 1 and st[-1] != 1:
+        raise ValueError(f"{what}: rows must be contiguous (last stride 1, got {st[-1]})")
+    ld = st[-2] if rows > 1 else max(st[-2], cols)
+    if ld < cols:
+        raise ValueError(f"{what}: rows overlap (row stride {ld} under {cols} columns)")
+    return ld
+
+
+def _batch_stride(t, what, ld):
+    """Stride between the matrices of a 3-D tensor, which must not overlap."""
+    need = (t.shape[1] - 1) * ld + t.shape[2]
+    if t.shape[0] > 1 and t.stride(0) < need:
+        raise ValueError(f"{what}: matrices overlap (stride {t.stride(0)} under {need} elements)")
+    return t.stride(0) if t.shape[0] > 1 else need
+
+
+def _vector(t, what, n, dtype):
+    """A contiguous tensor of ``n`` elements of ``dtype``, any shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what}: need a contiguous {dtype} tensor of {n} elements")
+
+
+def _offsets(t):
+    """Experts of a row_offset tensor (int32 [L+1])."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("row_offset: need a contiguous int32 tensor [L+1]")
+    L = t.numel() - 1
+    if not 1 <= L <= MOE_MAX_LOCAL_EXPERTS:
+        raise ValueError(f"row_offset: {L} experts, need 1 to {MOE_MAX_LOCAL_EXPERTS}")
+    return L
+
+
+def _expected(expected_rows):
+    if expected_rows is None:
+        return 0
+    if expected_rows < 1:
+        raise ValueError(f"expected_rows: need at least 1, got {expected_rows}")
+    return int(expected_rows)
+
+
+def _need_device(device):
+    if device.type != "cuda":
+        raise ValueError(f"need tensors on a GPU, got {device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """An output for work on ``stream``, allocated for that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(name, device, params, ptrs, stream):
+    if device.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream() if stream is None else stream
+        st = getattr(_lib.load(), name)(ctypes.byref(params), *ptrs, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            st = getattr(_lib.load(), name)(ctypes.byref(params), *ptrs, s.cuda_stream)
+    if st != _lib.MOE_OK:
+        _lib.check(st, name)
+
+
+# ---- rows to and from the experts -------------------------------------------
+
+_ROW_TYPES = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4, torch.float8_e4m3fn: 1, torch.uint8: 1,
+              torch.int16: 2}
+
+
+def check_dispatch_inputs(x, row_pair, row_offset, top_k, out):
+    ldx = _matrix(x, "x", tuple(_ROW_TYPES))
+    N, H = x.shape
+    L = _offsets(row_offset)
+    if not 1 <= top_k <= 16:
+        raise ValueError(f"top_k: need 1 to 16, got {top_k}")
+    if not isinstance(row_pair, torch.Tensor) or row_pair.dtype != torch.int32 or not row_pair.is_contiguous():
+        raise ValueError("row_pair: need a contiguous int32 tensor")
+    ldo = _matrix(out, "out", (x.dtype,))
+    if out.shape[1] != H:
+        raise ValueError(f"out: rows of {out.shape[1]} elements, x has {H}")
+    if row_pair.numel() < out.shape[0]:
+        raise ValueError(f"row_pair: {row_pair.numel()} entries for {out.shape[0]} rows")
+    _on(x.device, ("x", x), ("row_pair", row_pair), ("row_offset", row_offset), ("out", out))
+    return MoeRowsParams(N, out.shape[0], top_k, H, _ROW_TYPES[x.dtype], L, 0, ldx, ldo)
+
+
+def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
+    """Rows of the local experts: ``out[r] = x[row_pair[r] // top_k]`` for r in
+    row_offset[0] .. row_offset[L]-1 (a layout's arrays). x [N, H] of 1-, 2- or
+    4-byte elements; out [rows, H], allocated with one row for every entry of
+    row_pair when not given. The gradient of combine_rows."""
+    if out is None:
+        _matrix(x, "x", tuple(_ROW_TYPES))
+        _need_device(x.device)
+        out = _empty((row_pair.numel(), x.shape[1]), x.dtype, x.device, stream)
+    p = check_dispatch_inputs(x, row_pair, row_offset, top_k, out)
+    _need_device(x.device)
+    _launch("moe_dispatch_rows", x.device, p,
+            (x.data_ptr(), row_pair.data_ptr(), row_offset.data_ptr(), out.data_ptr()), stream)
+    return out
+
+
+def check_combine_rows_inputs(rows, pair_row, top_k, out):
+    ldr = _matrix(rows, "rows", (torch.bfloat16,))
+    if not 1 <= top_k <= 16:
+        raise ValueError(f"top_k: need 1 to 16, got {top_k}")
+    if (not isinstance(pair_row, torch.Tensor) or pair_row.dtype != torch.int32 or not pair_row.is_contiguous()
+            or pair_row.numel() % top_k):
+        raise ValueError("pair_row: need a contiguous int32 tensor of top_k entries a token")
+    N = pair_row.numel() // top_k
+    ldo = _matrix(out, "out", tuple(_OUT))
+    if tuple(out.shape) != (N, rows.shape[1]):
+        raise ValueError(f"out: need shape {(N, rows.shape[1])}, got {tuple(out.shape)}")
+    _on(rows.device, ("rows", rows), ("pair_row", pair_row), ("out", out))
+    return MoeRowsParams(N, rows.shape[0], top_k, rows.shape[1], 2, 0, _OUT[out.dtype], ldo, ldr)
+
+
+def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Each token's rows summed in fp32, in ascending slot order: ``out[n] =
+    sum of rows[pair_row[n * top_k + j]]`` over the slots whose pair_row is not
+    negative. rows bf16 [R, H]; out [N, H] bf16 (rounded once) or fp32. The
+    gradient of dispatch_rows."""
+    if out is None:
+        _matrix(rows, "rows", (torch.bfloat16,))
+        _need_device(rows.device)
+        if out_dtype not in _OUT:
+            raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
+        out = _empty((pair_row.numel() // max(1, top_k), rows.shape[1]), out_dtype, rows.device, stream)
+    p = check_combine_rows_inputs(rows, pair_row, top_k, out)
+    _need_device(rows.device)
+    _launch("moe_combine_rows", rows.device, p, (rows.data_ptr(), pair_row.data_ptr(), out.data_ptr()), stream)
+    return out
+
+
+# ---- matrix products grouped by expert ---------------------------------------
+
+def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate=False):
+    """x [rows, k], w [L, n, k], y [rows, n]; the operand that ``op`` writes is
+    bf16 or fp32, the others bf16."""
+    bf16, out = (torch.bfloat16,), tuple(_OUT)
+    ldx = _matrix(x, "x" if op != MOE_GROUPED_DGRAD else "out", out if op == MOE_GROUPED_DGRAD else bf16)
+    ldw = _matrix(w, "w" if op != MOE_GROUPED_WGRAD else "out", out if op == MOE_GROUPED_WGRAD else bf16, 3)
+    ldy = _matrix(y, "dy" if op != MOE_GROUPED_FORWARD else "out", out if op == MOE_GROUPED_FORWARD else bf16)
+    L, n, k = w.shape
+    if _offsets(row_offset) != L:
+        raise ValueError(f"row_offset: {row_offset.numel() - 1} experts, the weights have {L}")
+    if x.shape[0] != y.shape[0] or x.shape[1] != k or y.shape[1] != n:
+        raise ValueError(f"shapes do not fit: [rows, k] {tuple(x.shape)}, [L, n, k] {tuple(w.shape)}, "
+                         f"[rows, n] {tuple(y.shape)}")
+    _on(x.device, ("rows", x), ("weights", w), ("rows", y), ("row_offset", row_offset))
+    written = x if op == MOE_GROUPED_DGRAD else w if op == MOE_GROUPED_WGRAD else y
+    return MoeGroupedParams(op, L, x.shape[0], _expected(expected_rows), n, k, ldx, ldw, ldy,
+                            _batch_stride(w, "weights", ldw), _OUT[written.dtype], int(accumulate))
+
+
+def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, stream):
+    p = check_grouped_inputs(op, x, w, y, row_offset, expected_rows, accumulate)
+    _need_device(x.device)
+    _launch("moe_grouped_matmul", x.device, p,
+            (row_offset.data_ptr(), x.data_ptr(), w.data_ptr(), y.data_ptr()), stream)
+
+
+def _grouped_out(shape, ref, out_dtype, stream):
+    if out_dtype not in _OUT:
+        raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
+    _need_device(ref.device)
+    return _empty(shape, out_dtype, ref.device, stream)
+
+
+def grouped_matmul(x, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, stream=None):
+    """``out[r] = w[e] @ x[r]`` for the rows r of every expert e (row_offset
+    [L+1]): x bf16 [rows, k], w bf16 [L, n, k], out [rows, n] bf16 or fp32.
+    ``expected_rows`` (default: all rows of x) is how many rows the experts
+    hold together, when the buffers have room for many more: it only chooses
+    the kernel's tile."""
+    if out is None:
+        _matrix(x, "x", (torch.bfloat16,))
+        _matrix(w, "w", (torch.bfloat16,), 3)
+        out = _grouped_out((x.shape[0], w.shape[1]), x, out_dtype, stream)
+    _grouped(MOE_GROUPED_FORWARD, x, w, out, row_offset, expected_rows, False, stream)
+    return out
+
+
+def grouped_matmul_dgrad(dy, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, stream=None):
+    """Input gradient of grouped_matmul: ``out[r] = w[e].T @ dy[r]``; dy bf16
+    [rows, n], out [rows, k] bf16 or fp32."""
+    if out is None:
+        _matrix(dy, "dy", (torch.bfloat16,))
+        _matrix(w, "w", (torch.bfloat16,), 3)
+        out = _grouped_out((dy.shape[0], w.shape[2]), dy, out_dtype, stream)
+    _grouped(MOE_GROUPED_DGRAD, out, w, dy, row_offset, expected_rows, False, stream)
+    return out
+
+
+def grouped_matmul_wgrad(dy, x, row_offset, out=None, out_dtype=torch.bfloat16, accumulate=False,
+                         expected_rows=None, stream=None):
+    """Weight gradient of grouped_matmul: ``out[e] = sum over its rows of the
+    outer products dy[r] x[r]``, [L, n, k] bf16 or fp32; an expert without rows
+    gets zeros. With ``accumulate`` the sums are added to ``out``."""
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        _matrix(x, "x", (torch.bfloat16,))
+        _matrix(dy, "dy", (torch.bfloat16,))
+        out = _grouped_out((_offsets(row_offset), dy.shape[1], x.shape[1]), x, out_dtype, stream)
+    _grouped(MOE_GROUPED_WGRAD, x, out, dy, row_offset, expected_rows, accumulate, stream)
+    return out
+
+
+# ---- SwiGLU -------------------------------------------------------------------
+
+def _check_gate_up(a, row_weight, row_offset):
+    lda = _matrix(a, "gate_up", (torch.bfloat16,))
+    rows, cols = a.shape
+    if cols % 2:
+        raise ValueError(f"gate_up: need gate and up columns, got {cols}")
+    if row_weight is not None:
+        _vector(row_weight, "row_weight", rows, torch.float32)
+    return rows, cols // 2, lda, 1 if row_offset is None else _offsets(row_offset)
+
+
+def check_swiglu_inputs(a, row_weight, row_offset, h, scales):
+    rows, I, lda, L = _check_gate_up(a, row_weight, row_offset)
+    ldh = _matrix(h, "out", (torch.bfloat16,) + _CODES)
+    if tuple(h.shape) != (rows, I):
+        raise ValueError(f"out: need shape {(rows, I)}, got {tuple(h.shape)}")
+    fp8 = h.dtype in _CODES
+    lds = 0
+    if fp8:
+        lds = _matrix(scales, "scales", (torch.float32,))
+        if tuple(scales.shape) != (rows, _blocks(I)):
+            raise ValueError(f"scales: need shape {(rows, _blocks(I))}, got {tuple(scales.shape)}")
+    elif scales is not None:
+        raise ValueError("scales belong to an e4m3 output")
+    _on(a.device, ("gate_up", a), ("row_weight", row_weight), ("row_offset", row_offset), ("out", h), ("scales", scales))
+    return MoeSwigluParams(rows, I, L, MOE_SWIGLU_FP8 if fp8 else MOE_SWIGLU_BF16, lda, ldh, lds, 0)
+
+
+def swiglu(gate_up, row_weight=None, row_offset=None, out=None, scales=None, out_dtype=torch.bfloat16, stream=None):
+    """``out[r] = row_weight[r] * silu(gate) * up`` with gate, up the halves of
+    gate_up [rows, 2 I] (bf16, the rows of grouped_matmul with the fused
+    kernel's w1). out bf16 [rows, I]; or e4m3 (out_dtype or out
+    torch.float8_e4m3fn or uint8) with fp32 ``scales`` [rows, ceil(I/128)], the
+    fp32 values quantised as quantize_fp8 does: then (out, scales) is returned.
+    With ``row_offset`` only the experts' rows are computed."""
+    if out is None or (scales is None and (out.dtype if out is not None else out_dtype) in _CODES):
+        rows, I, _, _ = _check_gate_up(gate_up, row_weight, row_offset)
+        _need_device(gate_up.device)
+        if out is None:
+            if out_dtype != torch.bfloat16 and out_dtype not in _CODES:
+                raise ValueError(f"out_dtype: need bfloat16, float8_e4m3fn or uint8, got {out_dtype}")
+            out = _empty((rows, I), out_dtype, gate_up.device, stream)
+        if scales is None and out.dtype in _CODES:
+            scales = _empty((rows, _blocks(I)), torch.float32, gate_up.device, stream)
+    p = check_swiglu_inputs(gate_up, row_weight, row_offset, out, scales)
+    _need_device(gate_up.device)
+    _launch("moe_swiglu", gate_up.device, p,
+            (gate_up.data_ptr(), _ptr(row_weight), _ptr(row_offset), out.data_ptr(), _ptr(scales)), stream)
+    return out if scales is None else (out, scales)
+
+
+def check_swiglu_backward_inputs(a, dh, row_weight, row_offset, da, drow_weight):
+    rows, I, lda, L = _check_gate_up(a, row_weight, row_offset)
+    ldh = _matrix(dh, "dh", (torch.bfloat16,))
+    ldda = _matrix(da, "out", (torch.bfloat16,))
+    if tuple(dh.shape) != (rows, I):
+        raise ValueError(f"dh: need shape {(rows, I)}, got {tuple(dh.shape)}")
+    if tuple(da.shape) != (rows, 2 * I):
+        raise ValueError(f"out: need shape {(rows, 2 * I)}, got {tuple(da.shape)}")
+    if drow_weight is not None:
+        _vector(drow_weight, "drow_weight", rows, torch.float32)
+    _on(a.device, ("gate_up", a), ("dh", dh), ("row_weight", row_weight), ("row_offset", row_offset), ("out", da),
+        ("drow_weight", drow_weight))
+    return MoeSwigluParams(rows, I, L, MOE_SWIGLU_BF16, lda, ldh, 0, ldda)
+
+
+def swiglu_backward(gate_up, dh, row_weight=None, row_offset=None, out=None, drow_weight=None, stream=None):
+    """Gradients of swiglu for dh bf16 [rows, I]: (dgate_up [rows, 2 I] bf16,
+    drow_weight fp32 [rows]); the second is None without row_weight and
+    drow_weight. ``out`` may be gate_up itself."""
+    if out is None or (drow_weight is None and row_weight is not None):
+        rows, I, _, _ = _check_gate_up(gate_up, row_weight, row_offset)
+        _need_device(gate_up.device)
+        if out is None:
+            out = _empty((rows, 2 * I), torch.bfloat16, gate_up.device, stream)
+        if drow_weight is None and row_weight is not None:
+            drow_weight = _empty((rows,), torch.float32, gate_up.device, stream)
+    p = check_swiglu_backward_inputs(gate_up, dh, row_weight, row_offset, out, drow_weight)
+    _need_device(gate_up.device)
+    _launch("moe_swiglu_backward", gate_up.device, p,
+            (gate_up.data_ptr(), dh.data_ptr(), _ptr(row_weight), _ptr(row_offset), out.data_ptr(),
+             _ptr(drow_weight)), stream)
+    return out, drow_weight
+
+
+# ---- e4m3 with block scales ----------------------------------------------------
+
+def _scale_shape(x, block_rows):
+    return tuple(x.shape[:-2]) + (-(-x.shape[-2] // block_rows), _blocks(x.shape[-1]))
+
+
+def check_quantize_inputs(x, block_rows, row_offset, codes, scales):
+    if block_rows not in (1, BLOCK):
+        raise ValueError(f"block_rows: need 1 or {BLOCK}, got {block_rows}")
+    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+        raise ValueError("x: need a matrix or a batch of matrices")
+    ldx = _matrix(x, "x", tuple(_OUT), x.dim())
+    ldc = _matrix(codes, "out", _CODES, x.dim())
+    if codes.shape != x.shape:
+        raise ValueError(f"out: need shape {tuple(x.shape)}, got {tuple(codes.shape)}")
+    shape = _scale_shape(x, block_rows)
+    if not isinstance(scales, torch.Tensor) or tuple(scales.shape) != shape:
+        raise ValueError(f"scales: need shape {shape}")
+    _vector(scales, "scales", scales.numel(), torch.float32)
+    L = 1
+    if row_offset is not None:
+        if x.dim() != 2 or block_rows != 1:
+            raise ValueError("row_offset goes with a matrix in 1 x 128 blocks")
+        L = _offsets(row_offset)
+    _on(x.device, ("x", x), ("row_offset", row_offset), ("out", codes), ("scales", scales))
+    batch = x.shape[0] if x.dim() == 3 else 1
+    bsx = _batch_stride(x, "x", ldx) if x.dim() == 3 else 0
+    bsc = _batch_stride(codes, "out", ldc) if x.dim() == 3 else 0
+    return MoeQuantizeParams(x.shape[-2], batch, x.shape[-1], block_rows, _OUT[x.dtype], L, ldx, ldc, bsx, bsc)
+
+
+def quantize_fp8(x, block_rows=1, row_offset=None, out=None, scales=None, stream=None):
+    """x (bf16 or fp32, [rows, cols] or [batch, rows, cols]) in the e4m3 format
+    with fp32 block scales of the fp8 kernels: (codes, scales). Blocks of
+    ``block_rows`` (1: activations, 128: weights) x 128 elements, scale = amax /
+    448 (1 for a block of zeros), codes the e4m3 values nearest to x / scale.
+    With ``row_offset`` ([rows, cols], 1 x 128 blocks) only the experts' rows."""
+    if out is None or scales is None:
+        if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+            raise ValueError("x: need a matrix or a batch of matrices")
+        if block_rows not in (1, BLOCK):
+            raise ValueError(f"block_rows: need 1 or {BLOCK}, got {block_rows}")
+        _need_device(x.device)
+        if out is None:
+            out = _empty(tuple(x.shape), torch.float8_e4m3fn, x.device, stream)
+        if scales is None:
+            scales = _empty(_scale_shape(x, block_rows), torch.float32, x.device, stream)
+    p = check_quantize_inputs(x, block_rows, row_offset, out, scales)
+    _need_device(x.device)
+    if p.batch:
+        _launch("moe_quantize_fp8", x.device, p, (x.data_ptr(), _ptr(row_offset), out.data_ptr(), scales.data_ptr()),
+                stream)
+    return out, scales
+
+
+def check_fp8_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None):
+    ldx = _matrix(x, "x", _CODES)
+    grouped = row_offset is not None
+    ldw = _matrix(w, "w", _CODES, 3 if grouped else 2)
+    ldxs = _matrix(x_scales, "x_scales", (torch.float32,))
+    ldy = _matrix(y, "out", tuple(_OUT))
+    rows, k = x.shape
+    n = w.shape[-2]
+    if n < 1:
+        raise ValueError("w: no output features")
+    if w.shape[-1] != k or tuple(y.shape) != (rows, n):
+        raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, w {tuple(w.shape)}, out {tuple(y.shape)}")
+    if tuple(x_scales.shape) != (rows, _blocks(k)):
+        raise ValueError(f"x_scales: need shape {(rows, _blocks(k))}, got {tuple(x_scales.shape)}")
+    shape = tuple(w.shape[:-2]) + (_blocks(n), _blocks(k))
+    if not isinstance(w_scales, torch.Tensor) or tuple(w_scales.shape) != shape:
+        raise ValueError(f"w_scales: need shape {shape}")
+    _vector(w_scales, "w_scales", w_scales.numel(), torch.float32)
+    L, es = 1, 0
+    if grouped:
+        L = _offsets(row_offset)
+        if w.shape[0] != L:
+            raise ValueError(f"row_offset: {L} experts, the weights have {w.shape[0]}")
+        es = _batch_stride(w, "w", ldw)
+    _on(x.device, ("x", x), ("x_scales", x_scales), ("w", w), ("w_scales", w_scales), ("row_offset", row_offset), ("out", y))
+    return MoeFp8Params(L, rows, _expected(expected_rows), n, k, ldx, ldxs, ldw, ldy, es, _OUT[y.dtype])
+
+
+def fp8_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=torch.bfloat16, expected_rows=None,
+               stream=None):
+    """``out = (x * x_scales) @ (w * w_scales).T`` of e4m3 operands: x [rows, k]
+    with scales [rows, ceil(k/128)], w [n, k] with scales [ceil(n/128),
+    ceil(k/128)]; grouped by expert with ``row_offset``: w [L, n, k], w_scales
+    [L, ...], every row times its expert's matrix. out [rows, n] bf16 or fp32.
+    ``expected_rows`` as for grouped_matmul."""
+    if out is None:
+        _matrix(x, "x", _CODES)
+        if out_dtype not in _OUT:
+            raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
+        _need_device(x.device)
+        out = _empty((x.shape[0], w.shape[-2]), out_dtype, x.device, stream)
+    p = check_fp8_inputs(x, x_scales, w, w_scales, row_offset, out, expected_rows)
+    _need_device(x.device)
+    _launch("moe_fp8_matmul", x.device, p,
+            (_ptr(row_offset), x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), out.data_ptr()),
+            stream)
+    return out

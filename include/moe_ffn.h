@@ -480,6 +480,8 @@ typedef struct {
   int64_t expert_stride_w; /* elements between experts' matrices */
   int32_t out_dtype;       /* MOE_Y_FP32 or MOE_Y_BF16, of the operand written */
   int32_t accumulate;      /* MOE_GROUPED_WGRAD: add to W instead of overwriting it */
+  int32_t tile;            /* kernel configuration; 0 = automatic, an id that does not take
+                              the call's operands is MOE_ERR_UNSUPPORTED */
 } moe_grouped_params;
 int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w,
                            void* y, void* stream);
@@ -555,6 +557,7 @@ typedef struct {
   int64_t ld_x, ld_xs, ld_w, ld_y;
   int64_t expert_stride_w; /* elements */
   int32_t out_dtype;       /* MOE_Y_FP32 or MOE_Y_BF16 */
+  int32_t tile;            /* as moe_grouped_params */
 } moe_fp8_params;
 int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const void* x,
                        const float* x_scales, const void* w, const float* w_scales, void* y,

@@ -104,7 +104,8 @@ class MoeRowsParams(ctypes.Structure):
 class MoeGroupedParams(ctypes.Structure):
     _fields_ = [("op", c_i32), ("num_experts", c_i32), ("rows", c_i64), ("expected_rows", c_i64),
                 ("n", c_i32), ("k", c_i32), ("ld_x", c_i64), ("ld_w", c_i64), ("ld_y", c_i64),
-                ("expert_stride_w", c_i64), ("out_dtype", c_i32), ("accumulate", c_i32)]
+                ("expert_stride_w", c_i64), ("out_dtype", c_i32), ("accumulate", c_i32),
+                ("tile", c_i32)]
 
 
 class MoeSwigluParams(ctypes.Structure):
@@ -121,7 +122,7 @@ class MoeQuantizeParams(ctypes.Structure):
 class MoeFp8Params(ctypes.Structure):
     _fields_ = [("num_experts", c_i32), ("rows", c_i64), ("expected_rows", c_i64), ("n", c_i32),
                 ("k", c_i32), ("ld_x", c_i64), ("ld_xs", c_i64), ("ld_w", c_i64), ("ld_y", c_i64),
-                ("expert_stride_w", c_i64), ("out_dtype", c_i32)]
+                ("expert_stride_w", c_i64), ("out_dtype", c_i32), ("tile", c_i32)]
 
 
 class MoeError(RuntimeError):

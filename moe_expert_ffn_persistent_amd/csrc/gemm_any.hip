@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) moe_gemm_any(const GemmArgs a) {
     g.r0 = clamped_offset(a.row_offset, a.L, a.rows, g.e);
     g.Me = max(clamped_offset(a.row_offset, a.L, a.rows, g.e + 1) - g.r0, 0);
   } else if (a.row_offset) {
-    g = find_group<kAnyTile>(a.row_offset, a.L, a.rows, blockIdx.x);
+    g = GroupScan<kAnyTile>(a.row_offset, a.L, a.rows).find(blockIdx.x);
     if (!g.ok) return;
     i0 = g.m * kAnyTile;
   } else {

@@ -1,0 +1,381 @@
+// Grouped bf16 matrix products (forward, input gradient, weight gradient) for
+// 16-byte aligned operands:
+//
+//   out(i, j) = sum over c of T(i, c) F(j, c)
+//   forward  i = row, j = n, c = k     T = x            F = W[e]
+//   dgrad    i = row, j = k, c = n     T = dy           F = W[e]^T
+//   wgrad    i = n,   j = k, c = row   T = dy^T         F = x^T
+//
+// F is the MFMA's A operand and T its B operand (v_mfma_f32_32x32x16_bf16), so
+// a lane ends up with one output row i and runs of four consecutive columns j.
+// An operand whose unit stride is c is staged in LDS as rows of 64 c (128
+// bytes) and read 16 bytes a lane; one whose unit stride is i or j (marked TR)
+// is staged as it lies in memory, 64 rows of c, and read by
+// ds_read_b64_tr_b16, which hands each lane four consecutive c of its column.
+// No operand is transposed through registers or in HBM.
+//
+// A stage is 64 c wide; an NS-deep ring of stages is filled by direct-to-LDS
+// copies issued between the MFMAs of an earlier stage, one workgroup barrier
+// per stage. A ragged end (the last c of a row, or of an expert's rows in
+// wgrad) is zeros in LDS: lanes past the end write a zero instead of copying.
+// Rows i past an expert's end repeat its last row and are not stored.
+#include "internal.hpp"
+#include "ops_common.hpp"
+
+namespace moe {
+namespace {
+
+// LDS byte addresses are the low words of the generic pointers used here
+#pragma clang diagnostic ignored "-Wint-to-pointer-cast"
+
+constexpr int kBK = 64;   // c per stage
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes a lane from base + voff (bytes) to LDS m0 + 16 * lane
+__device__ __forceinline__ void dma16s(uint32_t voff, const char* base, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
+}
+
+template <int TM_, int TN_, int WT_, int WF_, int NS_, int SP_, int OCC_>
+struct CfgG {
+  static constexpr int TM = TM_, TN = TN_, WT = WT_, WF = WF_, NS = NS_, SP = SP_;
+  static constexpr int OCC = OCC_;                 // workgroups per CU that LDS and registers are cut for
+  static constexpr int NW = WT * WF, THREADS = 64 * NW;
+  static constexpr int TT = TM / WT, FT = TN / WF; // rows and columns of a wavefront
+  static constexpr int TB = TT / 32, FB = FT / 32;
+  static constexpr int T_BYTES = TM * kBK * 2, F_BYTES = TN * kBK * 2;
+  static constexpr int STAGE = T_BYTES + F_BYTES;
+  static constexpr int NIT = T_BYTES / 1024 / NW, NIF = F_BYTES / 1024 / NW, NI = NIT + NIF;
+  static constexpr int EPI = NW * 32 * FT * 4;     // epilogue staging: 32 rows a wavefront, fp32
+  static constexpr int LDS = NS * STAGE > EPI ? NS * STAGE : EPI;
+  static constexpr int issue_slot(int i, int nm) { return i * nm * SP / (NI * 8); }
+  static_assert(T_BYTES % (1024 * NW) == 0 && F_BYTES % (1024 * NW) == 0, "copies split evenly over the wavefronts");
+  static_assert(NS >= 2 && NI * (NS - 1) <= 63, "vmcnt range");
+  static_assert(LDS * OCC <= 160 * 1024, "LDS");
+};
+
+// One operand: TX rows (i or j) by 64 c a stage.
+template <bool TR, int TX, int NW>
+struct Operand {
+  static constexpr int NI = TX * kBK * 2 / 1024 / NW;   // 1 KiB copies of a wavefront per stage
+  static constexpr int RB = TR ? TX * 2 : kBK * 2;      // bytes of an LDS row
+  static constexpr int RPI = 1024 / RB;                 // LDS rows per copy
+  const char* base;        // stage 0 (uniform)
+  long long step;          // bytes from one stage to the next
+  long long istep;         // TR: bytes between this wavefront's copies
+  uint32_t voff[TR ? 1 : NI];
+
+  // Physical place of what a lane reads. Normal rows: chunk c of row r sits at
+  // c ^ (r >> 1 & 7), so that 16 rows at one chunk hit distinct banks.
+  // TR rows: a transposing read takes 64 bytes of four consecutive rows for 32
+  // lanes, so 64-byte pieces are spread by the row over the 256-byte bank line.
+  __device__ __forceinline__ static int swz(int r) {
+    constexpr int NG = RB / 64;
+    if constexpr (!TR) return (r >> 1) & 7;
+    else if constexpr (NG >= 4) return r & 3;
+    else if constexpr (NG == 2) return (r >> 1) & 1;
+    else return 0;
+  }
+
+  // p: element (row 0, c 0) of the tile's matrix; x0: the tile's first row (i
+  // or j) of `nx`; ld: elements between rows of memory
+  __device__ __forceinline__ void setup(const void* p, long long ld, int x0, int nx) {
+    const int wave = uni((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+    const char* b = static_cast<const char*>(p);
+    if constexpr (!TR) {
+      base = b + (long long)x0 * ld * 2;
+      step = kBK * 2;
+      istep = 0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = (wave + NW * i) * RPI + lane / 8;
+        const int c = (lane & 7) ^ swz(r);
+        voff[i] = (uint32_t)min(r, nx - 1 - x0) * (uint32_t)(ld * 2) + c * 16;
+      }
+    } else {
+      const int r = lane * 16 / RB, pc = (lane * 16 % RB) / 16;
+      const int c = pc ^ (swz(wave * RPI + r) << 2);   // logical 16-byte piece
+      base = b + (long long)wave * RPI * ld * 2;
+      step = (long long)kBK * ld * 2;
+      istep = (long long)NW * RPI * ld * 2;
+      voff[0] = (uint32_t)r * (uint32_t)(ld * 2) + (uint32_t)min(x0 + c * 8, nx - 8) * 2;
+    }
+  }
+
+  __device__ __forceinline__ void issue(int i, int kt, uint32_t slot) const {
+    const uint32_t dst = uni(slot + ((threadIdx.x >> 6) + NW * i) * 1024);
+    if constexpr (!TR) dma16s(voff[i], base + kt * step, dst);
+    else dma16s(voff[0], base + kt * step + i * istep, dst);
+  }
+
+  // The last stage when it holds only `left` < 64 c: lanes past the end write zeros.
+  __device__ __forceinline__ void issue_tail(int kt, int left, char* slot) const {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = (wave + NW * i) * RPI + (TR ? lane * 16 / RB : lane / 8);
+      const bool in = TR ? r < left : ((lane & 7) ^ swz(r)) * 8 < left;
+      if (in) issue(i, kt, (uint32_t)(uintptr_t)slot);
+      else *reinterpret_cast<uint4*>(slot + (wave + NW * i) * 1024 + lane * 16) = uint4{0, 0, 0, 0};
+    }
+  }
+
+  // MFMA fragment of the 32 rows x0.. of k-step ks: lane l gets row l % 32,
+  // c = 16 ks + 8 (l / 32) .. + 7
+  __device__ __forceinline__ static bf16x8 frag(const char* stage, int x0, int ks) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (!TR) {
+      const int r = x0 + (lane & 31);
+      const int c = (2 * ks + (lane >> 5)) ^ swz(lane & 31);   // x0 is a multiple of 32
+      return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(stage + r * RB + c * 16));
+    } else {
+      // lane 16 q + i addresses row (i / 4) of its group's four, 8 bytes at
+      // column 4 (i % 4), and receives column i of the four rows
+      typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+      const int i = lane & 15, r = 16 * ks + 8 * (lane >> 5) + (i >> 2);
+      const int col = ((lane >> 4) & 1) * 32 + (i & 3) * 8;   // bytes in the 64-byte piece
+      const char* p = stage + r * RB + (((x0 / 32) ^ swz(r)) * 64) + col;
+      const char* p4 = stage + (r + 4) * RB + (((x0 / 32) ^ swz(r + 4)) * 64) + col;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uint32_t)(uintptr_t)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uint32_t)(uintptr_t)p4);
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    }
+  }
+};
+
+template <class C, bool TTR, bool FTR>
+struct TileG {
+  Operand<TTR, C::TM, C::NW> t;
+  Operand<FTR, C::TN, C::NW> f;
+  f32x16 acc[C::FB][C::TB];
+
+  __device__ __forceinline__ void issue(int i, int kt, uint32_t slot) const {
+    if (i < C::NIF) f.issue(i, kt, slot);
+    else t.issue(i - C::NIF, kt, slot + C::F_BYTES);
+  }
+
+  // One stage of MFMAs; with COPY the copies of stage kt_next spread over the
+  // first SP/8 of them. Fragments of k-step ks+1 are read during the MFMAs of
+  // k-step ks.
+  template <bool COPY>
+  __device__ __forceinline__ void compute(const char* stage, int wf, int wt, int kt_next, uint32_t slot) {
+    constexpr int KS = kBK / 16, NMF = C::FB * C::TB, NL = C::FB + C::TB;
+    bf16x8 af[2][C::FB], bf[2][C::TB];
+    auto load = [&](int ks, int q) {
+      if (q < C::FB) af[ks & 1][q] = f.frag(stage, wf * C::FT + q * 32, ks);
+      else bf[ks & 1][q - C::FB] = t.frag(stage + C::F_BYTES, wt * C::TT + (q - C::FB) * 32, ks);
+    };
+#pragma unroll
+    for (int q = 0; q < NL; ++q) load(0, q);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+      for (int m = 0; m < NMF; ++m) {
+        const int fb = m / C::TB, tb = m % C::TB;
+        acc[fb][tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[ks & 1][fb], bf[ks & 1][tb], acc[fb][tb], 0, 0, 0);
+        if (ks + 1 < KS) {
+#pragma unroll
+          for (int q = 0; q < NL; ++q)
+            if ((q < NMF ? q : NMF - 1) == m) load(ks + 1, q);
+        }
+        if constexpr (COPY) {
+#pragma unroll
+          for (int i = 0; i < C::NI; ++i)
+            if (C::issue_slot(i, KS * NMF) == ks * NMF + m) issue(i, kt_next, slot);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  // All of c: `nc` of them.
+  __device__ __forceinline__ void mainloop(char* lds, int nc, int wf, int wt) {
+#pragma unroll
+    for (int fb = 0; fb < C::FB; ++fb)
+#pragma unroll
+      for (int tb = 0; tb < C::TB; ++tb) acc[fb][tb] = f32x16{};
+    const uint32_t ring = (uint32_t)(uintptr_t)lds;
+    const int left = nc % kBK, full = nc / kBK, nk = full + (left != 0);
+    auto tail = [&](int kt) {
+      char* slot = lds + (kt % C::NS) * C::STAGE;
+      f.issue_tail(kt, left, slot);
+      t.issue_tail(kt, left, slot + C::F_BYTES);
+    };
+#pragma unroll
+    for (int s = 0; s < C::NS - 1; ++s) {
+      if (s < full) {
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i) issue(i, s, ring + s * C::STAGE);
+      } else if (s < nk) {
+        tail(s);
+      }
+    }
+    int slot = 0;
+    const int nmain = full - (C::NS - 1);   // stages that copy a later whole stage
+    for (int kt = 0; kt < nmain; ++kt) {
+      vm_wait<C::NI * (C::NS - 2)>();
+      lds_barrier();
+      const int nslot = slot == 0 ? C::NS - 1 : slot - 1;
+      compute<true>(lds + slot * C::STAGE, wf, wt, kt + C::NS - 1, ring + nslot * C::STAGE);
+      slot = slot + 1 == C::NS ? 0 : slot + 1;
+    }
+    for (int kt = max(nmain, 0); kt < nk; ++kt) {
+      // a tail stage's copies are fewer (and zeros written) in some lanes: wait for all
+      if (left) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else vm_wait_ahead<C::NI, C::NS - 2>(nk - 1 - kt);
+      lds_barrier();
+      if (left && kt + C::NS - 1 == full) tail(full);
+      compute<false>(lds + slot * C::STAGE, wf, wt, 0, 0);
+      slot = slot + 1 == C::NS ? 0 : slot + 1;
+    }
+  }
+
+  // Output rows i0 .. of ni, columns j0 .. of nj: every wavefront stages its 32
+  // rows by FT columns in its own LDS and writes whole pieces of 16 bytes, FT
+  // columns of a row together. ADD: the sum is added to what is there, in fp32,
+  // before the one rounding.
+  template <bool BF16, bool ADD>
+  __device__ __forceinline__ void store(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int wf,
+                                        int wt) {
+    constexpr bool PACK = BF16 && !ADD;               // staged as bf16, else as fp32
+    constexpr int EB = PACK ? 2 : 4, OB = BF16 ? 2 : 4;   // bytes of a staged and of an output element
+    constexpr int ROWB = C::FT * EB, NCH = ROWB / 16, RPP = 64 / NCH;
+    const int tid = opaque(threadIdx.x), lane = tid & 63;
+    char* mine = lds + (tid >> 6) * (32 * C::FT * 4);
+    lds_barrier();   // every wavefront is done with the ring
+#pragma unroll
+    for (int tb = 0; tb < C::TB; ++tb) {
+#pragma unroll
+      for (int fb = 0; fb < C::FB; ++fb) {
+        f32x16 v = acc[fb][tb];
+        asm volatile("" : "+v"(v));
+#pragma unroll
+        for (int g4 = 0; g4 < 4; ++g4) {
+          const int col = fb * 32 + (lane >> 5) * 4 + g4 * 8;
+          char* p = mine + stage_off<ROWB>(lane & 31, col * EB);
+          if constexpr (PACK)
+            *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(v[g4 * 4], v[g4 * 4 + 1]), pack_bf16x2(v[g4 * 4 + 2], v[g4 * 4 + 3])};
+          else
+            *reinterpret_cast<float4*>(p) = float4{v[g4 * 4], v[g4 * 4 + 1], v[g4 * 4 + 2], v[g4 * 4 + 3]};
+        }
+      }
+      // the staging is this wavefront's own: no barrier, only its writes landed
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const int c = lane % NCH, col = j0 + wf * C::FT + c * (16 / EB);
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += RPP) {
+        const int r = r0 + lane / NCH, i = i0 + wt * C::TT + tb * 32 + r;
+        if (i < ni && col < nj) {
+          const uint4 v = *reinterpret_cast<const uint4*>(mine + stage_off<ROWB>(r, c * 16));
+          char* p = static_cast<char*>(out) + ((long long)i * ld + col) * OB;
+          if constexpr (!ADD) {
+            *reinterpret_cast<uint4*>(p) = v;
+          } else {
+            const float4 s = __builtin_bit_cast(float4, v);
+            if constexpr (BF16) {
+              const uint2 o = *reinterpret_cast<const uint2*>(p);
+              *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(bf16_lo(o.x) + s.x, bf16_hi(o.x) + s.y),
+                                                   pack_bf16x2(bf16_lo(o.y) + s.z, bf16_hi(o.y) + s.w)};
+            } else {
+              const float4 o = *reinterpret_cast<const float4*>(p);
+              *reinterpret_cast<float4*>(p) = float4{o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w};
+            }
+          }
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  }
+};
+
+template <class C, int OP>
+__global__ void __launch_bounds__(C::THREADS, C::NW / 4 * C::OCC > 0 ? C::NW / 4 * C::OCC : 1) moe_gemm_bf16(const GemmArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  constexpr bool WG = OP == MOE_GROUPED_WGRAD;
+  const int wave = uni((int)(threadIdx.x >> 6)), wf = wave % C::WF, wt = wave / C::WF;
+  const int tile = xcd_tile(blockIdx.x);
+  TileG<C, WG, OP != MOE_GROUPED_FORWARD> g;
+  const __bf16* x = static_cast<const __bf16*>(a.x);
+  const __bf16* w = static_cast<const __bf16*>(a.w);
+  const __bf16* y = static_cast<const __bf16*>(a.y);
+  if constexpr (WG) {
+    const int mi = (a.n + C::TM - 1) / C::TM, ni = (a.k + C::TN - 1) / C::TN;
+    const int e = tile / (mi * ni);
+    if (e >= a.L) return;
+    int i, j;
+    tile_at(tile - e * mi * ni, mi, ni, i, j);
+    const int r0 = uni(clamped_offset(a.row_offset, a.L, a.rows, e));
+    const int Me = uni(max(clamped_offset(a.row_offset, a.L, a.rows, e + 1) - r0, 0));
+    if (Me == 0 && a.accumulate) return;
+    g.t.setup(y + (long long)r0 * a.ld_y, a.ld_y, i * C::TM, a.n);
+    g.f.setup(x + (long long)r0 * a.ld_x, a.ld_x, j * C::TN, a.k);
+    g.mainloop(lds, Me, wf, wt);
+    char* out = static_cast<char*>(a.w) + (long long)e * a.es_w * (a.out_bf16 ? 2 : 4);
+    const int i0 = i * C::TM, j0 = j * C::TN;
+    if (a.out_bf16) {
+      if (a.accumulate) g.template store<true, true>(lds, out, a.ld_w, i0, a.n, j0, a.k, wf, wt);
+      else g.template store<true, false>(lds, out, a.ld_w, i0, a.n, j0, a.k, wf, wt);
+    } else {
+      if (a.accumulate) g.template store<false, true>(lds, out, a.ld_w, i0, a.n, j0, a.k, wf, wt);
+      else g.template store<false, false>(lds, out, a.ld_w, i0, a.n, j0, a.k, wf, wt);
+    }
+  } else {
+    constexpr bool FWD = OP == MOE_GROUPED_FORWARD;
+    const int nj = FWD ? a.n : a.k, nc = FWD ? a.k : a.n, ni = (nj + C::TN - 1) / C::TN;
+    const GroupScan<C::TM> scan(a.row_offset, a.L, a.rows);
+    if (tile >= scan.total * ni) return;
+    int p, j;
+    tile_at(tile, scan.total, ni, p, j);
+    const Group gr = scan.find(p);
+    const long long ldt = FWD ? a.ld_x : a.ld_y, ldo = FWD ? a.ld_y : a.ld_x;
+    g.t.setup((FWD ? x : y) + (long long)gr.r0 * ldt, ldt, gr.m * C::TM, gr.Me);
+    g.f.setup(w + (long long)gr.e * a.es_w, a.ld_w, j * C::TN, nj);
+    g.mainloop(lds, nc, wf, wt);
+    char* out = static_cast<char*>(FWD ? a.y : a.x) + (long long)gr.r0 * ldo * (a.out_bf16 ? 2 : 4);
+    if (a.out_bf16) g.template store<true, false>(lds, out, ldo, gr.m * C::TM, gr.Me, j * C::TN, nj, wf, wt);
+    else g.template store<false, false>(lds, out, ldo, gr.m * C::TM, gr.Me, j * C::TN, nj, wf, wt);
+  }
+}
+
+//                   rows cols  wavefronts ring spread workgroups per CU
+using Large = CfgG<256, 256, 2, 4, 2, 2, 1>;
+using Medium = CfgG<128, 256, 2, 4, 3, 4, 1>;
+using Square = CfgG<128, 128, 2, 2, 2, 4, 2>;
+using Small = CfgG<64, 128, 1, 4, 3, 4, 2>;
+
+template <class C, int OP>
+hipError_t launch(const GemmArgs& a, hipStream_t s) {
+  const long long nj = ((OP == MOE_GROUPED_FORWARD ? a.n : a.k) + C::TN - 1) / C::TN;
+  const long long mi = OP == MOE_GROUPED_WGRAD ? (long long)a.L * ((a.n + C::TM - 1) / C::TM)
+                                               : ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM;
+  const long long grid = (nj * mi + 255) / 256 * 256;   // xcd_tile deals 256 at a time
+  if (grid * C::THREADS >= (1ll << 32)) return launch_gemm_any(a, false, s);
+  moe_gemm_bf16<C, OP><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int OP>
+hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
+  switch (id) {
+    case 1: return launch<Large, OP>(a, s);
+    case 2: return launch<Medium, OP>(a, s);
+    case 3: return launch<Square, OP>(a, s);
+    case 4: return launch<Small, OP>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s) {
+  switch (a.op) {
+    case MOE_GROUPED_FORWARD: return launch_tile<MOE_GROUPED_FORWARD>(id, a, s);
+    case MOE_GROUPED_DGRAD: return launch_tile<MOE_GROUPED_DGRAD>(id, a, s);
+    default: return launch_tile<MOE_GROUPED_WGRAD>(id, a, s);
+  }
+}
+
+}  // namespace moe

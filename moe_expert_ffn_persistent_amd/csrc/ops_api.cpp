@@ -22,6 +22,12 @@ int expected_rows(int64_t expected, int64_t rows) {
   return (int)(expected > 0 && expected < rows ? expected : rows);
 }
 
+int choose_bf16(const GemmArgs& a) {
+  const long long avg = a.expected / a.L;
+  if (a.op == MOE_GROUPED_WGRAD) return (long long)a.L * ((a.n + 255) / 256) * ((a.k + 255) / 256) >= 256 ? 1 : 3;
+  return avg > 192 ? 1 : avg > 64 ? 2 : 4;
+}
+
 }  // namespace
 
 extern "C" {
@@ -81,7 +87,7 @@ int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offse
       p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows || p->expected_rows < 0 ||
       p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || p->ld_x < p->k || p->ld_w < p->k ||
       p->ld_y < p->n || p->expert_stride_w < (p->num_experts > 1 ? (p->n - 1) * p->ld_w + p->k : 0) ||
-      !dtype_ok(p->out_dtype))
+      !dtype_ok(p->out_dtype) || p->tile < 0)
     return MOE_ERR_INVALID_ARG;
   const bool wgrad = p->op == MOE_GROUPED_WGRAD, fwd = p->op == MOE_GROUPED_FORWARD;
   if (p->accumulate && !wgrad) return MOE_ERR_INVALID_ARG;
@@ -107,7 +113,14 @@ int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offse
   a.out_bf16 = p->out_dtype == MOE_Y_BF16;
   a.accumulate = p->accumulate != 0;
   a.expected = expected_rows(p->expected_rows, p->rows);
-  return done(launch_gemm_any(a, false, (hipStream_t)stream));
+  // The 16-byte kernels: rows of every operand start and end on 16 bytes, and
+  // their lane offsets (256 rows of a tile) fit 32 bits.
+  const bool fast = aligned(x, 16) && aligned(w, 16) && aligned(y, 16) && p->n % 8 == 0 && p->k % 8 == 0 &&
+                    p->ld_x % 8 == 0 && p->ld_w % 8 == 0 && p->ld_y % 8 == 0 && p->expert_stride_w % 8 == 0 &&
+                    std::max(p->ld_x, std::max(p->ld_w, p->ld_y)) <= (1 << 22);
+  if (p->tile > kBf16GemmTiles || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
+  if (!fast) return done(launch_gemm_any(a, false, (hipStream_t)stream));
+  return done(launch_gemm_bf16(p->tile > 0 ? p->tile : choose_bf16(a), a, (hipStream_t)stream));
 }
 
 int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_weight, const int32_t* row_offset,
@@ -203,8 +216,9 @@ int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const
   if (!p || p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows ||
       p->expected_rows < 0 || p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || p->ld_x < p->k ||
       p->ld_w < p->k || p->ld_y < p->n || p->ld_xs < (p->k + 127) / 128 ||
-      p->expert_stride_w < (p->num_experts > 1 ? (p->n - 1) * p->ld_w + p->k : 0) || !dtype_ok(p->out_dtype))
+      p->expert_stride_w < (p->num_experts > 1 ? (p->n - 1) * p->ld_w + p->k : 0) || !dtype_ok(p->out_dtype) || p->tile < 0)
     return MOE_ERR_INVALID_ARG;
+  if (p->tile > 0) return MOE_ERR_UNSUPPORTED;
   if (!row_offset && p->num_experts != 1) return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
   if (!x || !x_scales || !w || !w_scales || !y || !aligned(y, p->out_dtype == MOE_Y_BF16 ? 2 : 4))

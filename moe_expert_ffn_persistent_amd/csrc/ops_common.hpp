@@ -20,47 +20,75 @@ __device__ __forceinline__ int clamped_offset(const int32_t* off, int L, int row
   return min(max(off[min(i, L)], 0), rows);
 }
 
-// M-block `p` of the experts' blocks of TM rows: every wavefront finds it by
-// itself, a lane looking at four experts (L <= 256), with one prefix sum over
-// the lanes. Not ok: past the last block.
+// The experts' M-blocks of TM rows, counted by every wavefront for itself: a
+// lane looks at four experts (L <= 256), one prefix sum over the lanes.
 template <int TM>
-__device__ __forceinline__ Group find_group(const int32_t* off, int L, int rows, int p) {
+struct GroupScan {
   static_assert(MOE_MAX_LOCAL_EXPERTS <= 256, "four experts a lane");
-  const int lane = threadIdx.x & 63;
-  int o[5], t[4];
+  int o[5], t[4], excl, sum;
+  int total;   // M-blocks of all experts
+
+  __device__ __forceinline__ GroupScan(const int32_t* off, int L, int rows) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int j = 0; j < 5; ++j) o[j] = clamped_offset(off, L, rows, lane * 4 + j);
-  int sum = 0;
+    for (int j = 0; j < 5; ++j) o[j] = clamped_offset(off, L, rows, lane * 4 + j);
+    sum = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    t[j] = (max(o[j + 1] - o[j], 0) + TM - 1) / TM;
-    sum += t[j];
+    for (int j = 0; j < 4; ++j) {
+      t[j] = (max(o[j + 1] - o[j], 0) + TM - 1) / TM;
+      sum += t[j];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += v;
+    }
+    excl = incl - sum;
+    total = __builtin_amdgcn_readlane(incl, 63);
   }
-  int incl = sum;
+
+  // M-block p (uniform); not ok past the last one
+  __device__ __forceinline__ Group find(int p) const {
+    const int lane = threadIdx.x & 63;
+    int q = p - excl;
+    const uint64_t hit = __ballot(q >= 0 && q < sum);
+    Group g{0, 0, 0, 0, hit != 0};
+    if (!g.ok) return g;
+    int e = lane * 4, r0 = o[0], Me = o[1] - o[0];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += v;
+    for (int j = 0; j < 3; ++j) {
+      const bool past = e == lane * 4 + j && q >= t[j];
+      q -= past ? t[j] : 0;
+      e += past;
+      r0 = past ? o[j + 1] : r0;
+      Me = past ? o[j + 2] - o[j + 1] : Me;
+    }
+    const int src = __builtin_ctzll(hit);
+    g.e = __builtin_amdgcn_readlane(e, src);
+    g.m = __builtin_amdgcn_readlane(q, src);
+    g.r0 = __builtin_amdgcn_readlane(r0, src);
+    g.Me = __builtin_amdgcn_readlane(Me, src);
+    return g;
   }
-  int q = p - (incl - sum);
-  const uint64_t hit = __ballot(q >= 0 && q < sum);
-  Group g{0, 0, 0, 0, hit != 0};
-  if (!g.ok) return g;
-  int e = lane * 4, r0 = o[0], Me = o[1] - o[0];
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const bool past = e == lane * 4 + j && q >= t[j];
-    q -= past ? t[j] : 0;
-    e += past;
-    r0 = past ? o[j + 1] : r0;
-    Me = past ? o[j + 2] - o[j + 1] : Me;
-  }
-  const int src = __builtin_ctzll(hit);
-  g.e = __builtin_amdgcn_readlane(e, src);
-  g.m = __builtin_amdgcn_readlane(q, src);
-  g.r0 = __builtin_amdgcn_readlane(r0, src);
-  g.Me = __builtin_amdgcn_readlane(Me, src);
-  return g;
+};
+
+// Tile of workgroup b: workgroups go round-robin over the 8 XCDs, so blocks of
+// 32 consecutive tiles (an XCD's compute units) are dealt to the XCDs in turn:
+// tiles that run together on one XCD, and share operand rows in its L2, are
+// neighbours.
+__device__ __forceinline__ int xcd_tile(int b) {
+  const int x = b & 7, i = b >> 3;
+  return ((i >> 5) * 8 + x) * 32 + (i & 31);
+}
+
+// Neighbouring tiles t of a grid of `mi` x `ni`: groups of four rows, column
+// by column.
+__device__ __forceinline__ void tile_at(int t, int mi, int ni, int& i, int& j) {
+  const int g = t / (4 * ni), rem = t - g * 4 * ni;
+  const int h = min(4, mi - g * 4);
+  j = rem / h;
+  i = g * 4 + rem - j * h;
 }
 
 // Rows to work on: all of them, or row_offset[0] .. row_offset[L]-1.

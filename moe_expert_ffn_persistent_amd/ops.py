@@ -205,7 +205,7 @@ def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stre
 
 # ---- matrix products grouped by expert ---------------------------------------
 
-def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate=False):
+def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate=False, tile=0):
     """x [rows, k], w [L, n, k], y [rows, n]; the operand that ``op`` writes is
     bf16 or fp32, the others bf16."""
     bf16, out = (torch.bfloat16,), tuple(_OUT)
@@ -221,11 +221,11 @@ def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate
     _on(x.device, ("rows", x), ("weights", w), ("rows", y), ("row_offset", row_offset))
     written = x if op == MOE_GROUPED_DGRAD else w if op == MOE_GROUPED_WGRAD else y
     return MoeGroupedParams(op, L, x.shape[0], _expected(expected_rows), n, k, ldx, ldw, ldy,
-                            _batch_stride(w, "weights", ldw), _OUT[written.dtype], int(accumulate))
+                            _batch_stride(w, "weights", ldw), _OUT[written.dtype], int(accumulate), tile)
 
 
-def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, stream):
-    p = check_grouped_inputs(op, x, w, y, row_offset, expected_rows, accumulate)
+def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, tile, stream):
+    p = check_grouped_inputs(op, x, w, y, row_offset, expected_rows, accumulate, tile)
     _need_device(x.device)
     _launch("moe_grouped_matmul", x.device, p,
             (row_offset.data_ptr(), x.data_ptr(), w.data_ptr(), y.data_ptr()), stream)
@@ -238,33 +238,34 @@ def _grouped_out(shape, ref, out_dtype, stream):
     return _empty(shape, out_dtype, ref.device, stream)
 
 
-def grouped_matmul(x, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, stream=None):
+def grouped_matmul(x, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, tile=0, stream=None):
     """``out[r] = w[e] @ x[r]`` for the rows r of every expert e (row_offset
     [L+1]): x bf16 [rows, k], w bf16 [L, n, k], out [rows, n] bf16 or fp32.
     ``expected_rows`` (default: all rows of x) is how many rows the experts
     hold together, when the buffers have room for many more: it only chooses
-    the kernel's tile."""
+    the kernel's tile, which ``tile`` (0: automatic) names outright."""
     if out is None:
         _matrix(x, "x", (torch.bfloat16,))
         _matrix(w, "w", (torch.bfloat16,), 3)
         out = _grouped_out((x.shape[0], w.shape[1]), x, out_dtype, stream)
-    _grouped(MOE_GROUPED_FORWARD, x, w, out, row_offset, expected_rows, False, stream)
+    _grouped(MOE_GROUPED_FORWARD, x, w, out, row_offset, expected_rows, False, tile, stream)
     return out
 
 
-def grouped_matmul_dgrad(dy, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, stream=None):
+def grouped_matmul_dgrad(dy, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, tile=0,
+                         stream=None):
     """Input gradient of grouped_matmul: ``out[r] = w[e].T @ dy[r]``; dy bf16
     [rows, n], out [rows, k] bf16 or fp32."""
     if out is None:
         _matrix(dy, "dy", (torch.bfloat16,))
         _matrix(w, "w", (torch.bfloat16,), 3)
         out = _grouped_out((dy.shape[0], w.shape[2]), dy, out_dtype, stream)
-    _grouped(MOE_GROUPED_DGRAD, out, w, dy, row_offset, expected_rows, False, stream)
+    _grouped(MOE_GROUPED_DGRAD, out, w, dy, row_offset, expected_rows, False, tile, stream)
     return out
 
 
 def grouped_matmul_wgrad(dy, x, row_offset, out=None, out_dtype=torch.bfloat16, accumulate=False,
-                         expected_rows=None, stream=None):
+                         expected_rows=None, tile=0, stream=None):
     """Weight gradient of grouped_matmul: ``out[e] = sum over its rows of the
     outer products dy[r] x[r]``, [L, n, k] bf16 or fp32; an expert without rows
     gets zeros. With ``accumulate`` the sums are added to ``out``."""
@@ -274,7 +275,7 @@ def grouped_matmul_wgrad(dy, x, row_offset, out=None, out_dtype=torch.bfloat16, 
         _matrix(x, "x", (torch.bfloat16,))
         _matrix(dy, "dy", (torch.bfloat16,))
         out = _grouped_out((_offsets(row_offset), dy.shape[1], x.shape[1]), x, out_dtype, stream)
-    _grouped(MOE_GROUPED_WGRAD, x, out, dy, row_offset, expected_rows, accumulate, stream)
+    _grouped(MOE_GROUPED_WGRAD, x, out, dy, row_offset, expected_rows, accumulate, tile, stream)
     return out
 
 
@@ -419,7 +420,7 @@ def quantize_fp8(x, block_rows=1, row_offset=None, out=None, scales=None, stream
     return out, scales
 
 
-def check_fp8_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None):
+def check_fp8_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None, tile=0):
     ldx = _matrix(x, "x", _CODES)
     grouped = row_offset is not None
     ldw = _matrix(w, "w", _CODES, 3 if grouped else 2)
@@ -444,23 +445,24 @@ def check_fp8_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None
             raise ValueError(f"row_offset: {L} experts, the weights have {w.shape[0]}")
         es = _batch_stride(w, "w", ldw)
     _on(x.device, ("x", x), ("x_scales", x_scales), ("w", w), ("w_scales", w_scales), ("row_offset", row_offset), ("out", y))
-    return MoeFp8Params(L, rows, _expected(expected_rows), n, k, ldx, ldxs, ldw, ldy, es, _OUT[y.dtype])
+    return MoeFp8Params(L, rows, _expected(expected_rows), n, k, ldx, ldxs, ldw, ldy, es, _OUT[y.dtype],
+                        tile)
 
 
 def fp8_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=torch.bfloat16, expected_rows=None,
-               stream=None):
+               tile=0, stream=None):
     """``out = (x * x_scales) @ (w * w_scales).T`` of e4m3 operands: x [rows, k]
     with scales [rows, ceil(k/128)], w [n, k] with scales [ceil(n/128),
     ceil(k/128)]; grouped by expert with ``row_offset``: w [L, n, k], w_scales
     [L, ...], every row times its expert's matrix. out [rows, n] bf16 or fp32.
-    ``expected_rows`` as for grouped_matmul."""
+    ``expected_rows`` and ``tile`` as for grouped_matmul."""
     if out is None:
         _matrix(x, "x", _CODES)
         if out_dtype not in _OUT:
             raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
         _need_device(x.device)
         out = _empty((x.shape[0], w.shape[-2]), out_dtype, x.device, stream)
-    p = check_fp8_inputs(x, x_scales, w, w_scales, row_offset, out, expected_rows)
+    p = check_fp8_inputs(x, x_scales, w, w_scales, row_offset, out, expected_rows, tile)
     _need_device(x.device)
     _launch("moe_fp8_matmul", x.device, p,
             (_ptr(row_offset), x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), out.data_ptr()),

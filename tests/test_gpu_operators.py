@@ -94,7 +94,7 @@ def call(op, x, w, y, off, **kw):
     return moe.grouped_matmul_wgrad(y, x, off, out=w, **kw)
 
 
-def run_grouped(op, counts, k, n, out_dtype, seed, first=0, behind=0, pad=0, lead=0, expected_rows=None):
+def run_grouped(op, counts, k, n, out_dtype, seed, first=0, behind=0, pad=0, lead=0, expected_rows=None, tile=0):
     """One grouped product with NaN in every row that no expert owns and a
     sentinel in the output, checked against 64 bits."""
     g = gen(seed)
@@ -113,7 +113,7 @@ def run_grouped(op, counts, k, n, out_dtype, seed, first=0, behind=0, pad=0, lea
         w = torch.full((L, n, k), 7.0, dtype=out_dtype)
     dx, dw, dy = strided(x, pad, lead), strided(w, pad, lead), strided(y, pad, lead)
     say(f"op={op} counts={counts if L < 9 else L} k={k} n={n} out={out_dtype} first={first} behind={behind} pad={pad} lead={lead}")
-    got = call(op, dx, dw, dy, up(off), expected_rows=expected_rows)
+    got = call(op, dx, dw, dy, up(off), expected_rows=expected_rows, tile=tile)
     torch.cuda.synchronize()
     if op == WGRAD:
         assert_close(got, ref, out_dtype, mag, terms, f"wgrad {counts}")
@@ -162,6 +162,15 @@ def test_grouped_strides_and_alignment(op, pad, lead):
 def test_grouped_tile_choice_changes_no_result(op, expected):
     # expected_rows chooses the kernel; any choice is right for any counts
     run_grouped(op, [0, 33, 290, 5], 264, 328, BF, seed=17, expected_rows=expected, behind=1)
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("tile", [1, 2, 3, 4])
+@pytest.mark.parametrize("op", [FWD, DGRAD, WGRAD], ids=["forward", "dgrad", "wgrad"])
+@pytest.mark.parametrize("counts,k,n", [([0, 33, 290, 1], 264, 328), ([70, 257], 64, 8), ([3, 0, 200], 8, 64), ([64, 128], 512, 256),
+                                        ([191, 129], 1032, 136)])
+def test_grouped_every_tile(counts, k, n, op, tile, out_dtype):
+    run_grouped(op, counts, k, n, out_dtype, seed=k + n, first=2, behind=4, pad=8, tile=tile)
 
 
 @pytest.mark.parametrize("op", [FWD, DGRAD, WGRAD], ids=["forward", "dgrad", "wgrad"])

@@ -240,7 +240,7 @@ def _call(name, params, *ptrs):
 
 def _grouped(**kw):
     base = dict(op=0, num_experts=2, rows=4, expected_rows=0, n=8, k=16, ld_x=16, ld_w=16, ld_y=8, expert_stride_w=128,
-                out_dtype=_lib.MOE_Y_BF16, accumulate=0)
+                out_dtype=_lib.MOE_Y_BF16, accumulate=0, tile=0)
     base.update(kw)
     return _lib.MoeGroupedParams(*base.values())
 
@@ -248,7 +248,7 @@ def _grouped(**kw):
 @pytest.mark.parametrize("kw", [dict(op=3), dict(op=-1), dict(num_experts=0), dict(num_experts=257), dict(rows=-1),
                                 dict(rows=(1 << 28) + 1), dict(n=0), dict(k=0), dict(k=(1 << 20) + 1), dict(ld_x=15),
                                 dict(ld_w=15), dict(ld_y=7), dict(expert_stride_w=127), dict(out_dtype=2),
-                                dict(accumulate=1), dict(expected_rows=-1)])
+                                dict(accumulate=1), dict(expected_rows=-1), dict(tile=-1)])
 def test_c_grouped_refuses(kw):
     assert _call("moe_grouped_matmul", _grouped(**kw), 16, 16, 16, 16) == _lib.MOE_ERR_INVALID_ARG
 
@@ -257,6 +257,9 @@ def test_c_grouped_refuses_missing_and_misaligned_pointers():
     for ptrs in ((None, 16, 16, 16), (16, None, 16, 16), (16, 16, None, 16), (16, 16, 16, None), (16, 17, 16, 16)):
         assert _call("moe_grouped_matmul", _grouped(), *ptrs) == _lib.MOE_ERR_INVALID_ARG
     assert _call("moe_grouped_matmul", _grouped(out_dtype=_lib.MOE_Y_FP32), 16, 16, 16, 18) == _lib.MOE_ERR_INVALID_ARG
+    # a tile id that does not exist, or does not take these operands
+    assert _call("moe_grouped_matmul", _grouped(tile=99), 16, 16, 16, 16) == _lib.MOE_ERR_UNSUPPORTED
+    assert _call("moe_grouped_matmul", _grouped(tile=1), 16, 18, 16, 16) == _lib.MOE_ERR_UNSUPPORTED
     # nothing to do: no rows
     assert _call("moe_grouped_matmul", _grouped(rows=0), None, None, None, None) == _lib.MOE_OK
     assert _call("moe_grouped_matmul", _grouped(rows=0, op=2), None, None, None, None) == _lib.MOE_ERR_INVALID_ARG
@@ -302,15 +305,15 @@ def test_c_quantize_refuses(kw):
 
 
 @pytest.mark.parametrize("kw", [dict(num_experts=0), dict(rows=-1), dict(n=0), dict(k=0), dict(ld_x=255), dict(ld_xs=1),
-                                dict(ld_w=255), dict(ld_y=7), dict(expert_stride_w=2047), dict(out_dtype=9)])
+                                dict(ld_w=255), dict(ld_y=7), dict(expert_stride_w=2047), dict(out_dtype=9), dict(tile=-1)])
 def test_c_fp8_refuses(kw):
     base = dict(num_experts=2, rows=4, expected_rows=0, n=8, k=256, ld_x=256, ld_xs=2, ld_w=256, ld_y=8,
-                expert_stride_w=2048, out_dtype=1)
+                expert_stride_w=2048, out_dtype=1, tile=0)
     base.update(kw)
     assert _call("moe_fp8_matmul", _lib.MoeFp8Params(*base.values()), 16, 16, 16, 16, 16, 16) == _lib.MOE_ERR_INVALID_ARG
 
 
 def test_c_fp8_dense_has_one_matrix():
     base = dict(num_experts=2, rows=4, expected_rows=0, n=8, k=256, ld_x=256, ld_xs=2, ld_w=256, ld_y=8,
-                expert_stride_w=2048, out_dtype=1)
+                expert_stride_w=2048, out_dtype=1, tile=0)
     assert _call("moe_fp8_matmul", _lib.MoeFp8Params(*base.values()), None, 16, 16, 16, 16, 16) == _lib.MOE_ERR_INVALID_ARG

@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmoe_ffn.so")
 ARCH = "gfx950"
 
 SOURCES = ["layout.hip", "ffn_bf16.hip", "ffn_fp8.hip", "ffn_w4a8.hip", "combine.hip", "burst.hip",
-           "mfma_probe.hip", "rows.hip", "swiglu.hip", "gemm_any.hip", "gemm_bf16.hip",
+           "mfma_probe.hip", "rows.hip", "swiglu.hip", "gemm_any.hip", "gemm_bf16.hip", "gemm_fp8.hip",
            "api.cpp", "ops_api.cpp", "planner.cpp"]
 
 COMMON = [

@@ -37,18 +37,25 @@ __device__ __forceinline__ void dma16s(uint32_t voff, const char* base, uint32_t
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
 }
 
-template <int TM_, int TN_, int WT_, int WF_, int NS_, int SP_, int OCC_>
+// KW > 1: the workgroup's KW wavefronts share one small tile and split c: each
+// takes every KW-th stage through a ring of its own, without barriers, and
+// their sums are joined in LDS in wavefront order. For calls with few tiles,
+// where one wavefront's chain of stages would leave the memory idle.
+template <int TM_, int TN_, int WT_, int WF_, int NS_, int SP_, int OCC_, int KW_ = 1>
 struct CfgG {
   static constexpr int TM = TM_, TN = TN_, WT = WT_, WF = WF_, NS = NS_, SP = SP_;
   static constexpr int OCC = OCC_;                 // workgroups per CU that LDS and registers are cut for
-  static constexpr int NW = WT * WF, THREADS = 64 * NW;
+  static constexpr int KW = KW_;
+  static constexpr int NW = WT * WF, THREADS = 64 * NW * KW;
   static constexpr int TT = TM / WT, FT = TN / WF; // rows and columns of a wavefront
   static constexpr int TB = TT / 32, FB = FT / 32;
   static constexpr int T_BYTES = TM * kBK * 2, F_BYTES = TN * kBK * 2;
   static constexpr int STAGE = T_BYTES + F_BYTES;
   static constexpr int NIT = T_BYTES / 1024 / NW, NIF = F_BYTES / 1024 / NW, NI = NIT + NIF;
   static constexpr int EPI = NW * 32 * FT * 4;     // epilogue staging: 32 rows a wavefront, fp32
-  static constexpr int LDS = NS * STAGE > EPI ? NS * STAGE : EPI;
+  static constexpr int RING = NS * STAGE > EPI ? NS * STAGE : EPI;
+  static constexpr int LDS = KW * RING;
+  static_assert(KW == 1 || (NW == 1 && TM == 32), "split wavefronts hold the whole tile each");
   static constexpr int issue_slot(int i, int nm) { return i * nm * SP / (NI * 8); }
   static_assert(T_BYTES % (1024 * NW) == 0 && F_BYTES % (1024 * NW) == 0, "copies split evenly over the wavefronts");
   static_assert(NS >= 2 && NI * (NS - 1) <= 63, "vmcnt range");
@@ -58,6 +65,7 @@ struct CfgG {
 // One operand: TX rows (i or j) by 64 c a stage.
 template <bool TR, int TX, int NW>
 struct Operand {
+  __device__ __forceinline__ static int wave_of() { return NW == 1 ? 0 : uni((int)(threadIdx.x >> 6)); }
   static constexpr int NI = TX * kBK * 2 / 1024 / NW;   // 1 KiB copies of a wavefront per stage
   static constexpr int RB = TR ? TX * 2 : kBK * 2;      // bytes of an LDS row
   static constexpr int RPI = 1024 / RB;                 // LDS rows per copy
@@ -81,7 +89,7 @@ struct Operand {
   // p: element (row 0, c 0) of the tile's matrix; x0: the tile's first row (i
   // or j) of `nx`; ld: elements between rows of memory
   __device__ __forceinline__ void setup(const void* p, long long ld, int x0, int nx) {
-    const int wave = uni((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+    const int wave = wave_of(), lane = threadIdx.x & 63;
     const char* b = static_cast<const char*>(p);
     if constexpr (!TR) {
       base = b + (long long)x0 * ld * 2;
@@ -104,14 +112,14 @@ struct Operand {
   }
 
   __device__ __forceinline__ void issue(int i, int kt, uint32_t slot) const {
-    const uint32_t dst = uni(slot + ((threadIdx.x >> 6) + NW * i) * 1024);
+    const uint32_t dst = uni(slot + (wave_of() + NW * i) * 1024);
     if constexpr (!TR) dma16s(voff[i], base + kt * step, dst);
     else dma16s(voff[0], base + kt * step + i * istep, dst);
   }
 
   // The last stage when it holds only `left` < 64 c: lanes past the end write zeros.
   __device__ __forceinline__ void issue_tail(int kt, int left, char* slot) const {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = wave_of(), lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = (wave + NW * i) * RPI + (TR ? lane * 16 / RB : lane / 8);
@@ -191,45 +199,106 @@ struct TileG {
     }
   }
 
-  // All of c: `nc` of them.
-  __device__ __forceinline__ void mainloop(char* lds, int nc, int wf, int wt) {
+  // All of c, `nc` of them (with KW > 1, the stages kw, kw + KW, ... of them).
+  __device__ __forceinline__ void mainloop(char* lds, int nc, int wf, int wt, int kw) {
 #pragma unroll
     for (int fb = 0; fb < C::FB; ++fb)
 #pragma unroll
       for (int tb = 0; tb < C::TB; ++tb) acc[fb][tb] = f32x16{};
     const uint32_t ring = (uint32_t)(uintptr_t)lds;
-    const int left = nc % kBK, full = nc / kBK, nk = full + (left != 0);
-    auto tail = [&](int kt) {
-      char* slot = lds + (kt % C::NS) * C::STAGE;
-      f.issue_tail(kt, left, slot);
-      t.issue_tail(kt, left, slot + C::F_BYTES);
+    const int all = nc / kBK;                                            // whole stages
+    const int left = all % C::KW == kw ? nc % kBK : 0;                   // c of this wavefront's short last stage
+    const int full = C::KW == 1 ? all : (all - kw + C::KW - 1) / C::KW;  // its whole stages (all >= 0, kw < KW)
+    const int nk = full + (left != 0);
+    auto at = [&](int s) { return C::KW == 1 ? s : kw + C::KW * s; };
+    auto tail = [&](int s) {
+      char* slot = lds + (s % C::NS) * C::STAGE;
+      f.issue_tail(at(s), left, slot);
+      t.issue_tail(at(s), left, slot + C::F_BYTES);
     };
 #pragma unroll
     for (int s = 0; s < C::NS - 1; ++s) {
       if (s < full) {
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) issue(i, s, ring + s * C::STAGE);
+        for (int i = 0; i < C::NI; ++i) issue(i, at(s), ring + s * C::STAGE);
       } else if (s < nk) {
         tail(s);
       }
     }
     int slot = 0;
     const int nmain = full - (C::NS - 1);   // stages that copy a later whole stage
-    for (int kt = 0; kt < nmain; ++kt) {
+    for (int s = 0; s < nmain; ++s) {
       vm_wait<C::NI * (C::NS - 2)>();
-      lds_barrier();
+      if constexpr (C::KW == 1) lds_barrier();
       const int nslot = slot == 0 ? C::NS - 1 : slot - 1;
-      compute<true>(lds + slot * C::STAGE, wf, wt, kt + C::NS - 1, ring + nslot * C::STAGE);
+      compute<true>(lds + slot * C::STAGE, wf, wt, at(s + C::NS - 1), ring + nslot * C::STAGE);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
-    for (int kt = max(nmain, 0); kt < nk; ++kt) {
-      // a tail stage's copies are fewer (and zeros written) in some lanes: wait for all
+    for (int s = max(nmain, 0); s < nk; ++s) {
+      // a short stage's copies are fewer, and zeros written, in some lanes: wait for all
       if (left) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      else vm_wait_ahead<C::NI, C::NS - 2>(nk - 1 - kt);
-      lds_barrier();
-      if (left && kt + C::NS - 1 == full) tail(full);
+      else vm_wait_ahead<C::NI, C::NS - 2>(nk - 1 - s);
+      if constexpr (C::KW == 1) lds_barrier();
+      if (left && s + C::NS - 1 == full) tail(full);
       compute<false>(lds + slot * C::STAGE, wf, wt, 0, 0);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
+    }
+  }
+
+  // KW > 1: the wavefronts' sums to LDS, joined in their order and written out.
+  __device__ __forceinline__ void store_split(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int kw,
+                                              bool bf16, bool add) {
+    constexpr int ROWB = C::TN * 4, NCH = ROWB / 16;
+    const int lane = threadIdx.x & 63;
+    char* mine = lds + kw * C::RING;   // this wavefront's ring: it alone used it
+#pragma unroll
+    for (int fb = 0; fb < C::FB; ++fb)
+#pragma unroll
+      for (int g4 = 0; g4 < 4; ++g4) {
+        const f32x16& v = acc[fb][0];
+        *reinterpret_cast<float4*>(mine + stage_off<ROWB>(lane & 31, (fb * 32 + (lane >> 5) * 4 + g4 * 8) * 4)) =
+            float4{v[g4 * 4], v[g4 * 4 + 1], v[g4 * 4 + 2], v[g4 * 4 + 3]};
+      }
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < 32 * NCH; idx += C::THREADS) {
+      const int r = idx / NCH, c = idx - r * NCH, i = i0 + r, col = j0 + c * 4;
+      if (i >= ni || col >= nj) continue;
+      float4 s = *reinterpret_cast<const float4*>(lds + stage_off<ROWB>(r, c * 16));
+#pragma unroll
+      for (int w = 1; w < C::KW; ++w) {
+        const float4 o = *reinterpret_cast<const float4*>(lds + w * C::RING + stage_off<ROWB>(r, c * 16));
+        s = float4{s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w};
+      }
+      const long long at = (long long)i * ld + col;
+      if (bf16) {
+        uint2* p = reinterpret_cast<uint2*>(static_cast<__bf16*>(out) + at);
+        if (add) {
+          const uint2 o = *p;
+          s = float4{s.x + bf16_lo(o.x), s.y + bf16_hi(o.x), s.z + bf16_lo(o.y), s.w + bf16_hi(o.y)};
+        }
+        *p = uint2{pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)};
+      } else {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+        if (add) {
+          const float4 o = *p;
+          s = float4{s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w};
+        }
+        *p = s;
+      }
+    }
+  }
+
+  // Either way out
+  __device__ __forceinline__ void write(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int wf, int wt,
+                                        int kw, bool bf16, bool add) {
+    if constexpr (C::KW > 1) {
+      store_split(lds, out, ld, i0, ni, j0, nj, kw, bf16, add);
+    } else if (bf16) {
+      if (add) store<true, true>(lds, out, ld, i0, ni, j0, nj, wf, wt);
+      else store<true, false>(lds, out, ld, i0, ni, j0, nj, wf, wt);
+    } else {
+      if (add) store<false, true>(lds, out, ld, i0, ni, j0, nj, wf, wt);
+      else store<false, false>(lds, out, ld, i0, ni, j0, nj, wf, wt);
     }
   }
 
@@ -292,10 +361,12 @@ struct TileG {
 };
 
 template <class C, int OP>
-__global__ void __launch_bounds__(C::THREADS, C::NW / 4 * C::OCC > 0 ? C::NW / 4 * C::OCC : 1) moe_gemm_bf16(const GemmArgs a) {
+__global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_gemm_bf16(const GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   constexpr bool WG = OP == MOE_GROUPED_WGRAD;
-  const int wave = uni((int)(threadIdx.x >> 6)), wf = wave % C::WF, wt = wave / C::WF;
+  const int wave = uni((int)(threadIdx.x >> 6)), kw = C::KW == 1 ? 0 : wave;
+  const int wf = C::KW == 1 ? wave % C::WF : 0, wt = C::KW == 1 ? wave / C::WF : 0;
+  char* const ring = lds + kw * C::RING;
   const int tile = xcd_tile(blockIdx.x);
   TileG<C, WG, OP != MOE_GROUPED_FORWARD> g;
   const __bf16* x = static_cast<const __bf16*>(a.x);
@@ -312,16 +383,9 @@ __global__ void __launch_bounds__(C::THREADS, C::NW / 4 * C::OCC > 0 ? C::NW / 4
     if (Me == 0 && a.accumulate) return;
     g.t.setup(y + (long long)r0 * a.ld_y, a.ld_y, i * C::TM, a.n);
     g.f.setup(x + (long long)r0 * a.ld_x, a.ld_x, j * C::TN, a.k);
-    g.mainloop(lds, Me, wf, wt);
+    g.mainloop(ring, Me, wf, wt, kw);
     char* out = static_cast<char*>(a.w) + (long long)e * a.es_w * (a.out_bf16 ? 2 : 4);
-    const int i0 = i * C::TM, j0 = j * C::TN;
-    if (a.out_bf16) {
-      if (a.accumulate) g.template store<true, true>(lds, out, a.ld_w, i0, a.n, j0, a.k, wf, wt);
-      else g.template store<true, false>(lds, out, a.ld_w, i0, a.n, j0, a.k, wf, wt);
-    } else {
-      if (a.accumulate) g.template store<false, true>(lds, out, a.ld_w, i0, a.n, j0, a.k, wf, wt);
-      else g.template store<false, false>(lds, out, a.ld_w, i0, a.n, j0, a.k, wf, wt);
-    }
+    g.write(lds, out, a.ld_w, i * C::TM, a.n, j * C::TN, a.k, wf, wt, kw, a.out_bf16, a.accumulate);
   } else {
     constexpr bool FWD = OP == MOE_GROUPED_FORWARD;
     const int nj = FWD ? a.n : a.k, nc = FWD ? a.k : a.n, ni = (nj + C::TN - 1) / C::TN;
@@ -333,10 +397,9 @@ __global__ void __launch_bounds__(C::THREADS, C::NW / 4 * C::OCC > 0 ? C::NW / 4
     const long long ldt = FWD ? a.ld_x : a.ld_y, ldo = FWD ? a.ld_y : a.ld_x;
     g.t.setup((FWD ? x : y) + (long long)gr.r0 * ldt, ldt, gr.m * C::TM, gr.Me);
     g.f.setup(w + (long long)gr.e * a.es_w, a.ld_w, j * C::TN, nj);
-    g.mainloop(lds, nc, wf, wt);
+    g.mainloop(ring, nc, wf, wt, kw);
     char* out = static_cast<char*>(FWD ? a.y : a.x) + (long long)gr.r0 * ldo * (a.out_bf16 ? 2 : 4);
-    if (a.out_bf16) g.template store<true, false>(lds, out, ldo, gr.m * C::TM, gr.Me, j * C::TN, nj, wf, wt);
-    else g.template store<false, false>(lds, out, ldo, gr.m * C::TM, gr.Me, j * C::TN, nj, wf, wt);
+    g.write(lds, out, ldo, gr.m * C::TM, gr.Me, j * C::TN, nj, wf, wt, kw, a.out_bf16, false);
   }
 }
 
@@ -345,6 +408,8 @@ using Large = CfgG<256, 256, 2, 4, 2, 2, 1>;
 using Medium = CfgG<128, 256, 2, 4, 3, 4, 1>;
 using Square = CfgG<128, 128, 2, 2, 2, 4, 2>;
 using Small = CfgG<64, 128, 1, 4, 3, 4, 2>;
+using Split = CfgG<32, 32, 1, 1, 2, 4, 1, 8>;
+using Split64 = CfgG<32, 64, 1, 1, 3, 4, 1, 4>;
 
 template <class C, int OP>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
@@ -364,6 +429,8 @@ hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
     case 2: return launch<Medium, OP>(a, s);
     case 3: return launch<Square, OP>(a, s);
     case 4: return launch<Small, OP>(a, s);
+    case 5: return launch<Split, OP>(a, s);
+    case 6: return launch<Split64, OP>(a, s);
   }
   return hipErrorInvalidValue;
 }

@@ -1,0 +1,348 @@
+// Block-scaled e4m3 matrix products, dense or grouped by expert, for 16-byte
+// aligned operands:
+//
+//   y(r, n) = sum over 128-wide K blocks b of xs(r, b) ws(n/128, b) P_b(r, n),
+//   P_b(r, n) = sum over k in b of x(r, k) w(n, k)
+//
+// One v_mfma_scale_f32_16x16x128_f8f6f4 (unit scales) is one P_b of a 16 x 16
+// block: the fp32 scales are no powers of two and cannot ride in the MFMA, so
+// the VALU adds each P_b into the accumulator times its scales, two MFMAs
+// behind the matrix core (four FMAs a lane under a 32-cycle MFMA). Weights are
+// the A operand and rows the B operand: a lane holds one row and runs of four
+// consecutive n, its row scale is one register and its weight scale is uniform.
+//
+// The e4m3 MFMAs (this one and the unscaled 16x16x32 alike, measured) add eight
+// consecutive products after dropping each one's bits below 2^-13 of the
+// largest's power of two: about 1.5e-5 of a result, against the 2^-4 half step
+// of the operands. Products through bf16 MFMAs would keep those bits at half
+// the rate and with a conversion of every operand, and were not taken.
+//
+// A stage is one K block (128 bytes a row): an NS-deep LDS ring filled by
+// direct-to-LDS copies between the MFMAs of an earlier stage; the stage's row
+// scales come along as four-byte copies. The weight scales of 64 blocks sit in
+// one register of a wavefront, a lane each. A ragged last block is zeros in
+// LDS.
+#include "internal.hpp"
+#include "ops_common.hpp"
+
+namespace moe {
+namespace {
+
+// 16 (or 4) bytes a lane from base + voff (bytes) to LDS m0 + 16 (4) * lane
+__device__ __forceinline__ void dma16s(uint32_t voff, const char* base, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4s(uint32_t voff, const char* base, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
+}
+
+// KW > 1: KW wavefronts split K (see the bf16 kernel): a ring each, sums joined in LDS.
+template <int TM_, int TN_, int WT_, int WF_, int NS_, int SP_, int OCC_, int KW_ = 1>
+struct CfgQ {
+  static constexpr int TM = TM_, TN = TN_, WT = WT_, WF = WF_, NS = NS_, SP = SP_, OCC = OCC_;
+  static constexpr int KW = KW_, NW = WT * WF, THREADS = 64 * NW * KW;
+  static constexpr int TT = TM / WT, FT = TN / WF;
+  static constexpr int TB = TT / 16, FB = FT / 16, NB = TB * FB;   // 16 x 16 blocks of a wavefront
+  static constexpr int NIT = TM * 128 / 1024 / NW, NIF = TN * 128 / 1024 / NW;
+  static constexpr int NI = NIT + NIF + 1;               // with the row-scale copy
+  static constexpr int F_BYTES = TN * 128, T_BYTES = TM * 128, S_BYTES = NW * 256;
+  static constexpr int STAGE = F_BYTES + T_BYTES + S_BYTES;
+  static constexpr int EPI = NW * 32 * FT * 4;
+  static constexpr int RING = NS * STAGE > EPI ? NS * STAGE : EPI;
+  static constexpr int LDS = KW * RING;
+  static_assert(KW == 1 || (NW == 1 && TM == 32), "split wavefronts hold the whole tile each");
+  static constexpr int issue_slot(int i) { return i * NB * SP / (NI * 8); }
+  static constexpr int NP = 4;                           // products in flight
+  static_assert(FT <= 128 && 128 % FT == 0, "a wavefront's columns lie in one block of weight scales");
+  static_assert(NB % NP == 0 && TB % 2 == 0 && FB >= 2, "blocks of a wavefront");
+  static_assert(TM <= 64 * NW, "row-scale copies cover the tile");
+  static_assert((TM * 128) % (1024 * NW) == 0 && (TN * 128) % (1024 * NW) == 0, "copies split evenly");
+  static_assert(NS >= 2 && NI * (NS - 1) <= 63, "vmcnt range");
+  static_assert(LDS * OCC <= 160 * 1024, "LDS");
+};
+
+// Physical 16-byte chunk of logical chunk c in row r of a stage, and back: the
+// fragment reads take rows r16 at chunks 2g and 2g+1 (g = lane / 16), and this
+// bijection spreads both over all banks (measured without conflicts).
+__device__ __forceinline__ int chunk_at(int r, int c) { return c ^ ((r >> 1) & 7) ^ ((c & 2) << 1); }
+__device__ __forceinline__ int chunk_in(int r, int p) {
+  const int q = p ^ ((r >> 1) & 7);
+  return q ^ ((q & 2) << 1);
+}
+
+template <class C>
+struct TileQ {
+  const char *fbase, *tbase, *sbase;
+  uint32_t fv[C::NIF], tv[C::NIT], sv;
+  f32x4 acc[C::FB][C::TB];
+  f32x4 part[C::NP];
+  float s_tail[2];
+
+  __device__ __forceinline__ static int wave_of() { return C::NW == 1 ? 0 : uni((int)(threadIdx.x >> 6)); }
+
+  template <int NI>
+  __device__ __forceinline__ static void offsets(uint32_t (&v)[NI], long long ld, int last) {
+    const int wave = wave_of(), lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = (wave + C::NW * i) * 8 + lane / 8;
+      v[i] = (uint32_t)min(r, last) * (uint32_t)ld + chunk_in(r, lane & 7) * 16;
+    }
+  }
+
+  __device__ __forceinline__ void issue(int i, int kt, uint32_t slot) const {
+    const uint32_t wave = wave_of();
+    slot = uni(slot);
+    if (i < C::NIF) dma16s(fv[i], fbase + kt * 128ll, slot + (wave + C::NW * i) * 1024);
+    else if (i < C::NIF + C::NIT) dma16s(tv[i - C::NIF], tbase + kt * 128ll, slot + C::F_BYTES + (wave + C::NW * (i - C::NIF)) * 1024);
+    else dma4s(sv, sbase + kt * 4ll, slot + C::F_BYTES + C::T_BYTES + wave * 256);
+  }
+
+  // the last block when it holds only `left` < 128 k: lanes past it write zeros
+  __device__ __forceinline__ void issue_tail(int kt, int left, char* slot) const {
+    const int wave = wave_of(), lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < C::NIF + C::NIT; ++i) {
+      const int j = i < C::NIF ? i : i - C::NIF;
+      const int r = (wave + C::NW * j) * 8 + lane / 8;
+      const bool in = chunk_in(r, lane & 7) * 16 < left;
+      if (in) issue(i, kt, (uint32_t)(uintptr_t)slot);
+      else *reinterpret_cast<uint4*>(slot + (i < C::NIF ? 0 : C::F_BYTES) + (wave + C::NW * j) * 1024 + lane * 16) = uint4{0, 0, 0, 0};
+    }
+    issue(C::NI - 1, kt, (uint32_t)(uintptr_t)slot);
+  }
+
+  __device__ __forceinline__ static i32x8 frag(const char* stage, int r, int c) {
+    const char* row = stage + r * 128;
+    const uint4 lo = *reinterpret_cast<const uint4*>(row + (chunk_at(r, c) << 4));
+    const uint4 hi = *reinterpret_cast<const uint4*>(row + (chunk_at(r, c + 1) << 4));
+    return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  }
+
+  // One K block; sw: its weight scale. The products of the stage's last two
+  // blocks are added during the first two MFMAs of the next one.
+  template <bool COPY>
+  __device__ __forceinline__ void compute(const char* stage, int wf, int wt, bool first, float sw, int kt_next, uint32_t slot) {
+    const int lane = threadIdx.x & 63, r16 = lane & 15, c0 = 2 * (lane >> 4);
+    const char* ts = stage + C::F_BYTES;
+    const float* sx = reinterpret_cast<const float*>(ts + C::T_BYTES) + wt * C::TT + r16;
+    i32x8 af[C::FB], bf[2];
+    float st[2];
+    bf[0] = frag(ts, wt * C::TT + r16, c0);
+    af[0] = frag(stage, wf * C::FT + r16, c0);
+    st[0] = sx[0] * sw;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < C::NB; ++b) {
+      const int j = b / C::FB, i = b % C::FB;
+      if (b + 1 < C::FB) af[b + 1] = frag(stage, wf * C::FT + (b + 1) * 16 + r16, c0);
+      if (i == 0 && j + 1 < C::TB) bf[(j + 1) & 1] = frag(ts, wt * C::TT + (j + 1) * 16 + r16, c0);
+      part[b % C::NP] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j & 1], f32x4{}, 0, 0, 0, 127, 0, 127);
+      const int q = b - 2;
+      if (q >= 0) {
+        const float s = st[(q / C::FB) & 1];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[q % C::FB][q / C::FB][v] += part[q % C::NP][v] * s;
+      } else if (!first) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[C::FB + q][C::TB - 1][v] += part[(q + C::NP) % C::NP][v] * s_tail[q + 2];
+      }
+      // the next rows' scale once the last use of the one it replaces is past
+      if (i == (C::FB > 2 ? 2 : 1) && j + 1 < C::TB) st[(j + 1) & 1] = sx[(j + 1) * 16] * sw;
+      if constexpr (COPY) {
+#pragma unroll
+        for (int k = 0; k < C::NI; ++k)
+          if (C::issue_slot(k) == b) issue(k, kt_next, slot);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    s_tail[0] = s_tail[1] = st[(C::TB - 1) & 1];
+  }
+
+  // All of K (with KW > 1, blocks kw, kw + KW, ...)
+  __device__ __forceinline__ void mainloop(char* lds, int K, const float* ws, int wf, int wt, int kw) {
+#pragma unroll
+    for (int i = 0; i < C::FB; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TB; ++j) acc[i][j] = f32x4{};
+    const int lane = threadIdx.x & 63;
+    const uint32_t ring = (uint32_t)(uintptr_t)lds;
+    const int all = K / 128, kb = (K + 127) / 128;
+    const int left = all % C::KW == kw ? K % 128 : 0;
+    const int full = C::KW == 1 ? all : (all - kw + C::KW - 1) / C::KW;
+    const int nk = full + (left != 0);
+    auto at = [&](int s) { return C::KW == 1 ? s : kw + C::KW * s; };
+#pragma unroll
+    for (int s = 0; s < C::NS - 1; ++s) {
+      if (s < full) {
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i) issue(i, at(s), ring + s * C::STAGE);
+      } else if (s < nk) {
+        issue_tail(at(s), left, lds + s * C::STAGE);
+      }
+    }
+    float wsv = 0.f;
+    auto scale = [&](int s) {
+      if ((s & 63) == 0) wsv = ws[min(at(s + lane), kb - 1)];
+      return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv), s & 63));
+    };
+    int slot = 0;
+    const int nmain = full - (C::NS - 1);
+    for (int s = 0; s < nmain; ++s) {
+      const float sw = scale(s);
+      vm_wait<C::NI * (C::NS - 2)>();
+      if constexpr (C::KW == 1) lds_barrier();
+      const int nslot = slot == 0 ? C::NS - 1 : slot - 1;
+      compute<true>(lds + slot * C::STAGE, wf, wt, s == 0, sw, at(s + C::NS - 1), ring + nslot * C::STAGE);
+      slot = slot + 1 == C::NS ? 0 : slot + 1;
+    }
+    for (int s = max(nmain, 0); s < nk; ++s) {
+      const float sw = scale(s);
+      if (left) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else vm_wait_ahead<C::NI, C::NS - 2>(nk - 1 - s);
+      if constexpr (C::KW == 1) lds_barrier();
+      if (left && s + C::NS - 1 == full) issue_tail(at(full), left, lds + (full % C::NS) * C::STAGE);
+      compute<false>(lds + slot * C::STAGE, wf, wt, s == 0, sw, 0, 0);
+      slot = slot + 1 == C::NS ? 0 : slot + 1;
+    }
+    if (nk > 0) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        acc[C::FB - 2][C::TB - 1][v] += part[(C::NB - 2) % C::NP][v] * s_tail[0];
+        acc[C::FB - 1][C::TB - 1][v] += part[(C::NB - 1) % C::NP][v] * s_tail[1];
+      }
+    }
+  }
+
+  // KW > 1: the wavefronts' sums to LDS, joined in their order and written out.
+  __device__ __forceinline__ void store_split(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int kw,
+                                              bool bf16) {
+    constexpr int ROWB = C::TN * 4, NCH = ROWB / 16;
+    const int lane = threadIdx.x & 63;
+    char* mine = lds + kw * C::RING;
+#pragma unroll
+    for (int i = 0; i < C::FB; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TB; ++j)
+        *reinterpret_cast<float4*>(mine + stage_off<ROWB>(j * 16 + (lane & 15), (i * 16 + 4 * (lane >> 4)) * 4)) =
+            float4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < 32 * NCH; idx += C::THREADS) {
+      const int r = idx / NCH, c = idx - r * NCH, i = i0 + r, col = j0 + c * 4;
+      if (i >= ni || col >= nj) continue;
+      float4 s = *reinterpret_cast<const float4*>(lds + stage_off<ROWB>(r, c * 16));
+#pragma unroll
+      for (int w = 1; w < C::KW; ++w) {
+        const float4 o = *reinterpret_cast<const float4*>(lds + w * C::RING + stage_off<ROWB>(r, c * 16));
+        s = float4{s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w};
+      }
+      const long long p = (long long)i * ld + col;
+      if (bf16) *reinterpret_cast<uint2*>(static_cast<__bf16*>(out) + p) = uint2{pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)};
+      else *reinterpret_cast<float4*>(static_cast<float*>(out) + p) = s;
+    }
+  }
+
+  // Rows i0 .. of ni, columns j0 .. of nj (see the bf16 kernel's store)
+  template <bool BF16>
+  __device__ __forceinline__ void store(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int wf, int wt) {
+    constexpr int EB = BF16 ? 2 : 4, ROWB = C::FT * EB, NCH = ROWB / 16, RPP = 64 / NCH;
+    const int tid = opaque(threadIdx.x), lane = tid & 63;
+    char* mine = lds + (tid >> 6) * (32 * C::FT * 4);
+    lds_barrier();
+#pragma unroll
+    for (int jp = 0; jp < C::TB / 2; ++jp) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < C::FB; ++i) {
+          const f32x4& v = acc[i][2 * jp + h];
+          char* p = mine + stage_off<ROWB>(h * 16 + (lane & 15), (i * 16 + 4 * (lane >> 4)) * EB);
+          if constexpr (BF16) *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+          else *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const int c = lane % NCH, col = j0 + wf * C::FT + c * (16 / EB);
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += RPP) {
+        const int r = r0 + lane / NCH, i = i0 + wt * C::TT + jp * 32 + r;
+        if (i < ni && col < nj)
+          *reinterpret_cast<uint4*>(static_cast<char*>(out) + ((long long)i * ld + col) * EB) =
+              *reinterpret_cast<const uint4*>(mine + stage_off<ROWB>(r, c * 16));
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  }
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_gemm_fp8(const GemmArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  const int wave = uni((int)(threadIdx.x >> 6)), kw = C::KW == 1 ? 0 : wave, lane = threadIdx.x & 63;
+  const int wf = C::KW == 1 ? wave % C::WF : 0, wt = C::KW == 1 ? wave / C::WF : 0;
+  const int tile = xcd_tile(blockIdx.x);
+  const int ni = (a.n + C::TN - 1) / C::TN, kb = (a.k + 127) / 128, nb = (a.n + 127) / 128;
+  Group gr;
+  int j;
+  if (a.row_offset) {
+    const GroupScan<C::TM> scan(a.row_offset, a.L, a.rows);
+    if (tile >= scan.total * ni) return;
+    int p;
+    tile_at(tile, scan.total, ni, p, j);
+    gr = scan.find(p);
+  } else {
+    const int mi = (a.rows + C::TM - 1) / C::TM;
+    if (tile >= mi * ni) return;
+    gr = Group{0, 0, 0, a.rows, true};
+    tile_at(tile, mi, ni, gr.m, j);
+  }
+  TileQ<C> g;
+  const int i0 = gr.m * C::TM, j0 = j * C::TN;
+  g.fbase = static_cast<const char*>(a.w) + (long long)gr.e * a.es_w + (long long)j0 * a.ld_w;
+  g.tbase = static_cast<const char*>(a.x) + (long long)(gr.r0 + i0) * a.ld_x;
+  g.sbase = reinterpret_cast<const char*>(a.xs + (long long)(gr.r0 + i0) * a.ld_xs);
+  g.offsets(g.fv, a.ld_w, a.n - 1 - j0);
+  g.offsets(g.tv, a.ld_x, gr.Me - 1 - i0);
+  g.sv = (uint32_t)min((g.wave_of() * 64 + lane) % C::TM, gr.Me - 1 - i0) * (uint32_t)(a.ld_xs * 4);
+  const float* ws = a.ws + ((long long)gr.e * nb + min((j0 + wf * C::FT) / 128, nb - 1)) * kb;
+  g.mainloop(lds + kw * C::RING, a.k, ws, wf, wt, kw);
+  char* out = static_cast<char*>(a.y) + (long long)gr.r0 * a.ld_y * (a.out_bf16 ? 2 : 4);
+  if constexpr (C::KW > 1) g.store_split(lds, out, a.ld_y, i0, gr.Me, j0, a.n, kw, a.out_bf16);
+  else if (a.out_bf16) g.template store<true>(lds, out, a.ld_y, i0, gr.Me, j0, a.n, wf, wt);
+  else g.template store<false>(lds, out, a.ld_y, i0, gr.Me, j0, a.n, wf, wt);
+}
+
+//                   rows cols  wavefronts ring spread workgroups per CU
+using Large = CfgQ<256, 256, 2, 4, 2, 4, 1>;
+using Wide = CfgQ<192, 256, 2, 4, 2, 4, 1>;
+using Medium = CfgQ<128, 256, 2, 4, 3, 4, 1>;
+using Square = CfgQ<128, 128, 2, 2, 2, 4, 2>;
+using Small = CfgQ<64, 128, 1, 4, 3, 4, 2>;
+using Split = CfgQ<32, 32, 1, 1, 2, 4, 1, 8>;
+using Split64 = CfgQ<32, 64, 1, 1, 3, 4, 1, 4>;
+
+template <class C>
+hipError_t launch(const GemmArgs& a, hipStream_t s) {
+  const long long nj = (a.n + C::TN - 1) / C::TN;
+  const long long mi = a.row_offset ? ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM : (a.rows + C::TM - 1) / C::TM;
+  const long long grid = (nj * mi + 255) / 256 * 256;
+  if (grid * C::THREADS >= (1ll << 32)) return launch_gemm_any(a, true, s);
+  moe_gemm_fp8<C><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
+  switch (id) {
+    case 1: return launch<Large>(a, s);
+    case 2: return launch<Wide>(a, s);
+    case 3: return launch<Medium>(a, s);
+    case 4: return launch<Square>(a, s);
+    case 5: return launch<Small>(a, s);
+    case 6: return launch<Split>(a, s);
+    case 7: return launch<Split64>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace moe

@@ -163,9 +163,10 @@ struct GemmArgs {
   int expected;                // rows expected in all experts together
 };
 hipError_t launch_gemm_any(const GemmArgs& a, bool fp8, hipStream_t s);
-// tiles 1 .. kBf16GemmTiles of the 16-byte bf16 kernels
-constexpr int kBf16GemmTiles = 4;
+// tiles 1 .. kBf16GemmTiles (kFp8GemmTiles) of the 16-byte kernels
+constexpr int kBf16GemmTiles = 6, kFp8GemmTiles = 7;
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s);
+hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s);
 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t stream);
 

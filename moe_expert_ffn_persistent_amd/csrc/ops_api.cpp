@@ -28,6 +28,11 @@ int choose_bf16(const GemmArgs& a) {
   return avg > 192 ? 1 : avg > 64 ? 2 : 4;
 }
 
+int choose_fp8(const GemmArgs& a) {
+  const long long avg = a.expected / a.L;
+  return avg > 192 ? 1 : avg > 64 ? 3 : avg > 32 ? 5 : 6;
+}
+
 }  // namespace
 
 extern "C" {
@@ -218,7 +223,6 @@ int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const
       p->ld_w < p->k || p->ld_y < p->n || p->ld_xs < (p->k + 127) / 128 ||
       p->expert_stride_w < (p->num_experts > 1 ? (p->n - 1) * p->ld_w + p->k : 0) || !dtype_ok(p->out_dtype) || p->tile < 0)
     return MOE_ERR_INVALID_ARG;
-  if (p->tile > 0) return MOE_ERR_UNSUPPORTED;
   if (!row_offset && p->num_experts != 1) return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
   if (!x || !x_scales || !w || !w_scales || !y || !aligned(y, p->out_dtype == MOE_Y_BF16 ? 2 : 4))
@@ -242,7 +246,12 @@ int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const
   a.k = p->k;
   a.out_bf16 = p->out_dtype == MOE_Y_BF16;
   a.expected = expected_rows(p->expected_rows, p->rows);
-  return done(launch_gemm_any(a, true, (hipStream_t)stream));
+  const bool fast = aligned(x, 16) && aligned(w, 16) && aligned(y, 16) && p->n % 8 == 0 && p->k % 16 == 0 &&
+                    p->ld_x % 16 == 0 && p->ld_w % 16 == 0 && p->ld_y % 8 == 0 && p->expert_stride_w % 16 == 0 &&
+                    std::max(p->ld_x, std::max(p->ld_w, p->ld_xs)) <= (1 << 22);
+  if (p->tile > kFp8GemmTiles || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
+  if (!fast) return done(launch_gemm_any(a, true, (hipStream_t)stream));
+  return done(launch_gemm_fp8(p->tile > 0 ? p->tile : choose_fp8(a), a, (hipStream_t)stream));
 }
 
 }  // extern "C"

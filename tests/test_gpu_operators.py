@@ -19,6 +19,7 @@ pytestmark = pytest.mark.gpu
 BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
 ULP = 2.0 ** -23
+DROP = 7 * 2.0 ** -13
 FWD, DGRAD, WGRAD = _lib.MOE_GROUPED_FORWARD, _lib.MOE_GROUPED_DGRAD, _lib.MOE_GROUPED_WGRAD
 
 
@@ -56,9 +57,9 @@ def strided(t, pad, lead=0, fill=float("nan")):
     return v
 
 
-def assert_close(got, ref, dtype, mag, terms, what):
+def assert_close(got, ref, dtype, mag, terms, what, drop=0.0):
     got = got.double().cpu()
-    tol = HALF[dtype] * (1 + 2.0 ** -8) * ref.abs() + (terms + 8) * ULP * mag + 1e-37
+    tol = HALF[dtype] * (1 + 2.0 ** -8) * (ref.abs() + drop * mag) + ((terms + 8) * ULP + drop) * mag + 1e-37
     bad = ~((got - ref).abs() <= tol)
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {((got - ref).abs() / tol).max():.3g} of the bar"
 
@@ -165,10 +166,10 @@ def test_grouped_tile_choice_changes_no_result(op, expected):
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("tile", [1, 2, 3, 4])
+@pytest.mark.parametrize("tile", [1, 2, 3, 4, 5, 6])
 @pytest.mark.parametrize("op", [FWD, DGRAD, WGRAD], ids=["forward", "dgrad", "wgrad"])
 @pytest.mark.parametrize("counts,k,n", [([0, 33, 290, 1], 264, 328), ([70, 257], 64, 8), ([3, 0, 200], 8, 64), ([64, 128], 512, 256),
-                                        ([191, 129], 1032, 136)])
+                                        ([191, 129], 1032, 136), ([1, 700], 2056, 72)])
 def test_grouped_every_tile(counts, k, n, op, tile, out_dtype):
     run_grouped(op, counts, k, n, out_dtype, seed=k + n, first=2, behind=4, pad=8, tile=tile)
 
@@ -524,7 +525,16 @@ def test_fp8_tile_choice_changes_no_result(expected):
     run_fp8([0, 33, 290, 5], 328, 384, 320, BF, expected_rows=expected, behind=1)
 
 
-def run_fp8(counts, R, K, n, out_dtype, pad=0, lead=0, behind=0, expected_rows=None):
+@pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("tile", [1, 2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("counts,R,K,n", [([0, 33, 290, 1], 324, 272, 328), (None, 300, 64, 8), ([3, 0, 200], 203, 16, 64),
+                                          ([64, 128], 192, 512, 256), (None, 1, 8336, 136), (None, 257, 1040, 520)],
+                         ids=lambda v: str(v).replace(" ", ""))
+def test_fp8_every_tile(counts, R, K, n, tile, out_dtype):
+    run_fp8(counts, R, K, n, out_dtype, behind=3 if counts else 0, pad=16, tile=tile)
+
+
+def run_fp8(counts, R, K, n, out_dtype, pad=0, lead=0, behind=0, expected_rows=None, tile=0):
     g = gen(R + K + n)
     rows = R + behind
     L = 0 if counts is None else len(counts)
@@ -538,8 +548,8 @@ def run_fp8(counts, R, K, n, out_dtype, pad=0, lead=0, behind=0, expected_rows=N
     y = torch.full((rows, n), 7.0, dtype=out_dtype)
     say(f"fp8 counts={counts} R={R} K={K} n={n} {out_dtype} pad={pad} lead={lead}")
     got = moe.fp8_matmul(strided(x, pad, lead), strided(xs, 1 if pad else 0), strided(w, pad, lead), up(ws), row_offset=None if counts is None else up(off),
-                         out=strided(y, pad, lead), expected_rows=expected_rows).cpu()
-    assert_close(got[:R], ref[:R], out_dtype, mag[:R], K, f"fp8 {counts} {K} {n}")
+                         out=strided(y, pad, lead), expected_rows=expected_rows, tile=tile).cpu()
+    assert_close(got[:R], ref[:R], out_dtype, mag[:R], K, f"fp8 {counts} {K} {n}", DROP)
     assert (got[R:] == 7).all()
 
 
@@ -653,9 +663,9 @@ def test_fp8_layer():
     torch.cuda.synchronize()
     c = lambda t: t.cpu()   # noqa: E731
     ref, mag = fp8_reference(c(qx), c(sx), c(q1), c(s1), [0, M])
-    assert_close(a, ref, BF, mag, H, "first product")
+    assert_close(a, ref, BF, mag, H, "first product", DROP)
     ref, mag = fp8_reference(c(qh), c(sh), c(q2), c(s2), [0, M])
-    assert_close(y, ref, BF, mag, I, "second product")
+    assert_close(y, ref, BF, mag, I, "second product", DROP)
     # the whole layer against the unquantised one: x, w1 and w2, h each carry
     # half-step errors of 2^-4 at most, independent over hundreds of terms
     ad = x.double() @ w1.double().t()

@@ -317,3 +317,11 @@ def test_c_fp8_dense_has_one_matrix():
     base = dict(num_experts=2, rows=4, expected_rows=0, n=8, k=256, ld_x=256, ld_xs=2, ld_w=256, ld_y=8,
                 expert_stride_w=2048, out_dtype=1, tile=0)
     assert _call("moe_fp8_matmul", _lib.MoeFp8Params(*base.values()), None, 16, 16, 16, 16, 16) == _lib.MOE_ERR_INVALID_ARG
+
+
+def test_c_fp8_refuses_tiles_it_does_not_have():
+    base = dict(num_experts=1, rows=4, expected_rows=0, n=8, k=256, ld_x=256, ld_xs=2, ld_w=256, ld_y=8,
+                expert_stride_w=2048, out_dtype=1, tile=99)
+    assert _call("moe_fp8_matmul", _lib.MoeFp8Params(*base.values()), None, 16, 16, 16, 16, 16) == _lib.MOE_ERR_UNSUPPORTED
+    base.update(tile=1)
+    assert _call("moe_fp8_matmul", _lib.MoeFp8Params(*base.values()), None, 24, 16, 16, 16, 16) == _lib.MOE_ERR_UNSUPPORTED

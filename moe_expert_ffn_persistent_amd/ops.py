@@ -120,14 +120,59 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# Checked calls: the parameters that a check function made, by everything it
+# looked at (shapes, strides, dtypes, devices and the plain arguments; no
+# address and no value of a tensor), so that a call of sizes seen before costs a
+# lookup instead of the checks (about 2 us instead of 7, where a small kernel
+# runs for 3). Bounded: cleared when full.
+_PLANS: dict = {}
+_PLANS_MAX = 2048
+
+
+def _sig(t):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"need a tensor, got {type(t).__name__}")
+    return t.shape, t.stride(), t.dtype, t.get_device()
+
+
+def _plan(key, check, *args):
+    got = _PLANS.get(key)
+    if got is None:
+        p = check(*args)
+        _need_device(args[_FIRST_TENSOR[check]].device)
+        if len(_PLANS) >= _PLANS_MAX:
+            _PLANS.clear()
+        got = _PLANS[key] = ctypes.byref(p)
+    return got
+
+
+def _no_grad(*tensors):
+    """Raise where an input requires grad and grad mode is on: of the checks,
+    the one that shapes and types do not settle."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                _on(t.device, ("an input", t))
+
+
+_ENTRY: dict = {}
+
+
 def _launch(name, device, params, ptrs, stream):
-    if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        st = getattr(_lib.load(), name)(ctypes.byref(params), *ptrs, s.cuda_stream)
+    """One C entry point on the tensors' device (an index) and its current stream,
+    or the given one."""
+    fn = _ENTRY.get(name)
+    if fn is None:
+        fn = _ENTRY[name] = getattr(_lib.load(), name)
+    if device == torch._C._cuda_getDevice():
+        s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+        st = fn(params, *ptrs, s)
     else:
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            st = getattr(_lib.load(), name)(ctypes.byref(params), *ptrs, s.cuda_stream)
+            s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+            st = fn(params, *ptrs, s)
     if st != _lib.MOE_OK:
         _lib.check(st, name)
 
@@ -164,9 +209,10 @@ def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
         _matrix(x, "x", tuple(_ROW_TYPES))
         _need_device(x.device)
         out = _empty((row_pair.numel(), x.shape[1]), x.dtype, x.device, stream)
-    p = check_dispatch_inputs(x, row_pair, row_offset, top_k, out)
-    _need_device(x.device)
-    _launch("moe_dispatch_rows", x.device, p,
+    _no_grad(x, out)
+    p = _plan(("dispatch", _sig(x), _sig(row_pair), _sig(row_offset), top_k, _sig(out)), check_dispatch_inputs,
+              x, row_pair, row_offset, top_k, out)
+    _launch("moe_dispatch_rows", x.get_device(), p,
             (x.data_ptr(), row_pair.data_ptr(), row_offset.data_ptr(), out.data_ptr()), stream)
     return out
 
@@ -197,9 +243,10 @@ def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stre
         if out_dtype not in _OUT:
             raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
         out = _empty((pair_row.numel() // max(1, top_k), rows.shape[1]), out_dtype, rows.device, stream)
-    p = check_combine_rows_inputs(rows, pair_row, top_k, out)
-    _need_device(rows.device)
-    _launch("moe_combine_rows", rows.device, p, (rows.data_ptr(), pair_row.data_ptr(), out.data_ptr()), stream)
+    _no_grad(rows, out)
+    p = _plan(("combine", _sig(rows), _sig(pair_row), top_k, _sig(out)), check_combine_rows_inputs,
+              rows, pair_row, top_k, out)
+    _launch("moe_combine_rows", rows.get_device(), p, (rows.data_ptr(), pair_row.data_ptr(), out.data_ptr()), stream)
     return out
 
 
@@ -225,9 +272,10 @@ def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate
 
 
 def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, tile, stream):
-    p = check_grouped_inputs(op, x, w, y, row_offset, expected_rows, accumulate, tile)
-    _need_device(x.device)
-    _launch("moe_grouped_matmul", x.device, p,
+    _no_grad(x, w, y)
+    p = _plan((op, _sig(x), _sig(w), _sig(y), _sig(row_offset), expected_rows, accumulate, tile), check_grouped_inputs,
+              op, x, w, y, row_offset, expected_rows, accumulate, tile)
+    _launch("moe_grouped_matmul", x.get_device(), p,
             (row_offset.data_ptr(), x.data_ptr(), w.data_ptr(), y.data_ptr()), stream)
 
 
@@ -324,9 +372,10 @@ def swiglu(gate_up, row_weight=None, row_offset=None, out=None, scales=None, out
             out = _empty((rows, I), out_dtype, gate_up.device, stream)
         if scales is None and out.dtype in _CODES:
             scales = _empty((rows, _blocks(I)), torch.float32, gate_up.device, stream)
-    p = check_swiglu_inputs(gate_up, row_weight, row_offset, out, scales)
-    _need_device(gate_up.device)
-    _launch("moe_swiglu", gate_up.device, p,
+    _no_grad(gate_up, row_weight, out, scales)
+    p = _plan(("swiglu", _sig(gate_up), _sig(row_weight), _sig(row_offset), _sig(out), _sig(scales)), check_swiglu_inputs,
+              gate_up, row_weight, row_offset, out, scales)
+    _launch("moe_swiglu", gate_up.get_device(), p,
             (gate_up.data_ptr(), _ptr(row_weight), _ptr(row_offset), out.data_ptr(), _ptr(scales)), stream)
     return out if scales is None else (out, scales)
 
@@ -357,9 +406,10 @@ def swiglu_backward(gate_up, dh, row_weight=None, row_offset=None, out=None, dro
             out = _empty((rows, 2 * I), torch.bfloat16, gate_up.device, stream)
         if drow_weight is None and row_weight is not None:
             drow_weight = _empty((rows,), torch.float32, gate_up.device, stream)
-    p = check_swiglu_backward_inputs(gate_up, dh, row_weight, row_offset, out, drow_weight)
-    _need_device(gate_up.device)
-    _launch("moe_swiglu_backward", gate_up.device, p,
+    _no_grad(gate_up, dh, row_weight, out, drow_weight)
+    p = _plan(("swiglu_backward", _sig(gate_up), _sig(dh), _sig(row_weight), _sig(row_offset), _sig(out), _sig(drow_weight)),
+              check_swiglu_backward_inputs, gate_up, dh, row_weight, row_offset, out, drow_weight)
+    _launch("moe_swiglu_backward", gate_up.get_device(), p,
             (gate_up.data_ptr(), dh.data_ptr(), _ptr(row_weight), _ptr(row_offset), out.data_ptr(),
              _ptr(drow_weight)), stream)
     return out, drow_weight
@@ -412,11 +462,12 @@ def quantize_fp8(x, block_rows=1, row_offset=None, out=None, scales=None, stream
             out = _empty(tuple(x.shape), torch.float8_e4m3fn, x.device, stream)
         if scales is None:
             scales = _empty(_scale_shape(x, block_rows), torch.float32, x.device, stream)
-    p = check_quantize_inputs(x, block_rows, row_offset, out, scales)
-    _need_device(x.device)
-    if p.batch:
-        _launch("moe_quantize_fp8", x.device, p, (x.data_ptr(), _ptr(row_offset), out.data_ptr(), scales.data_ptr()),
-                stream)
+    _no_grad(x, out, scales)
+    p = _plan(("quantize", _sig(x), block_rows, _sig(row_offset), _sig(out), _sig(scales)), check_quantize_inputs,
+              x, block_rows, row_offset, out, scales)
+    if x.numel():
+        _launch("moe_quantize_fp8", x.get_device(), p,
+                (x.data_ptr(), _ptr(row_offset), out.data_ptr(), scales.data_ptr()), stream)
     return out, scales
 
 
@@ -462,9 +513,15 @@ def fp8_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=to
             raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
         _need_device(x.device)
         out = _empty((x.shape[0], w.shape[-2]), out_dtype, x.device, stream)
-    p = check_fp8_inputs(x, x_scales, w, w_scales, row_offset, out, expected_rows, tile)
-    _need_device(x.device)
-    _launch("moe_fp8_matmul", x.device, p,
+    _no_grad(x_scales, w_scales, out)
+    p = _plan(("fp8", _sig(x), _sig(x_scales), _sig(w), _sig(w_scales), _sig(row_offset), _sig(out), expected_rows, tile),
+              check_fp8_inputs, x, x_scales, w, w_scales, row_offset, out, expected_rows, tile)
+    _launch("moe_fp8_matmul", x.get_device(), p,
             (_ptr(row_offset), x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), out.data_ptr()),
             stream)
     return out
+
+
+# which argument of a check function is its first tensor
+_FIRST_TENSOR = {check_dispatch_inputs: 0, check_combine_rows_inputs: 0, check_grouped_inputs: 1, check_swiglu_inputs: 0,
+                 check_swiglu_backward_inputs: 0, check_quantize_inputs: 0, check_fp8_inputs: 0}

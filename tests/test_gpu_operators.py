@@ -689,3 +689,31 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in got:
         assert torch.equal(a, want_f) and torch.equal(b, want_w)
+
+
+def test_checks_hold_for_sizes_seen_before():
+    # a call of known sizes skips the checks that sizes settle, and no other
+    g = gen(41)
+    x, w, off = up(normal(g, 30, 64)), up(normal(g, 2, 32, 64)), up(offsets([10, 20]))
+    out = torch.empty(30, 32, dtype=BF, device="cuda")
+    want = moe.grouped_matmul(x, w, off).clone()
+    for _ in range(2):
+        assert torch.equal(moe.grouped_matmul(x, w, off, out=out), want)
+    with pytest.raises(ValueError):
+        moe.grouped_matmul(x, w.clone().requires_grad_(), off, out=out)
+    with pytest.raises(ValueError):
+        moe.grouped_matmul(x, w, off, out=out.cpu())
+    with pytest.raises(ValueError):
+        moe.grouped_matmul(x, w, off.cpu(), out=out)
+    with pytest.raises(ValueError):
+        moe.grouped_matmul(x, w.transpose(0, 1), off, out=out)
+    with pytest.raises(ValueError):
+        moe.grouped_matmul(x, w, off.long(), out=out)
+    with pytest.raises(_lib.MoeError):
+        moe.grouped_matmul(x, w, off, out=out, tile=99)
+    # an unaligned tensor of the same sizes takes another kernel, same numbers
+    buf = torch.empty(30 * 64 + 1, dtype=BF, device="cuda")
+    xu = buf[1:].view(30, 64)
+    xu.copy_(x)
+    got = moe.grouped_matmul(xu, w, off)
+    assert (got.float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max()

@@ -367,13 +367,13 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
   const int wave = uni((int)(threadIdx.x >> 6)), kw = C::KW == 1 ? 0 : wave;
   const int wf = C::KW == 1 ? wave % C::WF : 0, wt = C::KW == 1 ? wave / C::WF : 0;
   char* const ring = lds + kw * C::RING;
-  const int tile = xcd_tile(blockIdx.x);
   TileG<C, WG, OP != MOE_GROUPED_FORWARD> g;
   const __bf16* x = static_cast<const __bf16*>(a.x);
   const __bf16* w = static_cast<const __bf16*>(a.w);
   const __bf16* y = static_cast<const __bf16*>(a.y);
   if constexpr (WG) {
     const int mi = (a.n + C::TM - 1) / C::TM, ni = (a.k + C::TN - 1) / C::TN;
+    const int tile = xcd_tile(blockIdx.x, a.L * mi * ni);
     const int e = tile / (mi * ni);
     if (e >= a.L) return;
     int i, j;
@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
     constexpr bool FWD = OP == MOE_GROUPED_FORWARD;
     const int nj = FWD ? a.n : a.k, nc = FWD ? a.k : a.n, ni = (nj + C::TN - 1) / C::TN;
     const GroupScan<C::TM> scan(a.row_offset, a.L, a.rows);
+    const int tile = xcd_tile(blockIdx.x, scan.total * ni);
     if (tile >= scan.total * ni) return;
     int p, j;
     tile_at(tile, scan.total, ni, p, j);
@@ -416,7 +417,7 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
   const long long nj = ((OP == MOE_GROUPED_FORWARD ? a.n : a.k) + C::TN - 1) / C::TN;
   const long long mi = OP == MOE_GROUPED_WGRAD ? (long long)a.L * ((a.n + C::TM - 1) / C::TM)
                                                : ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM;
-  const long long grid = (nj * mi + 255) / 256 * 256;   // xcd_tile deals 256 at a time
+  const long long grid = (nj * mi + 255) / 256 * 256;   // whole deals of runs (xcd_tile)
   if (grid * C::THREADS >= (1ll << 32)) return launch_gemm_any(a, false, s);
   moe_gemm_bf16<C, OP><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
   return hipGetLastError();

@@ -279,18 +279,19 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   const int wave = uni((int)(threadIdx.x >> 6)), kw = C::KW == 1 ? 0 : wave, lane = threadIdx.x & 63;
   const int wf = C::KW == 1 ? wave % C::WF : 0, wt = C::KW == 1 ? wave / C::WF : 0;
-  const int tile = xcd_tile(blockIdx.x);
   const int ni = (a.n + C::TN - 1) / C::TN, kb = (a.k + 127) / 128, nb = (a.n + 127) / 128;
   Group gr;
   int j;
   if (a.row_offset) {
     const GroupScan<C::TM> scan(a.row_offset, a.L, a.rows);
+    const int tile = xcd_tile(blockIdx.x, scan.total * ni);
     if (tile >= scan.total * ni) return;
     int p;
     tile_at(tile, scan.total, ni, p, j);
     gr = scan.find(p);
   } else {
     const int mi = (a.rows + C::TM - 1) / C::TM;
+    const int tile = xcd_tile(blockIdx.x, mi * ni);
     if (tile >= mi * ni) return;
     gr = Group{0, 0, 0, a.rows, true};
     tile_at(tile, mi, ni, gr.m, j);

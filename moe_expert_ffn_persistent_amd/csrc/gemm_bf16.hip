@@ -19,6 +19,8 @@
 // per stage. A ragged end (the last c of a row, or of an expert's rows in
 // wgrad) is zeros in LDS: lanes past the end write a zero instead of copying.
 // Rows i past an expert's end repeat its last row and are not stored.
+#include <climits>
+
 #include "internal.hpp"
 #include "ops_common.hpp"
 
@@ -53,8 +55,9 @@ struct CfgG {
   static constexpr int STAGE = T_BYTES + F_BYTES;
   static constexpr int NIT = T_BYTES / 1024 / NW, NIF = F_BYTES / 1024 / NW, NI = NIT + NIF;
   static constexpr int EPI = NW * 32 * FT * 4;     // epilogue staging: 32 rows a wavefront, fp32
-  static constexpr int RING = NS * STAGE > EPI ? NS * STAGE : EPI;
+  static constexpr int RING = NS * STAGE;
   static constexpr int LDS = KW * RING;
+  static_assert(RING - STAGE >= EPI || KW > 1, "the epilogue stages behind the next tile's first stage");
   static_assert(KW == 1 || (NW == 1 && TM == 32), "split wavefronts hold the whole tile each");
   static constexpr int issue_slot(int i, int nm) { return i * nm * SP / (NI * 8); }
   static_assert(T_BYTES % (1024 * NW) == 0 && F_BYTES % (1024 * NW) == 0, "copies split evenly over the wavefronts");
@@ -166,14 +169,15 @@ struct TileG {
 
   // One stage of MFMAs; with COPY the copies of stage kt_next spread over the
   // first SP/8 of them. Fragments of k-step ks+1 are read during the MFMAs of
-  // k-step ks.
-  template <bool COPY>
+  // k-step ks. Only the first NTB of the wavefront's 32-row blocks are
+  // multiplied (the others hold no rows).
+  template <bool COPY, int NTB>
   __device__ __forceinline__ void compute(const char* stage, int wf, int wt, int kt_next, uint32_t slot) {
-    constexpr int KS = kBK / 16, NMF = C::FB * C::TB, NL = C::FB + C::TB;
+    constexpr int KS = kBK / 16, NMF = C::FB * NTB, NL = C::FB + NTB;
     bf16x8 af[2][C::FB], bf[2][C::TB];
     auto load = [&](int ks, int q) {
       if (q < C::FB) af[ks & 1][q] = f.frag(stage, wf * C::FT + q * 32, ks);
-      else bf[ks & 1][q - C::FB] = t.frag(stage + C::F_BYTES, wt * C::TT + (q - C::FB) * 32, ks);
+      else bf[ks & 1][q - C::FB] = t.frag(stage + C::F_BYTES, ((q - C::FB) * C::WT + wt) * 32, ks);
     };
 #pragma unroll
     for (int q = 0; q < NL; ++q) load(0, q);
@@ -182,7 +186,7 @@ struct TileG {
     for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
       for (int m = 0; m < NMF; ++m) {
-        const int fb = m / C::TB, tb = m % C::TB;
+        const int fb = m / NTB, tb = m % NTB;
         acc[fb][tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[ks & 1][fb], bf[ks & 1][tb], acc[fb][tb], 0, 0, 0);
         if (ks + 1 < KS) {
 #pragma unroll
@@ -199,7 +203,21 @@ struct TileG {
     }
   }
 
-  // All of c, `nc` of them (with KW > 1, the stages kw, kw + KW, ... of them).
+  // Copies of the first stage of `nc` c (with KW > 1, the wavefront's first).
+  __device__ __forceinline__ void first(char* lds, int nc, int kw) const {
+    const int all = nc / kBK;
+    if (kw < all) {
+#pragma unroll
+      for (int i = 0; i < C::NI; ++i) issue(i, kw, (uint32_t)(uintptr_t)lds);
+    } else if (kw == all && nc % kBK) {
+      f.issue_tail(kw, nc % kBK, lds);
+      t.issue_tail(kw, nc % kBK, lds + C::F_BYTES);
+    }
+  }
+
+  // All of c, `nc` of them (with KW > 1, the stages kw, kw + KW, ... of them),
+  // the first stage's copies already issued.
+  template <int NTB>
   __device__ __forceinline__ void mainloop(char* lds, int nc, int wf, int wt, int kw) {
 #pragma unroll
     for (int fb = 0; fb < C::FB; ++fb)
@@ -216,13 +234,20 @@ struct TileG {
       f.issue_tail(at(s), left, slot);
       t.issue_tail(at(s), left, slot + C::F_BYTES);
     };
+    if constexpr (C::NS > 2) {
+      // The other slots may hold the previous tile's staging: every wavefront is
+      // past it. Its stores are drained with the first stage, so that the counts
+      // below see copies only.
+      vm_wait<0>();
+      if constexpr (C::KW == 1) lds_barrier();
 #pragma unroll
-    for (int s = 0; s < C::NS - 1; ++s) {
-      if (s < full) {
+      for (int s = 1; s < C::NS - 1; ++s) {
+        if (s < full) {
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) issue(i, at(s), ring + s * C::STAGE);
-      } else if (s < nk) {
-        tail(s);
+          for (int i = 0; i < C::NI; ++i) issue(i, at(s), ring + s * C::STAGE);
+        } else if (s < nk) {
+          tail(s);
+        }
       }
     }
     int slot = 0;
@@ -231,7 +256,7 @@ struct TileG {
       vm_wait<C::NI * (C::NS - 2)>();
       if constexpr (C::KW == 1) lds_barrier();
       const int nslot = slot == 0 ? C::NS - 1 : slot - 1;
-      compute<true>(lds + slot * C::STAGE, wf, wt, at(s + C::NS - 1), ring + nslot * C::STAGE);
+      compute<true, NTB>(lds + slot * C::STAGE, wf, wt, at(s + C::NS - 1), ring + nslot * C::STAGE);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
     for (int s = max(nmain, 0); s < nk; ++s) {
@@ -240,9 +265,26 @@ struct TileG {
       else vm_wait_ahead<C::NI, C::NS - 2>(nk - 1 - s);
       if constexpr (C::KW == 1) lds_barrier();
       if (left && s + C::NS - 1 == full) tail(full);
-      compute<false>(lds + slot * C::STAGE, wf, wt, 0, 0);
+      compute<false, NTB>(lds + slot * C::STAGE, wf, wt, 0, 0);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
+  }
+
+  // The tile's `rows` rows (at least one): 32-row blocks go to the row
+  // wavefronts in turn, so a short tile keeps all of them equally busy with
+  // fewer MFMAs.
+  __device__ __forceinline__ void multiply(char* lds, int rows, int nc, int wf, int wt, int kw) {
+    const int blocks = (min(rows, C::TM) + 32 * C::WT - 1) / (32 * C::WT);
+    if constexpr (C::TB >= 4) {
+      switch (blocks) {
+        case 1: return mainloop<1>(lds, nc, wf, wt, kw);
+        case 2: return mainloop<2>(lds, nc, wf, wt, kw);
+        case 3: return mainloop<3>(lds, nc, wf, wt, kw);
+      }
+    } else if constexpr (C::TB == 2) {
+      if (blocks == 1) return mainloop<1>(lds, nc, wf, wt, kw);
+    }
+    mainloop<C::TB>(lds, nc, wf, wt, kw);
   }
 
   // KW > 1: the wavefronts' sums to LDS, joined in their order and written out.
@@ -304,7 +346,8 @@ struct TileG {
 
   // Output rows i0 .. of ni, columns j0 .. of nj: every wavefront stages its 32
   // rows by FT columns in its own LDS and writes whole pieces of 16 bytes, FT
-  // columns of a row together. ADD: the sum is added to what is there, in fp32,
+  // columns of a row together. `lds`: staging, behind the first ring slot, which
+  // the next tile's copies may be filling. ADD: the sum is added to what is there, in fp32,
   // before the one rounding.
   template <bool BF16, bool ADD>
   __device__ __forceinline__ void store(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int wf,
@@ -313,8 +356,7 @@ struct TileG {
     constexpr int EB = PACK ? 2 : 4, OB = BF16 ? 2 : 4;   // bytes of a staged and of an output element
     constexpr int ROWB = C::FT * EB, NCH = ROWB / 16, RPP = 64 / NCH;
     const int tid = opaque(threadIdx.x), lane = tid & 63;
-    char* mine = lds + (tid >> 6) * (32 * C::FT * 4);
-    lds_barrier();   // every wavefront is done with the ring
+    char* mine = lds + C::STAGE + (tid >> 6) * (32 * C::FT * 4);
 #pragma unroll
     for (int tb = 0; tb < C::TB; ++tb) {
 #pragma unroll
@@ -336,7 +378,7 @@ struct TileG {
       const int c = lane % NCH, col = j0 + wf * C::FT + c * (16 / EB);
 #pragma unroll
       for (int r0 = 0; r0 < 32; r0 += RPP) {
-        const int r = r0 + lane / NCH, i = i0 + wt * C::TT + tb * 32 + r;
+        const int r = r0 + lane / NCH, i = i0 + (tb * C::WT + wt) * 32 + r;
         if (i < ni && col < nj) {
           const uint4 v = *reinterpret_cast<const uint4*>(mine + stage_off<ROWB>(r, c * 16));
           char* p = static_cast<char*>(out) + ((long long)i * ld + col) * OB;
@@ -360,47 +402,79 @@ struct TileG {
   }
 };
 
+// A tile of the call: output rows i0 .. of ni, columns j0 .., nc sums, at `out`.
+struct Work {
+  int i0, ni, j0, nc;
+  char* out;
+};
+
+// One workgroup per place on the GPU walks the tiles blockIdx.x, + gridDim.x,
+// ...: while a tile is written out the next one's first stage is already on its
+// way (a tile of 16 stages spends a fifth of its time on its ends otherwise).
 template <class C, int OP>
 __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_gemm_bf16(const GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
-  constexpr bool WG = OP == MOE_GROUPED_WGRAD;
+  constexpr bool WG = OP == MOE_GROUPED_WGRAD, FWD = OP == MOE_GROUPED_FORWARD;
   const int wave = uni((int)(threadIdx.x >> 6)), kw = C::KW == 1 ? 0 : wave;
   const int wf = C::KW == 1 ? wave % C::WF : 0, wt = C::KW == 1 ? wave / C::WF : 0;
   char* const ring = lds + kw * C::RING;
-  TileG<C, WG, OP != MOE_GROUPED_FORWARD> g;
+  TileG<C, WG, !FWD> g;
   const __bf16* x = static_cast<const __bf16*>(a.x);
   const __bf16* w = static_cast<const __bf16*>(a.w);
   const __bf16* y = static_cast<const __bf16*>(a.y);
-  if constexpr (WG) {
-    const int mi = (a.n + C::TM - 1) / C::TM, ni = (a.k + C::TN - 1) / C::TN;
-    const int tile = xcd_tile(blockIdx.x, a.L * mi * ni);
-    const int e = tile / (mi * ni);
-    if (e >= a.L) return;
-    int i, j;
-    tile_at(tile - e * mi * ni, mi, ni, i, j);
-    const int r0 = uni(clamped_offset(a.row_offset, a.L, a.rows, e));
-    const int Me = uni(max(clamped_offset(a.row_offset, a.L, a.rows, e + 1) - r0, 0));
-    if (Me == 0 && a.accumulate) return;
-    g.t.setup(y + (long long)r0 * a.ld_y, a.ld_y, i * C::TM, a.n);
-    g.f.setup(x + (long long)r0 * a.ld_x, a.ld_x, j * C::TN, a.k);
-    g.mainloop(ring, Me, wf, wt, kw);
-    char* out = static_cast<char*>(a.w) + (long long)e * a.es_w * (a.out_bf16 ? 2 : 4);
-    g.write(lds, out, a.ld_w, i * C::TM, a.n, j * C::TN, a.k, wf, wt, kw, a.out_bf16, a.accumulate);
-  } else {
-    constexpr bool FWD = OP == MOE_GROUPED_FORWARD;
-    const int nj = FWD ? a.n : a.k, nc = FWD ? a.k : a.n, ni = (nj + C::TN - 1) / C::TN;
-    const GroupScan<C::TM> scan(a.row_offset, a.L, a.rows);
-    const int tile = xcd_tile(blockIdx.x, scan.total * ni);
-    if (tile >= scan.total * ni) return;
-    int p, j;
-    tile_at(tile, scan.total, ni, p, j);
-    const Group gr = scan.find(p);
-    const long long ldt = FWD ? a.ld_x : a.ld_y, ldo = FWD ? a.ld_y : a.ld_x;
-    g.t.setup((FWD ? x : y) + (long long)gr.r0 * ldt, ldt, gr.m * C::TM, gr.Me);
-    g.f.setup(w + (long long)gr.e * a.es_w, a.ld_w, j * C::TN, nj);
-    g.mainloop(ring, nc, wf, wt, kw);
-    char* out = static_cast<char*>(FWD ? a.y : a.x) + (long long)gr.r0 * ldo * (a.out_bf16 ? 2 : 4);
-    g.write(lds, out, ldo, gr.m * C::TM, gr.Me, j * C::TN, nj, wf, wt, kw, a.out_bf16, false);
+  const int nj = FWD ? a.n : a.k;                    // output columns
+  const int tj = (nj + C::TN - 1) / C::TN;           // tiles along them
+  const int ti = WG ? (a.n + C::TM - 1) / C::TM : 0; // wgrad: tiles along an expert's rows of W
+  const long long ldt = FWD ? a.ld_x : a.ld_y, ldo = WG ? a.ld_w : FWD ? a.ld_y : a.ld_x;
+  const int oe = a.out_bf16 ? 2 : 4;
+  const GroupScan<C::TM> scan(a.row_offset, a.L, a.rows);
+  const int total = WG ? a.L * ti * tj : scan.total * tj;
+
+  // tile of workgroup slot b: what it is, and the copies of its first stage
+  auto start = [&](int b, Work& wk) {
+    const int tile = xcd_tile(b, total);
+    if (tile >= total) return false;
+    if constexpr (WG) {
+      const int e = tile / (ti * tj);
+      int i, j;
+      tile_at(tile - e * ti * tj, ti, tj, i, j);
+      const int r0 = uni(clamped_offset(a.row_offset, a.L, a.rows, e));
+      const int Me = uni(max(clamped_offset(a.row_offset, a.L, a.rows, e + 1) - r0, 0));
+      wk = Work{i * C::TM, a.n, j * C::TN, Me, static_cast<char*>(a.w) + (long long)e * a.es_w * oe};
+      g.t.setup(y + (long long)r0 * a.ld_y, a.ld_y, wk.i0, a.n);
+      g.f.setup(x + (long long)r0 * a.ld_x, a.ld_x, wk.j0, a.k);
+    } else {
+      int p, j;
+      tile_at(tile, scan.total, tj, p, j);
+      const Group gr = scan.find(p);
+      wk = Work{gr.m * C::TM, gr.Me, j * C::TN, FWD ? a.k : a.n, static_cast<char*>(FWD ? a.y : a.x) + (long long)gr.r0 * ldo * oe};
+      g.t.setup((FWD ? x : y) + (long long)gr.r0 * ldt, ldt, wk.i0, wk.ni);
+      g.f.setup(w + (long long)gr.e * a.es_w, a.ld_w, wk.j0, nj);
+    }
+    g.first(ring, wk.nc, kw);
+    return true;
+  };
+
+  Work cur, next;
+  int b = blockIdx.x;
+  bool more = start(b, cur);
+  while (more) {
+    g.multiply(ring, cur.ni - cur.i0, cur.nc, wf, wt, kw);
+    b += gridDim.x;
+    const bool write = !WG || cur.nc > 0 || !a.accumulate;
+    if constexpr (C::KW == 1) {
+      lds_barrier();   // every wavefront is done with the ring
+      more = start(b, next);
+      if (write) g.write(lds, cur.out, ldo, cur.i0, cur.ni, cur.j0, nj, wf, wt, kw, a.out_bf16, a.accumulate);
+    } else {
+      if (write) g.write(lds, cur.out, ldo, cur.i0, cur.ni, cur.j0, nj, wf, wt, kw, a.out_bf16, a.accumulate);
+      __syncthreads();   // the joined sums are read
+      more = start(b, next);
+    }
+    // the staging's LDS writes and reads, and a short first stage's zeros, are
+    // this wavefront's own and done; the next loop's barrier publishes them
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    cur = next;
   }
 }
 
@@ -412,13 +486,18 @@ using Small = CfgG<64, 128, 1, 4, 3, 4, 2>;
 using Split = CfgG<32, 32, 1, 1, 2, 4, 1, 8>;
 using Split64 = CfgG<32, 64, 1, 1, 3, 4, 1, 4>;
 
+template <class C>
+constexpr GemmTile timed(double a, double b, double o) { return GemmTile{C::TM, C::TN, C::OCC, C::KW, a, b, o}; }
+
 template <class C, int OP>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
   const long long nj = ((OP == MOE_GROUPED_FORWARD ? a.n : a.k) + C::TN - 1) / C::TN;
   const long long mi = OP == MOE_GROUPED_WGRAD ? (long long)a.L * ((a.n + C::TM - 1) / C::TM)
                                                : ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM;
-  const long long grid = (nj * mi + 255) / 256 * 256;   // whole deals of runs (xcd_tile)
-  if (grid * C::THREADS >= (1ll << 32)) return launch_gemm_any(a, false, s);
+  const long long tiles = nj * mi;
+  if (tiles >= INT_MAX / 2) return launch_gemm_any(a, false, s);   // the kernel counts tiles in int
+  // a workgroup for each place on the GPU; a multiple of 8 keeps one on its XCD
+  const long long grid = std::min<long long>((tiles + 7) / 8 * 8, (long long)kCus * C::OCC);
   moe_gemm_bf16<C, OP><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -437,6 +516,12 @@ hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+// forward and dgrad; wgrad (whose operands both go through transposing reads)
+const GemmTile kBf16GemmTileTable[] = {timed<Large>(0.97, 1.49, 6), timed<Medium>(0.52, 0.89, 4), timed<Square>(0.62, 0.57, 1),
+                                       timed<Small>(0.31, 0.31, 3), timed<Split>(0.57, 0.89, 2), timed<Split64>(0.48, 0.62, 2)};
+const GemmTile kWgradTiles[] = {timed<Large>(1.05, 1.78, 6), timed<Medium>(0.62, 1.05, 4), timed<Square>(0.57, 0.52, 3),
+                                timed<Small>(0.31, 0.29, 3), timed<Split>(0, 0, 0), timed<Split64>(0, 0, 0)};
 
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s) {
   switch (a.op) {

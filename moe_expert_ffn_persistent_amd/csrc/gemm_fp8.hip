@@ -22,6 +22,8 @@
 // scales come along as four-byte copies. The weight scales of 64 blocks sit in
 // one register of a wavefront, a lane each. A ragged last block is zeros in
 // LDS.
+#include <climits>
+
 #include "internal.hpp"
 #include "ops_common.hpp"
 
@@ -47,11 +49,12 @@ struct CfgQ {
   static constexpr int NI = NIT + NIF + 1;               // with the row-scale copy
   static constexpr int F_BYTES = TN * 128, T_BYTES = TM * 128, S_BYTES = NW * 256;
   static constexpr int STAGE = F_BYTES + T_BYTES + S_BYTES;
-  static constexpr int EPI = NW * 32 * FT * 4;
-  static constexpr int RING = NS * STAGE > EPI ? NS * STAGE : EPI;
+  static constexpr int EPI = NW * 16 * FT * 4;
+  static constexpr int RING = NS * STAGE;
   static constexpr int LDS = KW * RING;
+  static_assert(RING - STAGE >= EPI || KW > 1, "the epilogue stages behind the next tile's first stage");
   static_assert(KW == 1 || (NW == 1 && TM == 32), "split wavefronts hold the whole tile each");
-  static constexpr int issue_slot(int i) { return i * NB * SP / (NI * 8); }
+  static constexpr int issue_slot(int i, int nb) { return i * nb * SP / (NI * 8); }
   static constexpr int NP = 4;                           // products in flight
   static_assert(FT <= 128 && 128 % FT == 0, "a wavefront's columns lie in one block of weight scales");
   static_assert(NB % NP == 0 && TB % 2 == 0 && FB >= 2, "blocks of a wavefront");
@@ -121,22 +124,26 @@ struct TileQ {
 
   // One K block; sw: its weight scale. The products of the stage's last two
   // blocks are added during the first two MFMAs of the next one.
-  template <bool COPY>
+  // Only the first NTP of the wavefront's 32-row blocks are multiplied.
+  template <bool COPY, int NTP>
   __device__ __forceinline__ void compute(const char* stage, int wf, int wt, bool first, float sw, int kt_next, uint32_t slot) {
+    constexpr int TB = 2 * NTP, NB = C::FB * TB;
+    // row of 16-row block j: 32-row blocks go to the row wavefronts in turn
+    auto row = [&](int j) { return ((j >> 1) * C::WT + wt) * 32 + (j & 1) * 16; };
     const int lane = threadIdx.x & 63, r16 = lane & 15, c0 = 2 * (lane >> 4);
     const char* ts = stage + C::F_BYTES;
-    const float* sx = reinterpret_cast<const float*>(ts + C::T_BYTES) + wt * C::TT + r16;
+    const float* sx = reinterpret_cast<const float*>(ts + C::T_BYTES) + r16;
     i32x8 af[C::FB], bf[2];
     float st[2];
-    bf[0] = frag(ts, wt * C::TT + r16, c0);
+    bf[0] = frag(ts, row(0) + r16, c0);
     af[0] = frag(stage, wf * C::FT + r16, c0);
-    st[0] = sx[0] * sw;
+    st[0] = sx[row(0)] * sw;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int b = 0; b < C::NB; ++b) {
+    for (int b = 0; b < NB; ++b) {
       const int j = b / C::FB, i = b % C::FB;
       if (b + 1 < C::FB) af[b + 1] = frag(stage, wf * C::FT + (b + 1) * 16 + r16, c0);
-      if (i == 0 && j + 1 < C::TB) bf[(j + 1) & 1] = frag(ts, wt * C::TT + (j + 1) * 16 + r16, c0);
+      if (i == 0 && j + 1 < TB) bf[(j + 1) & 1] = frag(ts, row(j + 1) + r16, c0);
       part[b % C::NP] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j & 1], f32x4{}, 0, 0, 0, 127, 0, 127);
       const int q = b - 2;
       if (q >= 0) {
@@ -145,21 +152,33 @@ struct TileQ {
         for (int v = 0; v < 4; ++v) acc[q % C::FB][q / C::FB][v] += part[q % C::NP][v] * s;
       } else if (!first) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[C::FB + q][C::TB - 1][v] += part[(q + C::NP) % C::NP][v] * s_tail[q + 2];
+        for (int v = 0; v < 4; ++v) acc[C::FB + q][TB - 1][v] += part[(q + C::NP) % C::NP][v] * s_tail[q + 2];
       }
       // the next rows' scale once the last use of the one it replaces is past
-      if (i == (C::FB > 2 ? 2 : 1) && j + 1 < C::TB) st[(j + 1) & 1] = sx[(j + 1) * 16] * sw;
+      if (i == (C::FB > 2 ? 2 : 1) && j + 1 < TB) st[(j + 1) & 1] = sx[row(j + 1)] * sw;
       if constexpr (COPY) {
 #pragma unroll
         for (int k = 0; k < C::NI; ++k)
-          if (C::issue_slot(k) == b) issue(k, kt_next, slot);
+          if (C::issue_slot(k, NB) == b) issue(k, kt_next, slot);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    s_tail[0] = s_tail[1] = st[(C::TB - 1) & 1];
+    s_tail[0] = s_tail[1] = st[(TB - 1) & 1];
   }
 
-  // All of K (with KW > 1, blocks kw, kw + KW, ...)
+  // Copies of the first block of K (with KW > 1, the wavefront's first)
+  __device__ __forceinline__ void first(char* lds, int K, int kw) const {
+    if (kw < K / 128) {
+#pragma unroll
+      for (int i = 0; i < C::NI; ++i) issue(i, kw, (uint32_t)(uintptr_t)lds);
+    } else if (kw == K / 128 && K % 128) {
+      issue_tail(kw, K % 128, lds);
+    }
+  }
+
+  // All of K (with KW > 1, blocks kw, kw + KW, ...), the first stage's copies
+  // already issued
+  template <int NTP>
   __device__ __forceinline__ void mainloop(char* lds, int K, const float* ws, int wf, int wt, int kw) {
 #pragma unroll
     for (int i = 0; i < C::FB; ++i)
@@ -172,13 +191,18 @@ struct TileQ {
     const int full = C::KW == 1 ? all : (all - kw + C::KW - 1) / C::KW;
     const int nk = full + (left != 0);
     auto at = [&](int s) { return C::KW == 1 ? s : kw + C::KW * s; };
+    if constexpr (C::NS > 2) {
+      // see the bf16 kernel: past the previous tile's staging, its stores drained
+      vm_wait<0>();
+      if constexpr (C::KW == 1) lds_barrier();
 #pragma unroll
-    for (int s = 0; s < C::NS - 1; ++s) {
-      if (s < full) {
+      for (int s = 1; s < C::NS - 1; ++s) {
+        if (s < full) {
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) issue(i, at(s), ring + s * C::STAGE);
-      } else if (s < nk) {
-        issue_tail(at(s), left, lds + s * C::STAGE);
+          for (int i = 0; i < C::NI; ++i) issue(i, at(s), ring + s * C::STAGE);
+        } else if (s < nk) {
+          issue_tail(at(s), left, lds + s * C::STAGE);
+        }
       }
     }
     float wsv = 0.f;
@@ -193,7 +217,7 @@ struct TileQ {
       vm_wait<C::NI * (C::NS - 2)>();
       if constexpr (C::KW == 1) lds_barrier();
       const int nslot = slot == 0 ? C::NS - 1 : slot - 1;
-      compute<true>(lds + slot * C::STAGE, wf, wt, s == 0, sw, at(s + C::NS - 1), ring + nslot * C::STAGE);
+      compute<true, NTP>(lds + slot * C::STAGE, wf, wt, s == 0, sw, at(s + C::NS - 1), ring + nslot * C::STAGE);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
     for (int s = max(nmain, 0); s < nk; ++s) {
@@ -202,16 +226,32 @@ struct TileQ {
       else vm_wait_ahead<C::NI, C::NS - 2>(nk - 1 - s);
       if constexpr (C::KW == 1) lds_barrier();
       if (left && s + C::NS - 1 == full) issue_tail(at(full), left, lds + (full % C::NS) * C::STAGE);
-      compute<false>(lds + slot * C::STAGE, wf, wt, s == 0, sw, 0, 0);
+      compute<false, NTP>(lds + slot * C::STAGE, wf, wt, s == 0, sw, 0, 0);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
     if (nk > 0) {
+      constexpr int TB = 2 * NTP, NB = C::FB * TB;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        acc[C::FB - 2][C::TB - 1][v] += part[(C::NB - 2) % C::NP][v] * s_tail[0];
-        acc[C::FB - 1][C::TB - 1][v] += part[(C::NB - 1) % C::NP][v] * s_tail[1];
+        acc[C::FB - 2][TB - 1][v] += part[(NB - 2) % C::NP][v] * s_tail[0];
+        acc[C::FB - 1][TB - 1][v] += part[(NB - 1) % C::NP][v] * s_tail[1];
       }
     }
+  }
+
+  // The tile's `rows` rows (at least one)
+  __device__ __forceinline__ void multiply(char* lds, int rows, int K, const float* ws, int wf, int wt, int kw) {
+    const int blocks = (min(rows, C::TM) + 32 * C::WT - 1) / (32 * C::WT);
+    if constexpr (C::TB >= 4) {
+      if (blocks == 1) return mainloop<1>(lds, K, ws, wf, wt, kw);
+    }
+    if constexpr (C::TB >= 6) {
+      if (blocks == 2) return mainloop<2>(lds, K, ws, wf, wt, kw);
+    }
+    if constexpr (C::TB >= 8) {
+      if (blocks == 3) return mainloop<3>(lds, K, ws, wf, wt, kw);
+    }
+    mainloop<C::TB / 2>(lds, K, ws, wf, wt, kw);
   }
 
   // KW > 1: the wavefronts' sums to LDS, joined in their order and written out.
@@ -242,30 +282,27 @@ struct TileQ {
     }
   }
 
-  // Rows i0 .. of ni, columns j0 .. of nj (see the bf16 kernel's store)
+  // Rows i0 .. of ni, columns j0 .. of nj (see the bf16 kernel's store), 16 rows at a time
   template <bool BF16>
   __device__ __forceinline__ void store(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int wf, int wt) {
     constexpr int EB = BF16 ? 2 : 4, ROWB = C::FT * EB, NCH = ROWB / 16, RPP = 64 / NCH;
     const int tid = opaque(threadIdx.x), lane = tid & 63;
-    char* mine = lds + (tid >> 6) * (32 * C::FT * 4);
-    lds_barrier();
+    char* mine = lds + C::STAGE + (tid >> 6) * (16 * C::FT * 4);
 #pragma unroll
-    for (int jp = 0; jp < C::TB / 2; ++jp) {
+    for (int j = 0; j < C::TB; ++j) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < C::FB; ++i) {
-          const f32x4& v = acc[i][2 * jp + h];
-          char* p = mine + stage_off<ROWB>(h * 16 + (lane & 15), (i * 16 + 4 * (lane >> 4)) * EB);
-          if constexpr (BF16) *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-          else *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
-        }
+      for (int i = 0; i < C::FB; ++i) {
+        const f32x4& v = acc[i][j];
+        char* p = mine + stage_off<ROWB>(lane & 15, (i * 16 + 4 * (lane >> 4)) * EB);
+        if constexpr (BF16) *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        else *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
+      }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       const int c = lane % NCH, col = j0 + wf * C::FT + c * (16 / EB);
 #pragma unroll
-      for (int r0 = 0; r0 < 32; r0 += RPP) {
-        const int r = r0 + lane / NCH, i = i0 + wt * C::TT + jp * 32 + r;
-        if (i < ni && col < nj)
+      for (int r0 = 0; r0 < 16; r0 += RPP) {
+        const int r = r0 + lane / NCH, i = i0 + ((j >> 1) * C::WT + wt) * 32 + (j & 1) * 16 + r;
+        if (r < 16 && i < ni && col < nj)
           *reinterpret_cast<uint4*>(static_cast<char*>(out) + ((long long)i * ld + col) * EB) =
               *reinterpret_cast<const uint4*>(mine + stage_off<ROWB>(r, c * 16));
       }
@@ -274,42 +311,65 @@ struct TileQ {
   }
 };
 
+// A tile of the call
+struct Work {
+  int i0, ni, j0;
+  const float* ws;
+  char* out;
+};
+
+// Workgroups walk the tiles as the bf16 kernel's do.
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_gemm_fp8(const GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   const int wave = uni((int)(threadIdx.x >> 6)), kw = C::KW == 1 ? 0 : wave, lane = threadIdx.x & 63;
   const int wf = C::KW == 1 ? wave % C::WF : 0, wt = C::KW == 1 ? wave / C::WF : 0;
-  const int ni = (a.n + C::TN - 1) / C::TN, kb = (a.k + 127) / 128, nb = (a.n + 127) / 128;
-  Group gr;
-  int j;
-  if (a.row_offset) {
-    const GroupScan<C::TM> scan(a.row_offset, a.L, a.rows);
-    const int tile = xcd_tile(blockIdx.x, scan.total * ni);
-    if (tile >= scan.total * ni) return;
-    int p;
-    tile_at(tile, scan.total, ni, p, j);
-    gr = scan.find(p);
-  } else {
-    const int mi = (a.rows + C::TM - 1) / C::TM;
-    const int tile = xcd_tile(blockIdx.x, mi * ni);
-    if (tile >= mi * ni) return;
-    gr = Group{0, 0, 0, a.rows, true};
-    tile_at(tile, mi, ni, gr.m, j);
-  }
+  char* const ring = lds + kw * C::RING;
+  const int tj = (a.n + C::TN - 1) / C::TN, kb = (a.k + 127) / 128, nb = (a.n + 127) / 128;
+  const int oe = a.out_bf16 ? 2 : 4;
+  const bool grouped = a.row_offset != nullptr;
+  const GroupScan<C::TM> scan(a.row_offset, grouped ? a.L : 0, a.rows);
+  const int ti = grouped ? scan.total : (a.rows + C::TM - 1) / C::TM, total = ti * tj;
   TileQ<C> g;
-  const int i0 = gr.m * C::TM, j0 = j * C::TN;
-  g.fbase = static_cast<const char*>(a.w) + (long long)gr.e * a.es_w + (long long)j0 * a.ld_w;
-  g.tbase = static_cast<const char*>(a.x) + (long long)(gr.r0 + i0) * a.ld_x;
-  g.sbase = reinterpret_cast<const char*>(a.xs + (long long)(gr.r0 + i0) * a.ld_xs);
-  g.offsets(g.fv, a.ld_w, a.n - 1 - j0);
-  g.offsets(g.tv, a.ld_x, gr.Me - 1 - i0);
-  g.sv = (uint32_t)min((g.wave_of() * 64 + lane) % C::TM, gr.Me - 1 - i0) * (uint32_t)(a.ld_xs * 4);
-  const float* ws = a.ws + ((long long)gr.e * nb + min((j0 + wf * C::FT) / 128, nb - 1)) * kb;
-  g.mainloop(lds + kw * C::RING, a.k, ws, wf, wt, kw);
-  char* out = static_cast<char*>(a.y) + (long long)gr.r0 * a.ld_y * (a.out_bf16 ? 2 : 4);
-  if constexpr (C::KW > 1) g.store_split(lds, out, a.ld_y, i0, gr.Me, j0, a.n, kw, a.out_bf16);
-  else if (a.out_bf16) g.template store<true>(lds, out, a.ld_y, i0, gr.Me, j0, a.n, wf, wt);
-  else g.template store<false>(lds, out, a.ld_y, i0, gr.Me, j0, a.n, wf, wt);
+
+  auto start = [&](int b, Work& wk) {
+    const int tile = xcd_tile(b, total);
+    if (tile >= total) return false;
+    int p, j;
+    tile_at(tile, ti, tj, p, j);
+    const Group gr = grouped ? scan.find(p) : Group{0, p, 0, a.rows, true};
+    const int i0 = gr.m * C::TM, j0 = j * C::TN;
+    g.fbase = static_cast<const char*>(a.w) + (long long)gr.e * a.es_w + (long long)j0 * a.ld_w;
+    g.tbase = static_cast<const char*>(a.x) + (long long)(gr.r0 + i0) * a.ld_x;
+    g.sbase = reinterpret_cast<const char*>(a.xs + (long long)(gr.r0 + i0) * a.ld_xs);
+    g.offsets(g.fv, a.ld_w, a.n - 1 - j0);
+    g.offsets(g.tv, a.ld_x, gr.Me - 1 - i0);
+    g.sv = (uint32_t)min((g.wave_of() * 64 + lane) % C::TM, gr.Me - 1 - i0) * (uint32_t)(a.ld_xs * 4);
+    wk = Work{i0, gr.Me, j0, a.ws + ((long long)gr.e * nb + min((j0 + wf * C::FT) / 128, nb - 1)) * kb,
+              static_cast<char*>(a.y) + (long long)gr.r0 * a.ld_y * oe};
+    g.first(ring, a.k, kw);
+    return true;
+  };
+
+  Work cur, next;
+  int b = blockIdx.x;
+  bool more = start(b, cur);
+  while (more) {
+    g.multiply(ring, cur.ni - cur.i0, a.k, cur.ws, wf, wt, kw);
+    b += gridDim.x;
+    if constexpr (C::KW == 1) {
+      lds_barrier();   // every wavefront is done with the ring
+      more = start(b, next);
+      if (a.out_bf16) g.template store<true>(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, wf, wt);
+      else g.template store<false>(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, wf, wt);
+    } else {
+      g.store_split(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, kw, a.out_bf16);
+      __syncthreads();   // the joined sums are read
+      more = start(b, next);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    cur = next;
+  }
 }
 
 //                   rows cols  wavefronts ring spread workgroups per CU
@@ -322,16 +382,24 @@ using Split = CfgQ<32, 32, 1, 1, 2, 4, 1, 8>;
 using Split64 = CfgQ<32, 64, 1, 1, 3, 4, 1, 4>;
 
 template <class C>
+constexpr GemmTile timed(double a, double b, double o) { return GemmTile{C::TM, C::TN, C::OCC, C::KW, a, b, o}; }
+
+template <class C>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
   const long long nj = (a.n + C::TN - 1) / C::TN;
   const long long mi = a.row_offset ? ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM : (a.rows + C::TM - 1) / C::TM;
-  const long long grid = (nj * mi + 255) / 256 * 256;
-  if (grid * C::THREADS >= (1ll << 32)) return launch_gemm_any(a, true, s);
+  const long long tiles = nj * mi;
+  if (tiles >= INT_MAX / 2) return launch_gemm_any(a, true, s);   // the kernel counts tiles in int
+  const long long grid = std::min<long long>((tiles + 7) / 8 * 8, (long long)kCus * C::OCC);
   moe_gemm_fp8<C><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
+
+const GemmTile kFp8GemmTileTable[] = {timed<Large>(1.15, 1.63, 6), timed<Wide>(0.97, 1.37, 4), timed<Medium>(0.74, 1.05, 4),
+                                      timed<Square>(0.57, 0.57, 3), timed<Small>(0.40, 0.40, 3), timed<Split>(0.68, 0.81, 2),
+                                      timed<Split64>(0.44, 0.62, 3)};
 
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
   switch (id) {

@@ -2,6 +2,8 @@
 // kernel choice. Nothing here allocates, waits or keeps state.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "internal.hpp"
 
 using namespace moe;
@@ -17,20 +19,52 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 
 bool dtype_ok(int32_t d) { return d == MOE_Y_FP32 || d == MOE_Y_BF16; }
 
-// the tile of a 16-byte kernel by the rows an expert is expected to have
 int expected_rows(int64_t expected, int64_t rows) {
   return (int)(expected > 0 && expected < rows ? expected : rows);
 }
 
-int choose_bf16(const GemmArgs& a) {
-  const long long avg = a.expected / a.L;
-  if (a.op == MOE_GROUPED_WGRAD) return (long long)a.L * ((a.n + 255) / 256) * ((a.k + 255) / 256) >= 256 ? 1 : 3;
-  return avg > 192 ? 1 : avg > 64 ? 2 : 4;
+// M-blocks of tm rows that the experts are expected to need: a partial block
+// each on top of their even share, one for an expert with few rows, none for
+// an expert that no row reaches.
+double expected_blocks(double rows, int L, int tm) {
+  if (L == 1) return std::ceil(rows / tm);
+  const double avg = rows / L;
+  return L * std::max(1.0 - std::exp(-avg), avg / tm + 0.5);
 }
 
-int choose_fp8(const GemmArgs& a) {
-  const long long avg = a.expected / a.L;
-  return avg > 192 ? 1 : avg > 64 ? 3 : avg > 32 ? 5 : 6;
+// Predicted microseconds of a call in tile t: every compute unit works through
+// its share of the tiles one after the other, `stages` stages and a fixed cost
+// each. The stage times are the tile's when its compute unit works alone (a)
+// and when all do (b: clock and memory are shared then); with two workgroups on
+// a compute unit b is a stage of one of the two. Fitted to 114 bf16 and 38 e4m3
+// calls of 1 to 16384 rows, 1 to 32 experts and 1024 to 7168 features, each
+// timed with every tile: the tile chosen is within 2% of the best one in the
+// mean, and within 30% at worst (where two tiles' rounds end differently).
+double predicted(const GemmTile& t, double tiles, double stages) {
+  const double q = std::max(1.0, std::ceil(tiles / kCus - 0.02));
+  const double s = t.a + (t.b - t.a) * std::min(1.0, tiles / kCus);
+  if (t.occ == 1) return q * (stages * s + t.o);
+  const double pairs = std::floor(q / 2);
+  return pairs * (stages * std::max(t.a, 2 * t.b) + t.o) + (q - 2 * pairs) * (stages * t.a + t.o);
+}
+
+int choose(const GemmTile* tiles, int n, const GemmArgs& a, int bk) {
+  const bool wgrad = a.op == MOE_GROUPED_WGRAD;
+  const int nj = a.op == MOE_GROUPED_FORWARD ? a.n : a.k, nc = a.op == MOE_GROUPED_FORWARD ? a.k : a.n;
+  int best = 1;
+  double least = 1e300;
+  for (int i = 0; i < n; ++i) {
+    const GemmTile& t = tiles[i];
+    if (wgrad && t.kw > 1) continue;   // an output tile for every 1024 columns: nothing to split for
+    const double blocks = wgrad ? (double)a.L * ((a.n + t.tm - 1) / t.tm) : expected_blocks(a.expected, a.L, t.tm);
+    const double stages = wgrad ? (double)a.expected / a.L / bk + 0.5 : std::max(1.0, (double)nc / bk / t.kw);
+    const double us = predicted(t, blocks * ((nj + t.tn - 1) / t.tn), stages);
+    if (us < least) {
+      least = us;
+      best = i + 1;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -125,7 +159,7 @@ int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offse
                     std::max(p->ld_x, std::max(p->ld_w, p->ld_y)) <= (1 << 22);
   if (p->tile > kBf16GemmTiles || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
   if (!fast) return done(launch_gemm_any(a, false, (hipStream_t)stream));
-  return done(launch_gemm_bf16(p->tile > 0 ? p->tile : choose_bf16(a), a, (hipStream_t)stream));
+  return done(launch_gemm_bf16(p->tile > 0 ? p->tile : choose(a.op == MOE_GROUPED_WGRAD ? kWgradTiles : kBf16GemmTileTable, kBf16GemmTiles, a, 64), a, (hipStream_t)stream));
 }
 
 int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_weight, const int32_t* row_offset,
@@ -251,7 +285,7 @@ int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const
                     std::max(p->ld_x, std::max(p->ld_w, p->ld_xs)) <= (1 << 22);
   if (p->tile > kFp8GemmTiles || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
   if (!fast) return done(launch_gemm_any(a, true, (hipStream_t)stream));
-  return done(launch_gemm_fp8(p->tile > 0 ? p->tile : choose_fp8(a), a, (hipStream_t)stream));
+  return done(launch_gemm_fp8(p->tile > 0 ? p->tile : choose(kFp8GemmTileTable, kFp8GemmTiles, a, 128), a, (hipStream_t)stream));
 }
 
 }  // extern "C"

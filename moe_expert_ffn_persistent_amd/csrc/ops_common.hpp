@@ -30,8 +30,9 @@ struct GroupScan {
 
   __device__ __forceinline__ GroupScan(const int32_t* off, int L, int rows) {
     const int lane = threadIdx.x & 63;
+    if (off == nullptr) L = 0;
 #pragma unroll
-    for (int j = 0; j < 5; ++j) o[j] = clamped_offset(off, L, rows, lane * 4 + j);
+    for (int j = 0; j < 5; ++j) o[j] = L == 0 ? 0 : clamped_offset(off, L, rows, lane * 4 + j);
     sum = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {

@@ -56,8 +56,8 @@ struct CfgG {
   static constexpr int NIT = T_BYTES / 1024 / NW, NIF = F_BYTES / 1024 / NW, NI = NIT + NIF;
   static constexpr int EPI = NW * 32 * FT * 4;     // epilogue staging: 32 rows a wavefront, fp32
   static constexpr int RING = NS * STAGE;
-  static constexpr int LDS = KW * RING;
-  static_assert(RING - STAGE >= EPI || KW > 1, "the epilogue stages behind the next tile's first stage");
+  // the epilogue stages behind the next tile's first stage
+  static constexpr int LDS = KW > 1 || RING >= STAGE + EPI ? KW * RING : STAGE + EPI;
   static_assert(KW == 1 || (NW == 1 && TM == 32), "split wavefronts hold the whole tile each");
   static constexpr int issue_slot(int i, int nm) { return i * nm * SP / (NI * 8); }
   static_assert(T_BYTES % (1024 * NW) == 0 && F_BYTES % (1024 * NW) == 0, "copies split evenly over the wavefronts");
@@ -72,6 +72,7 @@ struct Operand {
   static constexpr int NI = TX * kBK * 2 / 1024 / NW;   // 1 KiB copies of a wavefront per stage
   static constexpr int RB = TR ? TX * 2 : kBK * 2;      // bytes of an LDS row
   static constexpr int RPI = 1024 / RB;                 // LDS rows per copy
+  static_assert(1024 % RB == 0, "a copy fills whole LDS rows");
   const char* base;        // stage 0 (uniform)
   long long step;          // bytes from one stage to the next
   long long istep;         // TR: bytes between this wavefront's copies
@@ -275,14 +276,14 @@ struct TileG {
   // fewer MFMAs.
   __device__ __forceinline__ void multiply(char* lds, int rows, int nc, int wf, int wt, int kw) {
     const int blocks = (min(rows, C::TM) + 32 * C::WT - 1) / (32 * C::WT);
-    if constexpr (C::TB >= 4) {
-      switch (blocks) {
-        case 1: return mainloop<1>(lds, nc, wf, wt, kw);
-        case 2: return mainloop<2>(lds, nc, wf, wt, kw);
-        case 3: return mainloop<3>(lds, nc, wf, wt, kw);
-      }
-    } else if constexpr (C::TB == 2) {
+    if constexpr (C::TB >= 2) {
       if (blocks == 1) return mainloop<1>(lds, nc, wf, wt, kw);
+    }
+    if constexpr (C::TB >= 3) {
+      if (blocks == 2) return mainloop<2>(lds, nc, wf, wt, kw);
+    }
+    if constexpr (C::TB >= 4) {
+      if (blocks == 3) return mainloop<3>(lds, nc, wf, wt, kw);
     }
     mainloop<C::TB>(lds, nc, wf, wt, kw);
   }
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
 
 //                   rows cols  wavefronts ring spread workgroups per CU
 using Large = CfgG<256, 256, 2, 4, 2, 2, 1>;
+using Wide = CfgG<192, 256, 2, 4, 2, 2, 1>;
 using Medium = CfgG<128, 256, 2, 4, 3, 4, 1>;
 using Square = CfgG<128, 128, 2, 2, 2, 4, 2>;
 using Small = CfgG<64, 128, 1, 4, 3, 4, 2>;
@@ -506,11 +508,18 @@ template <int OP>
 hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
   switch (id) {
     case 1: return launch<Large, OP>(a, s);
-    case 2: return launch<Medium, OP>(a, s);
-    case 3: return launch<Square, OP>(a, s);
-    case 4: return launch<Small, OP>(a, s);
-    case 5: return launch<Split, OP>(a, s);
-    case 6: return launch<Split64, OP>(a, s);
+    case 3: return launch<Medium, OP>(a, s);
+    case 4: return launch<Square, OP>(a, s);
+    case 5: return launch<Small, OP>(a, s);
+  }
+  // not wgrad: its operands' LDS rows are a tile's columns, 1024 bytes must
+  // hold whole ones, and its tiles are many enough without splitting the sum
+  if constexpr (OP != MOE_GROUPED_WGRAD) {
+    switch (id) {
+      case 2: return launch<Wide, OP>(a, s);
+      case 6: return launch<Split, OP>(a, s);
+      case 7: return launch<Split64, OP>(a, s);
+    }
   }
   return hipErrorInvalidValue;
 }
@@ -518,10 +527,10 @@ hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
 }  // namespace
 
 // forward and dgrad; wgrad (whose operands both go through transposing reads)
-const GemmTile kBf16GemmTileTable[] = {timed<Large>(0.97, 1.49, 6), timed<Medium>(0.52, 0.89, 4), timed<Square>(0.62, 0.57, 1),
+const GemmTile kBf16GemmTileTable[] = {timed<Large>(0.97, 1.49, 6), timed<Wide>(0.75, 1.2, 5), timed<Medium>(0.52, 0.89, 4), timed<Square>(0.62, 0.57, 1),
                                        timed<Small>(0.31, 0.31, 3), timed<Split>(0.57, 0.89, 2), timed<Split64>(0.48, 0.62, 2)};
-const GemmTile kWgradTiles[] = {timed<Large>(1.05, 1.78, 6), timed<Medium>(0.62, 1.05, 4), timed<Square>(0.57, 0.52, 3),
-                                timed<Small>(0.31, 0.29, 3), timed<Split>(0, 0, 0), timed<Split64>(0, 0, 0)};
+const GemmTile kWgradTiles[] = {timed<Large>(1.05, 1.78, 6), GemmTile{}, timed<Medium>(0.62, 1.05, 4), timed<Square>(0.57, 0.52, 3),
+                                timed<Small>(0.31, 0.29, 3), GemmTile{}, GemmTile{}};
 
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s) {
   switch (a.op) {

@@ -19,9 +19,9 @@
 //
 // A stage is one K block (128 bytes a row): an NS-deep LDS ring filled by
 // direct-to-LDS copies between the MFMAs of an earlier stage; the stage's row
-// scales come along as four-byte copies. The weight scales of 64 blocks sit in
-// one register of a wavefront, a lane each. A ragged last block is zeros in
-// LDS.
+// scales come along as four-byte copies, and the weight scales by a wavefront
+// that has no rows left to fetch scales for (a load to registers would wait for
+// every copy and store in flight). A ragged last block is zeros in LDS.
 #include <climits>
 
 #include "internal.hpp"
@@ -54,11 +54,16 @@ struct CfgQ {
   static constexpr int LDS = KW * RING;
   static_assert(RING - STAGE >= EPI || KW > 1, "the epilogue stages behind the next tile's first stage");
   static_assert(KW == 1 || (NW == 1 && TM == 32), "split wavefronts hold the whole tile each");
-  static constexpr int issue_slot(int i, int nb) { return i * nb * SP / (NI * 8); }
+  // copies of a stage when only ntp 32-row blocks a wavefront hold rows, the
+  // row scales' last
+  static constexpr int copies(int ntp) { return NIF + NIT * ntp / (TB / 2) + 1; }
+  static constexpr int issue_slot(int i, int nb, int ni) { return i * nb * SP / (ni * 8); }
+  static_assert(NIT % (TB / 2) == 0, "copies of a row block");
   static constexpr int NP = 4;                           // products in flight
+  static_assert(16 * FT * 2 % 1024 == 0 || KW > 1, "a 16-row piece of the epilogue is whole stores");
   static_assert(FT <= 128 && 128 % FT == 0, "a wavefront's columns lie in one block of weight scales");
   static_assert(NB % NP == 0 && TB % 2 == 0 && FB >= 2, "blocks of a wavefront");
-  static_assert(TM <= 64 * NW, "row-scale copies cover the tile");
+  static_assert(TM < 64 * NW || KW > 1, "row-scale copies cover the tile, a wavefront is left for the weight scales");
   static_assert((TM * 128) % (1024 * NW) == 0 && (TN * 128) % (1024 * NW) == 0, "copies split evenly");
   static_assert(NS >= 2 && NI * (NS - 1) <= 63, "vmcnt range");
   static_assert(LDS * OCC <= 160 * 1024, "LDS");
@@ -122,17 +127,19 @@ struct TileQ {
     return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
   }
 
-  // One K block; sw: its weight scale. The products of the stage's last two
+  // One K block; sw: its weight scale (KW > 1; else it lies behind the row
+  // scales). The products of the stage's last two
   // blocks are added during the first two MFMAs of the next one.
   // Only the first NTP of the wavefront's 32-row blocks are multiplied.
   template <bool COPY, int NTP>
-  __device__ __forceinline__ void compute(const char* stage, int wf, int wt, bool first, float sw, int kt_next, uint32_t slot) {
-    constexpr int TB = 2 * NTP, NB = C::FB * TB;
+  __device__ __forceinline__ void compute(const char* stage, int wf, int wt, float sw, int kt_next, uint32_t slot) {
+    constexpr int TB = 2 * NTP, NB = C::FB * TB, NI = C::copies(NTP);
     // row of 16-row block j: 32-row blocks go to the row wavefronts in turn
     auto row = [&](int j) { return ((j >> 1) * C::WT + wt) * 32 + (j & 1) * 16; };
     const int lane = threadIdx.x & 63, r16 = lane & 15, c0 = 2 * (lane >> 4);
     const char* ts = stage + C::F_BYTES;
     const float* sx = reinterpret_cast<const float*>(ts + C::T_BYTES) + r16;
+    if constexpr (C::KW == 1) sw = *(reinterpret_cast<const float*>(ts + C::T_BYTES) + C::TM + wf * C::FT / 128);
     i32x8 af[C::FB], bf[2];
     float st[2];
     bf[0] = frag(ts, row(0) + r16, c0);
@@ -150,7 +157,7 @@ struct TileQ {
         const float s = st[(q / C::FB) & 1];
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[q % C::FB][q / C::FB][v] += part[q % C::NP][v] * s;
-      } else if (!first) {
+      } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[C::FB + q][TB - 1][v] += part[(q + C::NP) % C::NP][v] * s_tail[q + 2];
       }
@@ -158,8 +165,8 @@ struct TileQ {
       if (i == (C::FB > 2 ? 2 : 1) && j + 1 < TB) st[(j + 1) & 1] = sx[row(j + 1)] * sw;
       if constexpr (COPY) {
 #pragma unroll
-        for (int k = 0; k < C::NI; ++k)
-          if (C::issue_slot(k, NB) == b) issue(k, kt_next, slot);
+        for (int k = 0; k < NI; ++k)
+          if (C::issue_slot(k, NB, NI) == b) issue(k + 1 == NI ? C::NI - 1 : k, kt_next, slot);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -179,11 +186,16 @@ struct TileQ {
   // All of K (with KW > 1, blocks kw, kw + KW, ...), the first stage's copies
   // already issued
   template <int NTP>
-  __device__ __forceinline__ void mainloop(char* lds, int K, const float* ws, int wf, int wt, int kw) {
+  __device__ __forceinline__ void mainloop(char* lds, int K, const float* ws, int wf, int wt, int kw, int stores) {
+    constexpr int NI = C::copies(NTP);
 #pragma unroll
     for (int i = 0; i < C::FB; ++i)
 #pragma unroll
       for (int j = 0; j < C::TB; ++j) acc[i][j] = f32x4{};
+    // the first stage adds the products before it: nothing, exactly
+#pragma unroll
+    for (int i = 0; i < C::NP; ++i) part[i] = f32x4{};
+    s_tail[0] = s_tail[1] = 0.f;
     const int lane = threadIdx.x & 63;
     const uint32_t ring = (uint32_t)(uintptr_t)lds;
     const int all = K / 128, kb = (K + 127) / 128;
@@ -191,15 +203,15 @@ struct TileQ {
     const int full = C::KW == 1 ? all : (all - kw + C::KW - 1) / C::KW;
     const int nk = full + (left != 0);
     auto at = [&](int s) { return C::KW == 1 ? s : kw + C::KW * s; };
+    wait_first(stores);
     if constexpr (C::NS > 2) {
-      // see the bf16 kernel: past the previous tile's staging, its stores drained
-      vm_wait<0>();
+      // past the previous tile's staging
       if constexpr (C::KW == 1) lds_barrier();
 #pragma unroll
       for (int s = 1; s < C::NS - 1; ++s) {
         if (s < full) {
 #pragma unroll
-          for (int i = 0; i < C::NI; ++i) issue(i, at(s), ring + s * C::STAGE);
+          for (int i = 0; i < NI; ++i) issue(i + 1 == NI ? C::NI - 1 : i, at(s), ring + s * C::STAGE);
         } else if (s < nk) {
           issue_tail(at(s), left, lds + s * C::STAGE);
         }
@@ -207,6 +219,7 @@ struct TileQ {
     }
     float wsv = 0.f;
     auto scale = [&](int s) {
+      if constexpr (C::KW == 1) return 0.f;
       if ((s & 63) == 0) wsv = ws[min(at(s + lane), kb - 1)];
       return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv), s & 63));
     };
@@ -214,19 +227,20 @@ struct TileQ {
     const int nmain = full - (C::NS - 1);
     for (int s = 0; s < nmain; ++s) {
       const float sw = scale(s);
-      vm_wait<C::NI * (C::NS - 2)>();
+      if (s) vm_wait<NI * (C::NS - 2)>();   // the stage has landed (later ones may not have)
       if constexpr (C::KW == 1) lds_barrier();
       const int nslot = slot == 0 ? C::NS - 1 : slot - 1;
-      compute<true, NTP>(lds + slot * C::STAGE, wf, wt, s == 0, sw, at(s + C::NS - 1), ring + nslot * C::STAGE);
+      compute<true, NTP>(lds + slot * C::STAGE, wf, wt, sw, at(s + C::NS - 1), ring + nslot * C::STAGE);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
     for (int s = max(nmain, 0); s < nk; ++s) {
       const float sw = scale(s);
-      if (left) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      else vm_wait_ahead<C::NI, C::NS - 2>(nk - 1 - s);
+      if (s == 0) {
+      } else if (left) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else vm_wait_ahead<NI, C::NS - 2>(nk - 1 - s);
       if constexpr (C::KW == 1) lds_barrier();
       if (left && s + C::NS - 1 == full) issue_tail(at(full), left, lds + (full % C::NS) * C::STAGE);
-      compute<false, NTP>(lds + slot * C::STAGE, wf, wt, s == 0, sw, 0, 0);
+      compute<false, NTP>(lds + slot * C::STAGE, wf, wt, sw, 0, 0);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
     if (nk > 0) {
@@ -240,18 +254,27 @@ struct TileQ {
   }
 
   // The tile's `rows` rows (at least one)
-  __device__ __forceinline__ void multiply(char* lds, int rows, int K, const float* ws, int wf, int wt, int kw) {
+  __device__ __forceinline__ void multiply(char* lds, int rows, int K, const float* ws, int wf, int wt, int kw, int stores) {
     const int blocks = (min(rows, C::TM) + 32 * C::WT - 1) / (32 * C::WT);
     if constexpr (C::TB >= 4) {
-      if (blocks == 1) return mainloop<1>(lds, K, ws, wf, wt, kw);
+      if (blocks == 1) return mainloop<1>(lds, K, ws, wf, wt, kw, stores);
     }
     if constexpr (C::TB >= 6) {
-      if (blocks == 2) return mainloop<2>(lds, K, ws, wf, wt, kw);
+      if (blocks == 2) return mainloop<2>(lds, K, ws, wf, wt, kw, stores);
     }
     if constexpr (C::TB >= 8) {
-      if (blocks == 3) return mainloop<3>(lds, K, ws, wf, wt, kw);
+      if (blocks == 3) return mainloop<3>(lds, K, ws, wf, wt, kw, stores);
     }
-    mainloop<C::TB / 2>(lds, K, ws, wf, wt, kw);
+    mainloop<C::TB / 2>(lds, K, ws, wf, wt, kw, stores);
+  }
+
+  // see the bf16 kernel
+  __device__ __forceinline__ static void wait_first(int stores) {
+    static_assert(STORES<false> <= 63, "vmcnt range");
+    if (stores == STORES<true>) vm_wait<STORES<true>>();
+    else if (stores == STORES<false>) vm_wait<STORES<false>>();
+    else vm_wait<0>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 
   // KW > 1: the wavefronts' sums to LDS, joined in their order and written out.
@@ -284,6 +307,9 @@ struct TileQ {
 
   // Rows i0 .. of ni, columns j0 .. of nj (see the bf16 kernel's store), 16 rows at a time
   template <bool BF16>
+  static constexpr int STORES = C::TB * 16 * (C::FT * (BF16 ? 2 : 4) / 16) / 64;
+
+  template <bool BF16, bool WHOLE>
   __device__ __forceinline__ void store(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int wf, int wt) {
     constexpr int EB = BF16 ? 2 : 4, ROWB = C::FT * EB, NCH = ROWB / 16, RPP = 64 / NCH;
     const int tid = opaque(threadIdx.x), lane = tid & 63;
@@ -302,12 +328,24 @@ struct TileQ {
 #pragma unroll
       for (int r0 = 0; r0 < 16; r0 += RPP) {
         const int r = r0 + lane / NCH, i = i0 + ((j >> 1) * C::WT + wt) * 32 + (j & 1) * 16 + r;
-        if (r < 16 && i < ni && col < nj)
+        if (WHOLE || (r < 16 && i < ni && col < nj))
           *reinterpret_cast<uint4*>(static_cast<char*>(out) + ((long long)i * ld + col) * EB) =
               *reinterpret_cast<const uint4*>(mine + stage_off<ROWB>(r, c * 16));
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
+  }
+
+  // the stores that the wavefront issued, or 0 if it does not know
+  __device__ __forceinline__ int write(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int wf, int wt,
+                                       bool bf16) {
+    if (i0 + C::TM <= ni && j0 + C::TN <= nj) {
+      if (bf16) return store<true, true>(lds, out, ld, i0, ni, j0, nj, wf, wt), STORES<true>;
+      return store<false, true>(lds, out, ld, i0, ni, j0, nj, wf, wt), STORES<false>;
+    }
+    if (bf16) store<true, false>(lds, out, ld, i0, ni, j0, nj, wf, wt);
+    else store<false, false>(lds, out, ld, i0, ni, j0, nj, wf, wt);
+    return 0;
   }
 };
 
@@ -341,27 +379,35 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
     const int i0 = gr.m * C::TM, j0 = j * C::TN;
     g.fbase = static_cast<const char*>(a.w) + (long long)gr.e * a.es_w + (long long)j0 * a.ld_w;
     g.tbase = static_cast<const char*>(a.x) + (long long)(gr.r0 + i0) * a.ld_x;
-    g.sbase = reinterpret_cast<const char*>(a.xs + (long long)(gr.r0 + i0) * a.ld_xs);
     g.offsets(g.fv, a.ld_w, a.n - 1 - j0);
     g.offsets(g.tv, a.ld_x, gr.Me - 1 - i0);
-    g.sv = (uint32_t)min((g.wave_of() * 64 + lane) % C::TM, gr.Me - 1 - i0) * (uint32_t)(a.ld_xs * 4);
-    wk = Work{i0, gr.Me, j0, a.ws + ((long long)gr.e * nb + min((j0 + wf * C::FT) / 128, nb - 1)) * kb,
-              static_cast<char*>(a.y) + (long long)gr.r0 * a.ld_y * oe};
+    // scales: rows wave * 64 + lane of the tile, behind them the tile's blocks of weights
+    const long long wblock = (long long)gr.e * nb + j0 / 128;
+    const int srow = g.wave_of() * 64 + lane;
+    if (C::KW > 1 || g.wave_of() * 64 < C::TM) {
+      g.sbase = reinterpret_cast<const char*>(a.xs + (long long)(gr.r0 + i0) * a.ld_xs);
+      g.sv = (uint32_t)min(srow % C::TM, gr.Me - 1 - i0) * (uint32_t)(a.ld_xs * 4);
+    } else {
+      g.sbase = reinterpret_cast<const char*>(a.ws + wblock * kb);
+      g.sv = (uint32_t)min(srow - C::TM, min(1, nb - 1 - j0 / 128)) * (uint32_t)(kb * 4);
+    }
+    wk = Work{i0, gr.Me, j0, a.ws + wblock * kb, static_cast<char*>(a.y) + (long long)gr.r0 * a.ld_y * oe};
     g.first(ring, a.k, kw);
     return true;
   };
 
   Work cur, next;
   int b = blockIdx.x;
+  int stores = 0;   // of the previous tile, possibly in flight
   bool more = start(b, cur);
   while (more) {
-    g.multiply(ring, cur.ni - cur.i0, a.k, cur.ws, wf, wt, kw);
+    g.multiply(ring, cur.ni - cur.i0, a.k, cur.ws, wf, wt, kw, stores);
+    stores = 0;
     b += gridDim.x;
     if constexpr (C::KW == 1) {
       lds_barrier();   // every wavefront is done with the ring
       more = start(b, next);
-      if (a.out_bf16) g.template store<true>(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, wf, wt);
-      else g.template store<false>(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, wf, wt);
+      stores = g.write(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, wf, wt, a.out_bf16);
     } else {
       g.store_split(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, kw, a.out_bf16);
       __syncthreads();   // the joined sums are read

@@ -165,7 +165,7 @@ struct GemmArgs {
 constexpr int kCus = 256;   // compute units, places for a persistent workgroup
 hipError_t launch_gemm_any(const GemmArgs& a, bool fp8, hipStream_t s);
 // tiles 1 .. kBf16GemmTiles (kFp8GemmTiles) of the 16-byte kernels
-constexpr int kBf16GemmTiles = 6, kFp8GemmTiles = 7;
+constexpr int kBf16GemmTiles = 7, kFp8GemmTiles = 7;
 struct GemmTile {
   int tm, tn, occ, kw;   // rows, columns, workgroups per compute unit, wavefronts that split the sum
   double a, b, o;        // us: a stage alone, a stage with all compute units at work, a tile's ends

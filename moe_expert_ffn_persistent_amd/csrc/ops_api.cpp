@@ -55,7 +55,7 @@ int choose(const GemmTile* tiles, int n, const GemmArgs& a, int bk) {
   double least = 1e300;
   for (int i = 0; i < n; ++i) {
     const GemmTile& t = tiles[i];
-    if (wgrad && t.kw > 1) continue;   // an output tile for every 1024 columns: nothing to split for
+    if (t.tm == 0) continue;   // not a tile of this product
     const double blocks = wgrad ? (double)a.L * ((a.n + t.tm - 1) / t.tm) : expected_blocks(a.expected, a.L, t.tm);
     const double stages = wgrad ? (double)a.expected / a.L / bk + 0.5 : std::max(1.0, (double)nc / bk / t.kw);
     const double us = predicted(t, blocks * ((nj + t.tn - 1) / t.tn), stages);
@@ -157,9 +157,10 @@ int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offse
   const bool fast = aligned(x, 16) && aligned(w, 16) && aligned(y, 16) && p->n % 8 == 0 && p->k % 8 == 0 &&
                     p->ld_x % 8 == 0 && p->ld_w % 8 == 0 && p->ld_y % 8 == 0 && p->expert_stride_w % 8 == 0 &&
                     std::max(p->ld_x, std::max(p->ld_w, p->ld_y)) <= (1 << 22);
-  if (p->tile > kBf16GemmTiles || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
+  const GemmTile* tiles = wgrad ? kWgradTiles : kBf16GemmTileTable;
+  if (p->tile > kBf16GemmTiles || (p->tile > 0 && (!fast || tiles[p->tile - 1].tm == 0))) return MOE_ERR_UNSUPPORTED;
   if (!fast) return done(launch_gemm_any(a, false, (hipStream_t)stream));
-  return done(launch_gemm_bf16(p->tile > 0 ? p->tile : choose(a.op == MOE_GROUPED_WGRAD ? kWgradTiles : kBf16GemmTileTable, kBf16GemmTiles, a, 64), a, (hipStream_t)stream));
+  return done(launch_gemm_bf16(p->tile > 0 ? p->tile : choose(tiles, kBf16GemmTiles, a, 64), a, (hipStream_t)stream));
 }
 
 int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_weight, const int32_t* row_offset,

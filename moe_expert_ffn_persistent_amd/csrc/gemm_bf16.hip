@@ -527,10 +527,11 @@ hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
 }  // namespace
 
 // forward and dgrad; wgrad (whose operands both go through transposing reads)
-const GemmTile kBf16GemmTileTable[] = {timed<Large>(0.97, 1.49, 6), timed<Wide>(0.75, 1.2, 5), timed<Medium>(0.52, 0.89, 4), timed<Square>(0.62, 0.57, 1),
-                                       timed<Small>(0.31, 0.31, 3), timed<Split>(0.57, 0.89, 2), timed<Split64>(0.48, 0.62, 2)};
-const GemmTile kWgradTiles[] = {timed<Large>(1.05, 1.78, 6), GemmTile{}, timed<Medium>(0.62, 1.05, 4), timed<Square>(0.57, 0.52, 3),
-                                timed<Small>(0.31, 0.29, 3), GemmTile{}, GemmTile{}};
+const GemmTile kBf16GemmTileTable[] = {timed<Large>(0.81, 1.49, 5), timed<Wide>(0.74, 1.25, 4),  timed<Medium>(0.48, 0.89, 5),
+                                       timed<Square>(0.62, 0.57, 1), timed<Small>(0.29, 0.34, 4), timed<Split>(0.74, 0.97, 1),
+                                       timed<Split64>(0.52, 0.62, 2)};
+const GemmTile kWgradTiles[] = {timed<Large>(1.05, 1.78, 6), GemmTile{}, timed<Medium>(0.62, 0.97, 4), timed<Square>(0.52, 0.48, 4),
+                                timed<Small>(0.34, 0.31, 3), GemmTile{}, GemmTile{}};
 
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s) {
   switch (a.op) {

@@ -443,9 +443,9 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
 
 }  // namespace
 
-const GemmTile kFp8GemmTileTable[] = {timed<Large>(1.15, 1.63, 6), timed<Wide>(0.97, 1.37, 4), timed<Medium>(0.74, 1.05, 4),
-                                      timed<Square>(0.57, 0.57, 3), timed<Small>(0.40, 0.40, 3), timed<Split>(0.68, 0.81, 2),
-                                      timed<Split64>(0.44, 0.62, 3)};
+const GemmTile kFp8GemmTileTable[] = {timed<Large>(0.74, 1.63, 6),  timed<Wide>(0.68, 1.37, 5),  timed<Medium>(0.57, 0.97, 5),
+                                      timed<Square>(0.57, 0.62, 3), timed<Small>(0.34, 0.34, 4), timed<Split>(0.68, 0.68, 2),
+                                      timed<Split64>(0.62, 0.68, 2)};
 
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
   switch (id) {

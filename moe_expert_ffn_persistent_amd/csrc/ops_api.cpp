@@ -36,10 +36,11 @@ double expected_blocks(double rows, int L, int tm) {
 // its share of the tiles one after the other, `stages` stages and a fixed cost
 // each. The stage times are the tile's when its compute unit works alone (a)
 // and when all do (b: clock and memory are shared then); with two workgroups on
-// a compute unit b is a stage of one of the two. Fitted to 114 bf16 and 38 e4m3
-// calls of 1 to 16384 rows, 1 to 32 experts and 1024 to 7168 features, each
-// timed with every tile: the tile chosen is within 2% of the best one in the
-// mean, and within 30% at worst (where two tiles' rounds end differently).
+// a compute unit b is a stage of one of the two. Fitted to 198 bf16 and 66 e4m3
+// calls of 1 to 16384 rows, 1 to 32 experts and 600 to 7168 features, each
+// timed with every tile: the tile chosen took 1.5% longer than the best one in
+// the mean, 26% at worst (calls of a few rows to many experts, and where two
+// tiles' last rounds are filled differently).
 double predicted(const GemmTile& t, double tiles, double stages) {
   const double q = std::max(1.0, std::ceil(tiles / kCus - 0.02));
   const double s = t.a + (t.b - t.a) * std::min(1.0, tiles / kCus);

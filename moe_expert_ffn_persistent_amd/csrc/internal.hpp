@@ -146,7 +146,7 @@ struct QuantArgs {
   float* scales;
   long long rows, ld_x, ld_codes, bs_x, bs_codes;
   int batch, cols, L;
-  bool vec;
+  bool vec, vec16;             // rows of x 16-byte, of codes 8-byte and 16-byte aligned
 };
 hipError_t launch_quantize(const QuantArgs& a, int block_rows, bool fp32, hipStream_t s);
 

@@ -249,6 +249,7 @@ int32_t moe_quantize_fp8(const moe_quantize_params* p, const void* x, const int3
   a.L = p->num_experts;
   a.vec = aligned(x, 16) && aligned(codes, 8) && (a.ld_x * xe) % 16 == 0 && (a.bs_x * xe) % 16 == 0 &&
           a.ld_codes % 8 == 0 && a.bs_codes % 8 == 0;
+  a.vec16 = a.vec && aligned(codes, 16) && a.ld_codes % 16 == 0 && a.bs_codes % 16 == 0;
   return done(launch_quantize(a, p->block_rows, fp32, (hipStream_t)stream));
 }
 

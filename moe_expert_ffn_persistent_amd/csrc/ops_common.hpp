@@ -158,31 +158,30 @@ __device__ __forceinline__ float block_scale(uint32_t amax) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
 
-// The e4m3 codes of fp32(x[i] / scale), ties to even, exactly as a correctly
-// rounded division gives them, at the cost of a multiplication: x * (1/scale)
-// is within two units in the last place of the quotient, so the code can only
-// differ where that lies as near to a border between two codes (a tie: in the
-// normal range the 20 bits below the code's three mantissa bits are 0x80000);
-// those lanes, values in the code's subnormal range and scales whose reciprocal
-// is not a normal number divide. For normal data that is a few values in 10^4.
+// The e4m3 codes of fp32(x[i] / scale), ties to even, where the quotient is
+// correctly rounded: with inv = 1/scale correctly rounded, q = x inv is off by
+// less than 1.5 units in the last place, one correction q + inv (x - q scale)
+// with fused multiply-adds brings it within one, and a second one then rounds
+// correctly (Markstein's theorem). Without them codes differ: bf16 values
+// over an amax of 8 bits land exactly on the border between two codes once in
+// a few hundred. Scales so small that the residual's last bit (2^-47 of x)
+// would fall below the smallest fp32 number, or whose reciprocal does, divide.
 __device__ __forceinline__ uint2 quant8(const float (&x)[8], float scale) {
   const float inv = 1.f / scale;
   float y[8];
-  bool near = !(scale > 1e-37f && scale < 1e37f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     y[i] = x[i] * inv;
-    const uint32_t b = abs_bits(y[i]);
-    near |= ((b - (0x80000u - 4u)) & 0xfffffu) <= 8u;
-    near |= b - 1u < 0x3c800000u - 1u;   // 0 < |y| < 2^-6
+    y[i] = __builtin_fmaf(__builtin_fmaf(-y[i], scale, x[i]), inv, y[i]);
+    y[i] = __builtin_fmaf(__builtin_fmaf(-y[i], scale, x[i]), inv, y[i]);
   }
-  if (near) {
+  if (!(scale > 1e-26f && scale < 1e37f)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = x[i] / scale;
   }
   const bool finite = abs_bits(scale) < 0x7f800000u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -448.f), 448.f);
+  for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(y[i], -448.f, 448.f);
   uint2 q{pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7])};
   if (!finite) q = uint2{0x7f7f7f7fu, 0x7f7f7f7fu};
   return q;
@@ -198,12 +197,17 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, bool vec, uint2 q
   }
 }
 
-// Integer maximum over the 16 lanes of a row of lanes (quantisation: a lane
-// holds 8 of a block's 128 columns).
+// Integer maximum over 8 or 16 neighbouring lanes, all active (quantisation: a
+// lane holds 16 or 8 of a block's 128 columns): quad permutations and mirrors of
+// the lane row, no LDS.
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, true));    // lane ^ 1
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true));    // lane ^ 2
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));  // 7 - lane
+}
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d, 64));
-  return v;
+  v = max8(v);
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));  // 15 - lane
 }
 
 }  // namespace moe

@@ -36,34 +36,66 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_k(const RowsArgs a) {
 }
 
 // y[n] = sum of the token's rows, ascending slots, fp32. A workgroup of four
-// wavefronts takes a token, a lane eight columns at a time; the slots' row
-// indices are uniform (scalar loads), so slots of other GPUs cost nothing.
+// wavefronts takes a token. A wavefront finds the slots that are local with one
+// load and a ballot, so slots of other GPUs cost nothing, and a lane has eight
+// columns of up to four pieces of the row in flight, of the next slot before
+// this one's are added: 160 us with one piece and one slot at a time, 90 us
+// so (16384 tokens x 7168, 8 slots of which one in the mean is local: 470 MB).
 template <bool BF16>
 __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool vec) {
-  const int n = blockIdx.x;
-  const int32_t* idx = a.index + (size_t)n * a.k;
+  constexpr int U = 4;
+  const int n = blockIdx.x, lane = threadIdx.x & 63;
+  const int idx = lane < a.k ? a.index[(size_t)n * a.k + lane] : -1;
+  const uint64_t local = __ballot(idx >= 0 && idx < a.rows);
   char* yrow = static_cast<char*>(a.out) + (size_t)n * a.ld_out;
-  for (int c = threadIdx.x * 8; c < a.hidden; c += 256 * 8) {
-    const int m = min(8, a.hidden - c);
-    const bool v = vec && m == 8;
-    float s[8] = {};
-    for (int j = 0; j < a.k; ++j) {
-      const int r = uni(idx[j]);
-      if (r < 0 || r >= a.rows) continue;
-      float x[8];
-      load8(reinterpret_cast<const __bf16*>(static_cast<const char*>(a.in) + (size_t)r * a.ld_in) + c, m, v, x);
+  for (int c0 = threadIdx.x * 8; c0 < a.hidden; c0 += U * 2048) {
+    auto load = [&](int slot, uint4 (&v)[U]) {
+      const int r = __builtin_amdgcn_readlane(idx, slot);
+      const __bf16* row = reinterpret_cast<const __bf16*>(static_cast<const char*>(a.in) + (size_t)r * a.ld_in);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] += x[i];
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * 2048, m = a.hidden - c;
+        if (vec && m >= 8) {
+          v[u] = *reinterpret_cast<const uint4*>(row + c);
+        } else {
+          float x[8];
+          load8(row + c, m, false, x);
+          v[u] = pack8(x);   // exact: they are bf16
+        }
+      }
+    };
+    float s[U][8] = {};
+    uint64_t left = local;
+    uint4 v[2][U];
+    if (left) load(__builtin_ctzll(left), v[0]);
+    while (left) {
+      left &= left - 1;
+      if (left) load(__builtin_ctzll(left), v[1]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[8];
+        unpack8(v[0][u], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[u][i] += x[i];
+        v[0][u] = v[1][u];
+      }
     }
-    if constexpr (BF16) {
-      store8(reinterpret_cast<__bf16*>(yrow) + c, m, v, s);
-    } else {
-      float* y = reinterpret_cast<float*>(yrow) + c;
-      if (v) {
-        reinterpret_cast<float4*>(y)[0] = float4{s[0], s[1], s[2], s[3]};
-        reinterpret_cast<float4*>(y)[1] = float4{s[4], s[5], s[6], s[7]};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * 2048, m = min(8, a.hidden - c);
+      const bool whole = vec && m == 8;
+      if constexpr (BF16) {
+        if (m > 0) store8(reinterpret_cast<__bf16*>(yrow) + c, m, whole, s[u]);
       } else {
-        for (int i = 0; i < m; ++i) y[i] = s[i];
+        float* y = reinterpret_cast<float*>(yrow) + c;
+        if (whole) {
+          reinterpret_cast<float4*>(y)[0] = float4{s[u][0], s[u][1], s[u][2], s[u][3]};
+          reinterpret_cast<float4*>(y)[1] = float4{s[u][4], s[u][5], s[u][6], s[u][7]};
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < m) y[i] = s[u][i];
+        }
       }
     }
   }

@@ -423,12 +423,13 @@ using Large = CfgQ<256, 256, 2, 4, 2, 4, 1>;
 using Wide = CfgQ<192, 256, 2, 4, 2, 4, 1>;
 using Medium = CfgQ<128, 256, 2, 4, 3, 4, 1>;
 using Square = CfgQ<128, 128, 2, 2, 2, 4, 2>;
+using Deep = CfgQ<128, 128, 2, 4, 4, 4, 1>;   // for calls that give no compute unit a second tile
 using Small = CfgQ<64, 128, 1, 4, 3, 4, 2>;
 using Split = CfgQ<32, 32, 1, 1, 2, 4, 1, 8>;
 using Split64 = CfgQ<32, 64, 1, 1, 3, 4, 1, 4>;
 
 template <class C>
-constexpr GemmTile timed(double a, double b, double o) { return GemmTile{C::TM, C::TN, C::OCC, C::KW, a, b, o}; }
+constexpr GemmTile timed(double a, double c, double b, double o) { return GemmTile{C::TM, C::TN, C::OCC, C::KW, a, c, b, o}; }
 
 template <class C>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
@@ -443,9 +444,10 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
 
 }  // namespace
 
-const GemmTile kFp8GemmTileTable[] = {timed<Large>(0.74, 1.63, 6),  timed<Wide>(0.68, 1.37, 5),  timed<Medium>(0.57, 0.97, 5),
-                                      timed<Square>(0.57, 0.62, 3), timed<Small>(0.34, 0.34, 4), timed<Split>(0.68, 0.68, 2),
-                                      timed<Split64>(0.62, 0.68, 2)};
+const GemmTile kFp8GemmTileTable[] = {
+    timed<Large>(0.73, 1.67, 1.67, 6),  timed<Wide>(0.68, 1.36, 1.36, 5),  timed<Medium>(0.60, 0.96, 0.96, 5),
+    timed<Square>(0.37, 0.79, 0.54, 4), timed<Small>(0.28, 0.42, 0.32, 4), timed<Split>(0.68, 0.68, 0.68, 2),
+    timed<Split64>(0.60, 0.68, 0.68, 2), timed<Deep>(0.37, 0.56, 0.56, 5)};
 
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
   switch (id) {
@@ -456,6 +458,7 @@ hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
     case 5: return launch<Small>(a, s);
     case 6: return launch<Split>(a, s);
     case 7: return launch<Split64>(a, s);
+    case 8: return launch<Deep>(a, s);
   }
   return hipErrorInvalidValue;
 }

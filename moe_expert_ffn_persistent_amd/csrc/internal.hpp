@@ -165,10 +165,10 @@ struct GemmArgs {
 constexpr int kCus = 256;   // compute units, places for a persistent workgroup
 hipError_t launch_gemm_any(const GemmArgs& a, bool fp8, hipStream_t s);
 // tiles 1 .. kBf16GemmTiles (kFp8GemmTiles) of the 16-byte kernels
-constexpr int kBf16GemmTiles = 7, kFp8GemmTiles = 7;
+constexpr int kBf16GemmTiles = 8, kFp8GemmTiles = 8;
 struct GemmTile {
   int tm, tn, occ, kw;   // rows, columns, workgroups per compute unit, wavefronts that split the sum
-  double a, b, o;        // us: a stage alone, a stage with all compute units at work, a tile's ends
+  double a, c, b, o;     // us: a stage alone, with a workgroup on every compute unit, with occ of them, a tile's ends
 };
 extern const GemmTile kBf16GemmTileTable[], kWgradTiles[], kFp8GemmTileTable[];   // id - 1
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s);

@@ -34,19 +34,19 @@ double expected_blocks(double rows, int L, int tm) {
 
 // Predicted microseconds of a call in tile t: every compute unit works through
 // its share of the tiles one after the other, `stages` stages and a fixed cost
-// each. The stage times are the tile's when its compute unit works alone (a)
-// and when all do (b: clock and memory are shared then); with two workgroups on
-// a compute unit b is a stage of one of the two. Fitted to 198 bf16 and 66 e4m3
-// calls of 1 to 16384 rows, 1 to 32 experts and 600 to 7168 features, each
-// timed with every tile: the tile chosen took 1.5% longer than the best one in
-// the mean, 26% at worst (calls of a few rows to many experts, and where two
-// tiles' last rounds are filled differently).
+// each. A stage's time grows from the tile's when few compute units work (a) to
+// that with all of them at work (c: clock, L2 and memory are shared then); with
+// two workgroups on a compute unit a stage of one of them takes 2 b.
+// Fitted to 198 bf16 and 66 e4m3 calls of 1 to 16384 rows, 1 to 32 experts and
+// 600 to 7168 features, each timed with every tile: the tile chosen took 1.5%
+// longer than the best one in the mean, 25% at worst (a few rows to many
+// experts, and where two tiles' last rounds are filled differently).
 double predicted(const GemmTile& t, double tiles, double stages) {
   const double q = std::max(1.0, std::ceil(tiles / kCus - 0.02));
-  const double s = t.a + (t.b - t.a) * std::min(1.0, tiles / kCus);
-  if (t.occ == 1) return q * (stages * s + t.o);
+  const double one = t.a + (t.c - t.a) * std::min(1.0, tiles / kCus);
+  if (t.occ == 1) return q * (stages * one + t.o);
   const double pairs = std::floor(q / 2);
-  return pairs * (stages * std::max(t.a, 2 * t.b) + t.o) + (q - 2 * pairs) * (stages * t.a + t.o);
+  return pairs * (stages * std::max(one, 2 * t.b) + t.o) + (q - 2 * pairs) * (stages * one + t.o);
 }
 
 int choose(const GemmTile* tiles, int n, const GemmArgs& a, int bk) {

@@ -235,6 +235,17 @@ def test_grouped_keeps_other_experts_clean(op, value):
     assert_close(got[keep], ref[keep], BF, mag[keep], terms, "clean")
 
 
+@pytest.mark.parametrize("tile", [0, 1, 6])
+def test_grouped_subnormals_and_overflow(tile):
+    # subnormal bf16 operands count in full, and a sum past bf16's largest value
+    # is an infinity of its sign
+    x = torch.full((4, 64), 2.0 ** -130, dtype=BF)
+    w = torch.full((1, 8, 64), 2.0 ** 100, dtype=BF)
+    x[1], x[2] = 2.0 ** 60, -(2.0 ** 60)
+    got = moe.grouped_matmul(up(x), up(w), up(offsets([4])), tile=tile).cpu()
+    assert (got[0] == 2.0 ** -24).all() and (got[1] == float("inf")).all() and (got[2] == -float("inf")).all()
+
+
 def test_grouped_allocates_its_output_and_takes_a_stream():
     g = gen(2)
     x, w, off = normal(g, 60, 128), normal(g, 2, 64, 128), offsets([20, 40])

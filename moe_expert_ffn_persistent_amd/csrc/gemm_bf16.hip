@@ -384,7 +384,7 @@ struct TileG {
           const uint4 v = *reinterpret_cast<const uint4*>(mine + stage_off<ROWB>(r, c * 16));
           char* p = static_cast<char*>(out) + ((long long)i * ld + col) * OB;
           if constexpr (!ADD) {
-            __builtin_nontemporal_store(__builtin_bit_cast(i32x4, v), reinterpret_cast<i32x4*>(p));
+            *reinterpret_cast<uint4*>(p) = v;
           } else {
             const float4 s = __builtin_bit_cast(float4, v);
             if constexpr (BF16) {

@@ -329,7 +329,8 @@ struct TileQ {
       for (int r0 = 0; r0 < 16; r0 += RPP) {
         const int r = r0 + lane / NCH, i = i0 + ((j >> 1) * C::WT + wt) * 32 + (j & 1) * 16 + r;
         if (WHOLE || (r < 16 && i < ni && col < nj))
-          __builtin_nontemporal_store(*reinterpret_cast<const i32x4*>(mine + stage_off<ROWB>(r, c * 16)), reinterpret_cast<i32x4*>(static_cast<char*>(out) + ((long long)i * ld + col) * EB));
+          *reinterpret_cast<uint4*>(static_cast<char*>(out) + ((long long)i * ld + col) * EB) =
+              *reinterpret_cast<const uint4*>(mine + stage_off<ROWB>(r, c * 16));
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }

@@ -347,11 +347,11 @@ struct TileG {
 
   // Output rows i0 .. of ni, columns j0 .. of nj: every wavefront stages its 32
   // rows by FT columns in its own LDS and writes whole pieces of 16 bytes, FT
-  // columns of a row together. (Plain stores: past the caches, weight gradients
-  // of 268 MB were 9% faster, but rows that are no whole 128-byte lines took
-  // twice as long, 24 x 3344 x 936 bf16 68 against 32 us.) `lds`: staging, behind the first ring slot, which
-  // the next tile's copies may be filling. ADD: the sum is added to what is there, in fp32,
-  // before the one rounding.
+  // columns of a row together. `lds`: staging, behind the first ring slot, which
+  // the next tile's copies may be filling. ADD: the sum is added to what is
+  // there, in fp32, before the one rounding. (Plain stores: past the caches,
+  // weight gradients of 268 MB were 9% faster, but rows that are no whole
+  // 128-byte lines took twice as long, 24 x 3344 x 936 bf16 68 against 32 us.)
   template <bool BF16, bool ADD>
   __device__ __forceinline__ void store(char* lds, void* out, long long ld, int i0, int ni, int j0, int nj, int wf,
                                         int wt) {

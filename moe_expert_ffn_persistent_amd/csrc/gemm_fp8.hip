@@ -128,9 +128,9 @@ struct TileQ {
   }
 
   // One K block; sw: its weight scale (KW > 1; else it lies behind the row
-  // scales). The products of the stage's last two
-  // blocks are added during the first two MFMAs of the next one.
-  // Only the first NTP of the wavefront's 32-row blocks are multiplied.
+  // scales). The products of the stage's last two blocks are added during the
+  // first two MFMAs of the next one. Only the first NTP of the wavefront's
+  // 32-row blocks are multiplied.
   template <bool COPY, int NTP>
   __device__ __forceinline__ void compute(const char* stage, int wf, int wt, float sw, int kt_next, uint32_t slot) {
     constexpr int TB = 2 * NTP, NB = C::FB * TB, NI = C::copies(NTP);
@@ -268,7 +268,9 @@ struct TileQ {
     mainloop<C::TB / 2>(lds, K, ws, wf, wt, kw, stores);
   }
 
-  // see the bf16 kernel
+  // The first stage's copies have landed. They were issued before the previous
+  // tile's `stores` stores (0: any number), and memory operations are counted
+  // back in order: the stores may stay in flight.
   __device__ __forceinline__ static void wait_first(int stores) {
     static_assert(STORES<false> <= 63, "vmcnt range");
     if (stores == STORES<true>) vm_wait<STORES<true>>();

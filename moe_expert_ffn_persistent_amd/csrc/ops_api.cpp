@@ -12,10 +12,21 @@ namespace {
 
 constexpr long long kMaxRows = 1ll << 28;
 constexpr int kMaxCols = 1 << 20;
+// elements between rows or matrices: the checks below multiply by up to
+// kMaxRows, the kernels' byte offsets stay inside 64 bits
+constexpr long long kMaxStride = 1ll << 32, kMaxMatrix = 1ll << 52;
 
 int32_t done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// a row stride of rows of `cols` elements
+bool stride_ok(long long ld, long long cols) { return ld >= cols && ld <= kMaxStride; }
+
+// the distance between `count` matrices of `rows` such rows
+bool matrix_stride_ok(long long stride, long long count, long long rows, long long ld, long long cols) {
+  return count <= 1 || (stride >= (rows - 1) * ld + cols && stride <= kMaxMatrix);
+}
 
 bool dtype_ok(int32_t d) { return d == MOE_Y_FP32 || d == MOE_Y_BF16; }
 
@@ -76,8 +87,8 @@ int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t
                           const int32_t* row_offset, void* out, void* stream) {
   if (!p || p->tokens < 0 || p->rows < 0 || p->rows > kMaxRows || p->top_k < 1 || p->top_k > 16 || p->hidden < 1 ||
       p->hidden > kMaxCols || (p->elem_bytes != 1 && p->elem_bytes != 2 && p->elem_bytes != 4) ||
-      p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->ld_tokens < p->hidden ||
-      p->ld_rows < p->hidden || p->tokens * p->top_k > (1ll << 30))
+      p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || !stride_ok(p->ld_tokens, p->hidden) ||
+      !stride_ok(p->ld_rows, p->hidden) || p->tokens > (1ll << 30) / p->top_k)
     return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
   if (!row_pair || !row_offset || !out || (p->tokens && !x)) return MOE_ERR_INVALID_ARG;
@@ -100,8 +111,8 @@ int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t
 
 int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row, void* y, void* stream) {
   if (!p || p->tokens < 0 || p->rows < 0 || p->rows > kMaxRows || p->top_k < 1 || p->top_k > 16 || p->hidden < 1 ||
-      p->hidden > kMaxCols || p->elem_bytes != 2 || !dtype_ok(p->out_dtype) || p->ld_tokens < p->hidden ||
-      p->ld_rows < p->hidden || p->tokens > (1ll << 23))
+      p->hidden > kMaxCols || p->elem_bytes != 2 || !dtype_ok(p->out_dtype) || !stride_ok(p->ld_tokens, p->hidden) ||
+      !stride_ok(p->ld_rows, p->hidden) || p->tokens > (1ll << 23))
     return MOE_ERR_INVALID_ARG;
   if (p->tokens == 0) return MOE_OK;
   if (!pair_row || !y || (p->rows && !in)) return MOE_ERR_INVALID_ARG;
@@ -125,8 +136,9 @@ int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offse
                            void* stream) {
   if (!p || p->op < MOE_GROUPED_FORWARD || p->op > MOE_GROUPED_WGRAD || p->num_experts < 1 ||
       p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows || p->expected_rows < 0 ||
-      p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || p->ld_x < p->k || p->ld_w < p->k ||
-      p->ld_y < p->n || p->expert_stride_w < (p->num_experts > 1 ? (p->n - 1) * p->ld_w + p->k : 0) ||
+      p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || !stride_ok(p->ld_x, p->k) ||
+      !stride_ok(p->ld_w, p->k) || !stride_ok(p->ld_y, p->n) ||
+      !matrix_stride_ok(p->expert_stride_w, p->num_experts, p->n, p->ld_w, p->k) ||
       !dtype_ok(p->out_dtype) || p->tile < 0)
     return MOE_ERR_INVALID_ARG;
   const bool wgrad = p->op == MOE_GROUPED_WGRAD, fwd = p->op == MOE_GROUPED_FORWARD;
@@ -166,12 +178,12 @@ int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offse
 
 int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_weight, const int32_t* row_offset,
                    void* h, float* h_scales, void* stream) {
-  if (!p || p->rows < 0 || p->rows > kMaxRows || p->inter < 1 || p->inter > kMaxCols || p->ld_a < 2ll * p->inter ||
-      p->ld_h < p->inter || (p->out_format != MOE_SWIGLU_BF16 && p->out_format != MOE_SWIGLU_FP8) ||
+  if (!p || p->rows < 0 || p->rows > kMaxRows || p->inter < 1 || p->inter > kMaxCols ||
+      !stride_ok(p->ld_a, 2ll * p->inter) || !stride_ok(p->ld_h, p->inter) || (p->out_format != MOE_SWIGLU_BF16 && p->out_format != MOE_SWIGLU_FP8) ||
       (row_offset && (p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS)))
     return MOE_ERR_INVALID_ARG;
   const bool fp8 = p->out_format == MOE_SWIGLU_FP8;
-  if (fp8 && p->ld_scales < (p->inter + 127) / 128) return MOE_ERR_INVALID_ARG;
+  if (fp8 && !stride_ok(p->ld_scales, (p->inter + 127) / 128)) return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
   if (!a_ || !h || (fp8 && !h_scales) || !aligned(a_, 2) || (!fp8 && !aligned(h, 2))) return MOE_ERR_INVALID_ARG;
   SwigluArgs a{};
@@ -192,8 +204,8 @@ int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_
 
 int32_t moe_swiglu_backward(const moe_swiglu_params* p, const void* a_, const void* dh, const float* row_weight,
                             const int32_t* row_offset, void* da, float* drow_weight, void* stream) {
-  if (!p || p->rows < 0 || p->rows > kMaxRows || p->inter < 1 || p->inter > kMaxCols || p->ld_a < 2ll * p->inter ||
-      p->ld_da < 2ll * p->inter || p->ld_h < p->inter ||
+  if (!p || p->rows < 0 || p->rows > kMaxRows || p->inter < 1 || p->inter > kMaxCols ||
+      !stride_ok(p->ld_a, 2ll * p->inter) || !stride_ok(p->ld_da, 2ll * p->inter) || !stride_ok(p->ld_h, p->inter) ||
       (row_offset && (p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS)))
     return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
@@ -220,14 +232,14 @@ int32_t moe_quantize_fp8(const moe_quantize_params* p, const void* x, const int3
                          float* scales, void* stream) {
   if (!p || p->rows < 0 || p->rows > kMaxRows || p->batch < 1 || p->batch > 65535 || p->cols < 1 ||
       p->cols > kMaxCols || (p->block_rows != 1 && p->block_rows != 128) || !dtype_ok(p->in_dtype) ||
-      p->ld_x < p->cols || p->ld_codes < p->cols)
+      !stride_ok(p->ld_x, p->cols) || !stride_ok(p->ld_codes, p->cols))
     return MOE_ERR_INVALID_ARG;
   if (row_offset && (p->batch != 1 || p->block_rows != 1 || p->num_experts < 1 ||
                      p->num_experts > MOE_MAX_LOCAL_EXPERTS))
     return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
-  if (p->batch > 1 && (p->batch_stride_x < (p->rows - 1) * p->ld_x + p->cols ||
-                       p->batch_stride_codes < (p->rows - 1) * p->ld_codes + p->cols))
+  if (!matrix_stride_ok(p->batch_stride_x, p->batch, p->rows, p->ld_x, p->cols) ||
+      !matrix_stride_ok(p->batch_stride_codes, p->batch, p->rows, p->ld_codes, p->cols))
     return MOE_ERR_INVALID_ARG;
   if (p->block_rows == 128 && ((p->rows + 127) / 128) * ((p->cols + 127) / 128) > (1ll << 23))
     return MOE_ERR_UNSUPPORTED;
@@ -256,9 +268,9 @@ int32_t moe_quantize_fp8(const moe_quantize_params* p, const void* x, const int3
 int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const void* x, const float* x_scales,
                        const void* w, const float* w_scales, void* y, void* stream) {
   if (!p || p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows ||
-      p->expected_rows < 0 || p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || p->ld_x < p->k ||
-      p->ld_w < p->k || p->ld_y < p->n || p->ld_xs < (p->k + 127) / 128 ||
-      p->expert_stride_w < (p->num_experts > 1 ? (p->n - 1) * p->ld_w + p->k : 0) || !dtype_ok(p->out_dtype) || p->tile < 0)
+      p->expected_rows < 0 || p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || !stride_ok(p->ld_x, p->k) ||
+      !stride_ok(p->ld_w, p->k) || !stride_ok(p->ld_y, p->n) || !stride_ok(p->ld_xs, (p->k + 127) / 128) ||
+      !matrix_stride_ok(p->expert_stride_w, p->num_experts, p->n, p->ld_w, p->k) || !dtype_ok(p->out_dtype) || p->tile < 0)
     return MOE_ERR_INVALID_ARG;
   if (!row_offset && p->num_experts != 1) return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;

@@ -78,9 +78,10 @@ struct GroupScan {
 // runs of consecutive tiles are dealt to the XCDs in turn: tiles that run
 // together on one XCD, and share operand rows in its L2, are neighbours. A run
 // is 32 tiles (an XCD's compute units), fewer when that would leave XCDs
-// without any: 64 tiles on two XCDs ran up to 2.1 times as long as on all.
+// without any: 64 tiles on two XCDs ran up to 2.1 times as long as on all. With
+// no tiles (no expert has rows) the run is one, and every b lies past the end.
 __device__ __forceinline__ int xcd_tile(int b, int n) {
-  const int run = min(32, (n + 7) >> 3);
+  const int run = max(1, min(32, (n + 7) >> 3));
   const int x = b & 7, i = b >> 3, q = i / run;
   return (q * 8 + x) * run + i - q * run;
 }

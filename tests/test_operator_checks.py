@@ -325,3 +325,33 @@ def test_c_fp8_refuses_tiles_it_does_not_have():
     assert _call("moe_fp8_matmul", _lib.MoeFp8Params(*base.values()), None, 16, 16, 16, 16, 16) == _lib.MOE_ERR_UNSUPPORTED
     base.update(tile=1)
     assert _call("moe_fp8_matmul", _lib.MoeFp8Params(*base.values()), None, 24, 16, 16, 16, 16) == _lib.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("name, kw", [
+    ("moe_dispatch_rows", dict(tokens=1 << 62)), ("moe_dispatch_rows", dict(ld_tokens=1 << 61)),
+    ("moe_dispatch_rows", dict(ld_rows=(1 << 32) + 1)), ("moe_combine_rows", dict(ld_rows=1 << 62)),
+    ("moe_grouped_matmul", dict(ld_w=1 << 62)), ("moe_grouped_matmul", dict(ld_x=1 << 33)),
+    ("moe_grouped_matmul", dict(expert_stride_w=1 << 60)), ("moe_grouped_matmul", dict(rows=(1 << 28) + 1)),
+    ("moe_swiglu", dict(ld_a=1 << 62)), ("moe_swiglu_backward", dict(ld_da=1 << 62)),
+    ("moe_quantize_fp8", dict(ld_x=1 << 62)), ("moe_quantize_fp8", dict(batch_stride_codes=1 << 62)),
+    ("moe_fp8_matmul", dict(ld_xs=1 << 62)), ("moe_fp8_matmul", dict(ld_w=1 << 62))])
+def test_c_refuses_sizes_that_would_overflow(name, kw):
+    rows = dict(tokens=4, rows=8, top_k=2, hidden=8, elem_bytes=2, num_experts=2, out_dtype=1, ld_tokens=8, ld_rows=8)
+    swiglu = dict(rows=4, inter=8, num_experts=2, out_format=0, ld_a=16, ld_h=8, ld_scales=1, ld_da=16)
+    struct, base, ptrs = {
+        "moe_dispatch_rows": (_lib.MoeRowsParams, rows, 4), "moe_combine_rows": (_lib.MoeRowsParams, rows, 3),
+        "moe_grouped_matmul": (_lib.MoeGroupedParams, dict(
+            op=0, num_experts=2, rows=4, expected_rows=0, n=8, k=8, ld_x=8, ld_w=8, ld_y=8, expert_stride_w=64,
+            out_dtype=1, accumulate=0, tile=0), 4),
+        "moe_swiglu": (_lib.MoeSwigluParams, swiglu, 5), "moe_swiglu_backward": (_lib.MoeSwigluParams, swiglu, 6),
+        "moe_quantize_fp8": (_lib.MoeQuantizeParams, dict(
+            rows=4, batch=2, cols=8, block_rows=1, in_dtype=1, num_experts=0, ld_x=8, ld_codes=8, batch_stride_x=32,
+            batch_stride_codes=32), 4),
+        "moe_fp8_matmul": (_lib.MoeFp8Params, dict(
+            num_experts=2, rows=4, expected_rows=0, n=8, k=256, ld_x=256, ld_xs=2, ld_w=256, ld_y=8,
+            expert_stride_w=2048, out_dtype=1, tile=0), 6)}[name]
+    params = struct(*dict(base, **kw).values())
+    args = [16] * ptrs
+    if name == "moe_quantize_fp8":
+        args[1] = None
+    assert _call(name, params, *args) == _lib.MOE_ERR_INVALID_ARG

@@ -65,7 +65,7 @@ def _matrix(t, what, dtypes, dims=2):
     st = t.stride()
     if cols > 1 and st[-1] != 1:
         raise ValueError(f"{what}: rows must be contiguous (last stride 1, got {st[-1]})")
-    ld = st[-2] if rows > 1 else max(st[-2], cols)
+    ld = st[-2] if rows > 1 else cols
     if ld < cols:
         raise ValueError(f"{what}: rows overlap (row stride {ld} under {cols} columns)")
     return ld
@@ -83,6 +83,11 @@ def _vector(t, what, n, dtype):
     """A contiguous tensor of ``n`` elements of ``dtype``, any shape."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{what}: need a contiguous {dtype} tensor of {n} elements")
+
+
+def _indices(t, what):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{what}: need a contiguous int32 tensor")
 
 
 def _offsets(t):
@@ -112,6 +117,7 @@ def _empty(shape, dtype, device, stream):
     """An output for work on ``stream``, allocated for that stream."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    _check_stream(stream, device.index)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
@@ -150,7 +156,8 @@ def _plan(key, check, *args):
 
 def _no_grad(*tensors):
     """Raise where an input requires grad and grad mode is on: of the checks,
-    the one that shapes and types do not settle."""
+    the one that shapes and types do not settle (after _plan, which has made
+    sure that these are tensors)."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
@@ -160,9 +167,20 @@ def _no_grad(*tensors):
 _ENTRY: dict = {}
 
 
+def _check_stream(stream, device):
+    """``stream`` is one of the tensors' device (an index)."""
+    at = getattr(stream, "device_index", None)
+    if at is None:
+        raise ValueError(f"stream: need a torch.cuda.Stream, got {type(stream).__name__}")
+    if at != device:
+        raise ValueError(f"stream: of device {at}, the tensors are on device {device}")
+
+
 def _launch(name, device, params, ptrs, stream):
     """One C entry point on the tensors' device (an index) and its current stream,
     or the given one."""
+    if stream is not None:
+        _check_stream(stream, device)
     fn = _ENTRY.get(name)
     if fn is None:
         fn = _ENTRY[name] = getattr(_lib.load(), name)
@@ -189,8 +207,7 @@ def check_dispatch_inputs(x, row_pair, row_offset, top_k, out):
     L = _offsets(row_offset)
     if not 1 <= top_k <= 16:
         raise ValueError(f"top_k: need 1 to 16, got {top_k}")
-    if not isinstance(row_pair, torch.Tensor) or row_pair.dtype != torch.int32 or not row_pair.is_contiguous():
-        raise ValueError("row_pair: need a contiguous int32 tensor")
+    _indices(row_pair, "row_pair")
     ldo = _matrix(out, "out", (x.dtype,))
     if out.shape[1] != H:
         raise ValueError(f"out: rows of {out.shape[1]} elements, x has {H}")
@@ -208,10 +225,11 @@ def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
     if out is None:
         _matrix(x, "x", tuple(_ROW_TYPES))
         _need_device(x.device)
+        _indices(row_pair, "row_pair")
         out = _empty((row_pair.numel(), x.shape[1]), x.dtype, x.device, stream)
-    _no_grad(x, out)
     p = _plan(("dispatch", _sig(x), _sig(row_pair), _sig(row_offset), top_k, _sig(out)), check_dispatch_inputs,
               x, row_pair, row_offset, top_k, out)
+    _no_grad(x, out)
     _launch("moe_dispatch_rows", x.get_device(), p,
             (x.data_ptr(), row_pair.data_ptr(), row_offset.data_ptr(), out.data_ptr()), stream)
     return out
@@ -221,9 +239,9 @@ def check_combine_rows_inputs(rows, pair_row, top_k, out):
     ldr = _matrix(rows, "rows", (torch.bfloat16,))
     if not 1 <= top_k <= 16:
         raise ValueError(f"top_k: need 1 to 16, got {top_k}")
-    if (not isinstance(pair_row, torch.Tensor) or pair_row.dtype != torch.int32 or not pair_row.is_contiguous()
-            or pair_row.numel() % top_k):
-        raise ValueError("pair_row: need a contiguous int32 tensor of top_k entries a token")
+    _indices(pair_row, "pair_row")
+    if pair_row.numel() % top_k:
+        raise ValueError(f"pair_row: {pair_row.numel()} entries, need top_k ({top_k}) a token")
     N = pair_row.numel() // top_k
     ldo = _matrix(out, "out", tuple(_OUT))
     if tuple(out.shape) != (N, rows.shape[1]):
@@ -242,10 +260,11 @@ def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stre
         _need_device(rows.device)
         if out_dtype not in _OUT:
             raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
+        _indices(pair_row, "pair_row")
         out = _empty((pair_row.numel() // max(1, top_k), rows.shape[1]), out_dtype, rows.device, stream)
-    _no_grad(rows, out)
     p = _plan(("combine", _sig(rows), _sig(pair_row), top_k, _sig(out)), check_combine_rows_inputs,
               rows, pair_row, top_k, out)
+    _no_grad(rows, out)
     _launch("moe_combine_rows", rows.get_device(), p, (rows.data_ptr(), pair_row.data_ptr(), out.data_ptr()), stream)
     return out
 
@@ -272,9 +291,9 @@ def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate
 
 
 def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, tile, stream):
-    _no_grad(x, w, y)
     p = _plan((op, _sig(x), _sig(w), _sig(y), _sig(row_offset), expected_rows, accumulate, tile), check_grouped_inputs,
               op, x, w, y, row_offset, expected_rows, accumulate, tile)
+    _no_grad(x, w, y)
     _launch("moe_grouped_matmul", x.get_device(), p,
             (row_offset.data_ptr(), x.data_ptr(), w.data_ptr(), y.data_ptr()), stream)
 
@@ -372,9 +391,9 @@ def swiglu(gate_up, row_weight=None, row_offset=None, out=None, scales=None, out
             out = _empty((rows, I), out_dtype, gate_up.device, stream)
         if scales is None and out.dtype in _CODES:
             scales = _empty((rows, _blocks(I)), torch.float32, gate_up.device, stream)
-    _no_grad(gate_up, row_weight, out, scales)
     p = _plan(("swiglu", _sig(gate_up), _sig(row_weight), _sig(row_offset), _sig(out), _sig(scales)), check_swiglu_inputs,
               gate_up, row_weight, row_offset, out, scales)
+    _no_grad(gate_up, row_weight, out, scales)
     _launch("moe_swiglu", gate_up.get_device(), p,
             (gate_up.data_ptr(), _ptr(row_weight), _ptr(row_offset), out.data_ptr(), _ptr(scales)), stream)
     return out if scales is None else (out, scales)
@@ -406,9 +425,9 @@ def swiglu_backward(gate_up, dh, row_weight=None, row_offset=None, out=None, dro
             out = _empty((rows, 2 * I), torch.bfloat16, gate_up.device, stream)
         if drow_weight is None and row_weight is not None:
             drow_weight = _empty((rows,), torch.float32, gate_up.device, stream)
-    _no_grad(gate_up, dh, row_weight, out, drow_weight)
     p = _plan(("swiglu_backward", _sig(gate_up), _sig(dh), _sig(row_weight), _sig(row_offset), _sig(out), _sig(drow_weight)),
               check_swiglu_backward_inputs, gate_up, dh, row_weight, row_offset, out, drow_weight)
+    _no_grad(gate_up, dh, row_weight, out, drow_weight)
     _launch("moe_swiglu_backward", gate_up.get_device(), p,
             (gate_up.data_ptr(), dh.data_ptr(), _ptr(row_weight), _ptr(row_offset), out.data_ptr(),
              _ptr(drow_weight)), stream)
@@ -462,9 +481,9 @@ def quantize_fp8(x, block_rows=1, row_offset=None, out=None, scales=None, stream
             out = _empty(tuple(x.shape), torch.float8_e4m3fn, x.device, stream)
         if scales is None:
             scales = _empty(_scale_shape(x, block_rows), torch.float32, x.device, stream)
-    _no_grad(x, out, scales)
     p = _plan(("quantize", _sig(x), block_rows, _sig(row_offset), _sig(out), _sig(scales)), check_quantize_inputs,
               x, block_rows, row_offset, out, scales)
+    _no_grad(x, out, scales)
     if x.numel():
         _launch("moe_quantize_fp8", x.get_device(), p,
                 (x.data_ptr(), _ptr(row_offset), out.data_ptr(), scales.data_ptr()), stream)
@@ -509,13 +528,14 @@ def fp8_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=to
     ``expected_rows`` and ``tile`` as for grouped_matmul."""
     if out is None:
         _matrix(x, "x", _CODES)
+        _matrix(w, "w", _CODES, 2 if row_offset is None else 3)
         if out_dtype not in _OUT:
             raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
         _need_device(x.device)
         out = _empty((x.shape[0], w.shape[-2]), out_dtype, x.device, stream)
-    _no_grad(x_scales, w_scales, out)
     p = _plan(("fp8", _sig(x), _sig(x_scales), _sig(w), _sig(w_scales), _sig(row_offset), _sig(out), expected_rows, tile),
               check_fp8_inputs, x, x_scales, w, w_scales, row_offset, out, expected_rows, tile)
+    _no_grad(x, x_scales, w, w_scales, out)
     _launch("moe_fp8_matmul", x.get_device(), p,
             (_ptr(row_offset), x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), out.data_ptr()),
             stream)

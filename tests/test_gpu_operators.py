@@ -179,6 +179,14 @@ def test_grouped_every_tile(counts, k, n, op, tile, out_dtype):
     run_grouped(op, counts, k, n, out_dtype, seed=k + n, first=2, behind=4, pad=8, tile=tile)
 
 
+@pytest.mark.parametrize("pad", [0, 1], ids=["aligned", "odd"])
+@pytest.mark.parametrize("op", [FWD, DGRAD, WGRAD], ids=["forward", "dgrad", "wgrad"])
+def test_grouped_without_any_rows(op, pad):
+    # no expert has rows in buffers that hold some: rows stay, weight gradients are zeros
+    run_grouped(op, [0, 0, 0], 264 + pad, 328, BF, seed=7, first=3, behind=40)
+    run_grouped(op, [0], 264 + pad, 328, F32, seed=8)
+
+
 @pytest.mark.parametrize("op", [FWD, DGRAD, WGRAD], ids=["forward", "dgrad", "wgrad"])
 def test_grouped_most_experts(op):
     counts = torch.randint(0, 5, (256,), generator=gen(5)).tolist()

@@ -226,6 +226,41 @@ def test_host_tensors_are_refused():
         moe.fp8_matmul(z(R, 200, dtype=F8), z(R, 2, dtype=F32), z(130, 200, dtype=F8), z(2, 2, dtype=F32))
 
 
+def test_arguments_that_are_no_tensors_are_refused():
+    # also where the output is given, and nothing has to be allocated first
+    i32 = torch.zeros(8, dtype=torch.int32)
+    for call in (lambda: moe.dispatch_rows([1.0], i32, off(), 2, out=z(8, K)),
+                 lambda: moe.dispatch_rows(z(4, K), [0] * 8, off(), 2),
+                 lambda: moe.combine_rows(z(8, K), [0] * 8, 2),
+                 lambda: moe.combine_rows([1.0], i32, 2, out=z(4, K)),
+                 lambda: moe.grouped_matmul([1.0], z(L, N, K), off(), out=z(R, N)),
+                 lambda: moe.grouped_matmul_wgrad(z(R, N), z(R, K), [0, 1]),
+                 lambda: moe.swiglu([1.0], out=z(R, K)),
+                 lambda: moe.swiglu_backward([1.0], z(R, K), out=z(R, 2 * K)),
+                 lambda: moe.quantize_fp8([1.0], out=z(R, K, dtype=F8), scales=z(R, 1, dtype=F32)),
+                 lambda: moe.fp8_matmul(z(R, 200, dtype=F8), z(R, 2, dtype=F32), [1.0], z(2, 2, dtype=F32)),
+                 lambda: moe.fp8_matmul([1.0], z(R, 2, dtype=F32), z(N, 200, dtype=F8), z(1, 2, dtype=F32), out=z(R, N))):
+        with pytest.raises(ValueError):
+            call()
+
+
+class _Stream:
+    def __init__(self, device_index):
+        self.device_index = device_index
+
+
+def test_streams_of_another_device_are_refused():
+    ops._check_stream(_Stream(1), 1)
+    for stream in (_Stream(0), 7):
+        with pytest.raises(ValueError, match="stream"):
+            ops._check_stream(stream, 1)
+
+
+def test_single_rows_with_huge_strides_count_as_their_length():
+    x = torch.empty_strided((1, K), (1 << 40, 1), dtype=BF, device="meta")
+    assert ops._matrix(x, "x", (BF,)) == K
+
+
 # ---- the C entry points, with pointers that are never followed -------------------
 
 def _lib_or_skip():

@@ -503,8 +503,11 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
                                                : ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM;
   const long long tiles = nj * mi;
   if (tiles >= INT_MAX / 2) return launch_gemm_any(a, false, s);   // the kernel counts tiles in int
-  // a workgroup for each place on the GPU; a multiple of 8 keeps one on its XCD
-  const long long grid = std::min<long long>((tiles + 7) / 8 * 8, (long long)kCus * C::OCC);
+  // A workgroup for each place on the GPU; a multiple of 8 keeps one on its XCD.
+  // Past a tile for every compute unit all places get one, since the tile order
+  // is dealt in runs: with a workgroup for each of 288 to 320 tiles, places for
+  // the last ones stayed empty (2048 x 4096 x 2304 in 128 x 128: 84 us, now 52).
+  const long long grid = tiles > kCus ? kCus * C::OCC : (tiles + 7) / 8 * 8;
   moe_gemm_bf16<C, OP><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
   return hipGetLastError();
 }

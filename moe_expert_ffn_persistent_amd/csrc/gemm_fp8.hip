@@ -439,7 +439,7 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
   const long long mi = a.row_offset ? ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM : (a.rows + C::TM - 1) / C::TM;
   const long long tiles = nj * mi;
   if (tiles >= INT_MAX / 2) return launch_gemm_any(a, true, s);   // the kernel counts tiles in int
-  const long long grid = std::min<long long>((tiles + 7) / 8 * 8, (long long)kCus * C::OCC);
+  const long long grid = tiles > kCus ? kCus * C::OCC : (tiles + 7) / 8 * 8;
   moe_gemm_fp8<C><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
   return hipGetLastError();
 }

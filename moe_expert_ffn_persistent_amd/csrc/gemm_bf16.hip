@@ -487,14 +487,17 @@ using Wide = CfgG<192, 256, 2, 4, 2, 2, 1>;
 using Medium = CfgG<128, 256, 2, 4, 3, 4, 1>;
 using Square = CfgG<128, 128, 2, 2, 2, 4, 2>;
 // one workgroup per CU with four stages: 4 to 19% faster than Square where no
-// compute unit gets a second tile (1024 x 4096 x 4096: 36 against 45 us)
+// compute unit gets a second tile (1024 x 4096 x 4096: 36 against 45 us), never
+// the fastest where one does
 using Deep = CfgG<128, 128, 2, 4, 4, 4, 1>;
 using Small = CfgG<64, 128, 1, 4, 3, 4, 2>;
 using Split = CfgG<32, 32, 1, 1, 2, 4, 1, 8>;
 using Split64 = CfgG<32, 64, 1, 1, 3, 4, 1, 4>;
 
 template <class C>
-constexpr GemmTile timed(double a, double c, double b, double o) { return GemmTile{C::TM, C::TN, C::OCC, C::KW, a, c, b, o}; }
+constexpr GemmTile timed(double a, double c, double b, double o, bool once = false) {
+  return GemmTile{C::TM, C::TN, C::OCC, C::KW, a, c, b, o, once};
+}
 
 template <class C, int OP>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
@@ -539,7 +542,7 @@ hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
 const GemmTile kBf16GemmTileTable[] = {
     timed<Large>(0.84, 1.56, 1.56, 4),  timed<Wide>(0.73, 1.27, 1.27, 4),  timed<Medium>(0.48, 0.90, 0.90, 5),
     timed<Square>(0.47, 0.79, 0.54, 2), timed<Small>(0.22, 0.37, 0.32, 4), timed<Split>(0.78, 0.96, 0.96, 1),
-    timed<Split64>(0.52, 0.64, 0.64, 2), timed<Deep>(0.28, 0.48, 0.48, 5)};
+    timed<Split64>(0.52, 0.64, 0.64, 2), timed<Deep>(0.28, 0.48, 0.48, 5, true)};
 const GemmTile kWgradTiles[] = {
     timed<Large>(1.10, 1.79, 1.79, 6),  GemmTile{}, timed<Medium>(0.60, 0.96, 0.96, 4),
     timed<Square>(0.47, 0.70, 0.47, 4), timed<Small>(0.32, 0.32, 0.32, 3), GemmTile{}, GemmTile{}, GemmTile{}};

@@ -431,7 +431,9 @@ using Split = CfgQ<32, 32, 1, 1, 2, 4, 1, 8>;
 using Split64 = CfgQ<32, 64, 1, 1, 3, 4, 1, 4>;
 
 template <class C>
-constexpr GemmTile timed(double a, double c, double b, double o) { return GemmTile{C::TM, C::TN, C::OCC, C::KW, a, c, b, o}; }
+constexpr GemmTile timed(double a, double c, double b, double o, bool once = false) {
+  return GemmTile{C::TM, C::TN, C::OCC, C::KW, a, c, b, o, once};
+}
 
 template <class C>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
@@ -449,7 +451,7 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
 const GemmTile kFp8GemmTileTable[] = {
     timed<Large>(0.73, 1.67, 1.67, 6),  timed<Wide>(0.68, 1.36, 1.36, 5),  timed<Medium>(0.60, 0.96, 0.96, 5),
     timed<Square>(0.37, 0.79, 0.54, 4), timed<Small>(0.28, 0.42, 0.32, 4), timed<Split>(0.68, 0.68, 0.68, 2),
-    timed<Split64>(0.60, 0.68, 0.68, 2), timed<Deep>(0.37, 0.56, 0.56, 5)};
+    timed<Split64>(0.60, 0.68, 0.68, 2), timed<Deep>(0.37, 0.56, 0.56, 5, true)};
 
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
   switch (id) {

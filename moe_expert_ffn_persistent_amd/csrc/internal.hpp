@@ -169,6 +169,7 @@ constexpr int kBf16GemmTiles = 8, kFp8GemmTiles = 8;
 struct GemmTile {
   int tm, tn, occ, kw;   // rows, columns, workgroups per compute unit, wavefronts that split the sum
   double a, c, b, o;     // us: a stage alone, with a workgroup on every compute unit, with occ of them, a tile's ends
+  bool once;             // only for calls that give no compute unit a second tile
 };
 extern const GemmTile kBf16GemmTileTable[], kWgradTiles[], kFp8GemmTileTable[];   // id - 1
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s);

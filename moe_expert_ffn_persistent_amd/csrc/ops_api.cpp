@@ -49,9 +49,9 @@ double expected_blocks(double rows, int L, int tm) {
 // that with all of them at work (c: clock, L2 and memory are shared then); with
 // two workgroups on a compute unit a stage of one of them takes 2 b.
 // Fitted to 198 bf16 and 66 e4m3 calls of 1 to 16384 rows, 1 to 32 experts and
-// 600 to 7168 features, each timed with every tile: the tile chosen took 1.5%
-// longer than the best one in the mean, 25% at worst (a few rows to many
-// experts, and where two tiles' last rounds are filled differently).
+// 600 to 7168 features, each timed with every tile; over 222 and 74 calls the
+// tile chosen took 1.1% and 1.7% longer than the best one in the mean, 26% at
+// worst (a few rows to many experts).
 double predicted(const GemmTile& t, double tiles, double stages) {
   const double q = std::max(1.0, std::ceil(tiles / kCus - 0.02));
   const double one = t.a + (t.c - t.a) * std::min(1.0, tiles / kCus);
@@ -70,7 +70,9 @@ int choose(const GemmTile* tiles, int n, const GemmArgs& a, int bk) {
     if (t.tm == 0) continue;   // not a tile of this product
     const double blocks = wgrad ? (double)a.L * ((a.n + t.tm - 1) / t.tm) : expected_blocks(a.expected, a.L, t.tm);
     const double stages = wgrad ? (double)a.expected / a.L / bk + 0.5 : std::max(1.0, (double)nc / bk / t.kw);
-    const double us = predicted(t, blocks * ((nj + t.tn - 1) / t.tn), stages);
+    const double count = blocks * ((nj + t.tn - 1) / t.tn);
+    if (t.once && count > kCus) continue;
+    const double us = predicted(t, count, stages);
     if (us < least) {
       least = us;
       best = i + 1;

@@ -269,3 +269,14 @@ def predict_schedule(shape: MoeShape, plan: MoePlan, counts, params: MoeSchedPar
                                       None if params is None else ctypes.byref(params),
                                       ctypes.byref(out)), "moe_predict_schedule")
     return out
+
+
+def load_opcall():
+    """The operators' compiled call path (csrc/opcall.cpp); raises if it has
+    not been built."""
+    try:
+        from . import _opcall
+    except ImportError as e:
+        raise RuntimeError("the operators' call path is missing: build it with "
+                           "`python -m moe_expert_ffn_persistent_amd.build`") from e
+    return _opcall

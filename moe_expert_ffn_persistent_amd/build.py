@@ -1,7 +1,9 @@
-"""Build the HIP library libmoe_ffn.so in-tree for gfx950.
+"""Build the HIP library libmoe_ffn.so and the operators' call path
+_opcall.so in-tree for gfx950.
 
 Each source under csrc/ is compiled to an object under _build/ (in
 parallel), then linked into moe_expert_ffn_persistent_amd/libmoe_ffn.so.
+opcall.cpp is a Python module (host code against torch's headers).
 Run ``python -m moe_expert_ffn_persistent_amd.build``; it always rebuilds.
 """
 from __future__ import annotations
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_ffn.so")
+OPCALL = os.path.join(PKG, "_opcall.so")
 ARCH = "gfx950"
 
 SOURCES = ["layout.hip", "ffn_bf16.hip", "ffn_fp8.hip", "ffn_w4a8.hip", "combine.hip", "burst.hip",
@@ -58,10 +62,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_opcall() -> None:
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found: the operators' call path cannot be built")
+    tmp = OPCALL + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "opcall.cpp"), "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the C++ compiler failed for opcall.cpp:\n{r.stderr}")
+    os.replace(tmp, OPCALL)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
+        opcall = ex.submit(_build_opcall)
         objs = list(ex.map(_compile, SOURCES))
+        opcall.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -45,6 +45,8 @@ def _on(device, *named):
             continue
         if t.device != device:
             raise ValueError(f"{what}: on {t.device}, need {device}")
+        if t.is_neg():
+            raise ValueError(f"{what}: a view with a pending negation (resolve_neg() makes it a tensor)")
         if grad and t.requires_grad:
             raise ValueError(f"{what} requires grad, and this operator records nothing for autograd: "
                              "call it in a torch.autograd.Function or under torch.no_grad()")
@@ -113,6 +115,26 @@ def _need_device(device):
         raise ValueError(f"need tensors on a GPU, got {device}")
 
 
+def _sizes(t, what, dims):
+    """Shape of an input that an output is allocated for (all else about it is
+    checked with the call)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{what}: need a tensor of {dims} dimensions")
+    if not t.is_cuda:
+        _need_device(t.device)
+    return t.shape
+
+
+def _type(t):
+    return t.dtype if isinstance(t, torch.Tensor) else None
+
+
+def _out_type(dtype):
+    if dtype not in _OUT:
+        raise ValueError(f"out_dtype: need bfloat16 or float32, got {dtype}")
+    return dtype
+
+
 def _empty(shape, dtype, device, stream):
     """An output for work on ``stream``, allocated for that stream."""
     if stream is None:
@@ -126,45 +148,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# Checked calls: the parameters that a check function made, by everything it
-# looked at (shapes, strides, dtypes, devices and the plain arguments; no
-# address and no value of a tensor), so that a call of sizes seen before costs a
-# lookup instead of the checks (about 2 us instead of 7, where a small kernel
-# runs for 3). Bounded: cleared when full.
-_PLANS: dict = {}
-_PLANS_MAX = 2048
-
-
-def _sig(t):
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"need a tensor, got {type(t).__name__}")
-    return t.shape, t.stride(), t.dtype, t.get_device()
-
-
-def _plan(key, check, *args):
-    got = _PLANS.get(key)
-    if got is None:
-        p = check(*args)
-        _need_device(args[_FIRST_TENSOR[check]].device)
-        if len(_PLANS) >= _PLANS_MAX:
-            _PLANS.clear()
-        got = _PLANS[key] = ctypes.byref(p)
-    return got
-
-
-def _no_grad(*tensors):
-    """Raise where an input requires grad and grad mode is on: of the checks,
-    the one that shapes and types do not settle (after _plan, which has made
-    sure that these are tensors)."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                _on(t.device, ("an input", t))
-
-
-_ENTRY: dict = {}
+_ENTRY: dict = {}   # entry point -> its address, once it has been called
+_get_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_again = _remember = None
 
 
 def _check_stream(stream, device):
@@ -176,23 +163,45 @@ def _check_stream(stream, device):
         raise ValueError(f"stream: of device {at}, the tensors are on device {device}")
 
 
-def _launch(name, device, params, ptrs, stream):
-    """One C entry point on the tensors' device (an index) and its current stream,
-    or the given one."""
+def _call(name, check, args, plain, tensors, stream):
+    """One C entry point, ``tensors`` its pointers in order. ``check(*args)``
+    makes its parameters from their sizes and the ``plain`` arguments; for
+    sizes that it has seen the call is made again without it (csrc/opcall.cpp:
+    a call costs the host 3.9 us, 3.4 of them the launch)."""
+    entry = _ENTRY.get(name)
+    if entry is not None:
+        device = _get_device()
+        if stream is None:
+            s = _raw_stream(device)
+        else:
+            s = stream.cuda_stream if getattr(stream, "device_index", None) == device else None
+        if s is not None:
+            st = _again(entry, device, s, plain, *tensors)
+            if st is not None:
+                if st != _lib.MOE_OK:
+                    _lib.check(st, name)
+                return
+    _first_call(name, check, args, plain, tensors, stream)
+
+
+def _first_call(name, check, args, plain, tensors, stream):
+    global _again, _remember
+    params = check(*args)
+    device = next(t for t in tensors if t is not None).device
+    _need_device(device)
     if stream is not None:
-        _check_stream(stream, device)
-    fn = _ENTRY.get(name)
-    if fn is None:
-        fn = _ENTRY[name] = getattr(_lib.load(), name)
-    if device == torch._C._cuda_getDevice():
-        s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-        st = fn(params, *ptrs, s)
-    else:
-        with torch.cuda.device(device):
-            s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-            st = fn(params, *ptrs, s)
+        _check_stream(stream, device.index)
+    fn = getattr(_lib.load(), name)
+    if _again is None:
+        call = _lib.load_opcall()
+        _again, _remember = call.again, call.remember
+    with torch.cuda.device(device):
+        s = _raw_stream(device.index) if stream is None else stream.cuda_stream
+        st = fn(ctypes.byref(params), *map(_ptr, tensors), s)
     if st != _lib.MOE_OK:
         _lib.check(st, name)
+    entry = _ENTRY[name] = ctypes.cast(fn, ctypes.c_void_p).value
+    _remember(bytes(params), entry, device.index, plain, *tensors)
 
 
 # ---- rows to and from the experts -------------------------------------------
@@ -223,15 +232,11 @@ def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
     4-byte elements; out [rows, H], allocated with one row for every entry of
     row_pair when not given. The gradient of combine_rows."""
     if out is None:
-        _matrix(x, "x", tuple(_ROW_TYPES))
-        _need_device(x.device)
+        _, H = _sizes(x, "x", 2)
         _indices(row_pair, "row_pair")
-        out = _empty((row_pair.numel(), x.shape[1]), x.dtype, x.device, stream)
-    p = _plan(("dispatch", _sig(x), _sig(row_pair), _sig(row_offset), top_k, _sig(out)), check_dispatch_inputs,
-              x, row_pair, row_offset, top_k, out)
-    _no_grad(x, out)
-    _launch("moe_dispatch_rows", x.get_device(), p,
-            (x.data_ptr(), row_pair.data_ptr(), row_offset.data_ptr(), out.data_ptr()), stream)
+        out = _empty((row_pair.numel(), H), x.dtype, x.device, stream)
+    _call("moe_dispatch_rows", check_dispatch_inputs, (x, row_pair, row_offset, top_k, out), (top_k,),
+          (x, row_pair, row_offset, out), stream)
     return out
 
 
@@ -256,16 +261,11 @@ def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stre
     negative. rows bf16 [R, H]; out [N, H] bf16 (rounded once) or fp32. The
     gradient of dispatch_rows."""
     if out is None:
-        _matrix(rows, "rows", (torch.bfloat16,))
-        _need_device(rows.device)
-        if out_dtype not in _OUT:
-            raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
+        _, H = _sizes(rows, "rows", 2)
         _indices(pair_row, "pair_row")
-        out = _empty((pair_row.numel() // max(1, top_k), rows.shape[1]), out_dtype, rows.device, stream)
-    p = _plan(("combine", _sig(rows), _sig(pair_row), top_k, _sig(out)), check_combine_rows_inputs,
-              rows, pair_row, top_k, out)
-    _no_grad(rows, out)
-    _launch("moe_combine_rows", rows.get_device(), p, (rows.data_ptr(), pair_row.data_ptr(), out.data_ptr()), stream)
+        out = _empty((pair_row.numel() // max(1, top_k), H), _out_type(out_dtype), rows.device, stream)
+    _call("moe_combine_rows", check_combine_rows_inputs, (rows, pair_row, top_k, out), (top_k,), (rows, pair_row, out),
+          stream)
     return out
 
 
@@ -291,18 +291,8 @@ def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate
 
 
 def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, tile, stream):
-    p = _plan((op, _sig(x), _sig(w), _sig(y), _sig(row_offset), expected_rows, accumulate, tile), check_grouped_inputs,
-              op, x, w, y, row_offset, expected_rows, accumulate, tile)
-    _no_grad(x, w, y)
-    _launch("moe_grouped_matmul", x.get_device(), p,
-            (row_offset.data_ptr(), x.data_ptr(), w.data_ptr(), y.data_ptr()), stream)
-
-
-def _grouped_out(shape, ref, out_dtype, stream):
-    if out_dtype not in _OUT:
-        raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
-    _need_device(ref.device)
-    return _empty(shape, out_dtype, ref.device, stream)
+    _call("moe_grouped_matmul", check_grouped_inputs, (op, x, w, y, row_offset, expected_rows, accumulate, tile),
+          (op, expected_rows, accumulate, tile), (row_offset, x, w, y), stream)
 
 
 def grouped_matmul(x, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, tile=0, stream=None):
@@ -312,9 +302,9 @@ def grouped_matmul(x, w, row_offset, out=None, out_dtype=torch.bfloat16, expecte
     hold together, when the buffers have room for many more: it only chooses
     the kernel's tile, which ``tile`` (0: automatic) names outright."""
     if out is None:
-        _matrix(x, "x", (torch.bfloat16,))
-        _matrix(w, "w", (torch.bfloat16,), 3)
-        out = _grouped_out((x.shape[0], w.shape[1]), x, out_dtype, stream)
+        rows, _ = _sizes(x, "x", 2)
+        _, n, _ = _sizes(w, "w", 3)
+        out = _empty((rows, n), _out_type(out_dtype), x.device, stream)
     _grouped(MOE_GROUPED_FORWARD, x, w, out, row_offset, expected_rows, False, tile, stream)
     return out
 
@@ -324,9 +314,9 @@ def grouped_matmul_dgrad(dy, w, row_offset, out=None, out_dtype=torch.bfloat16, 
     """Input gradient of grouped_matmul: ``out[r] = w[e].T @ dy[r]``; dy bf16
     [rows, n], out [rows, k] bf16 or fp32."""
     if out is None:
-        _matrix(dy, "dy", (torch.bfloat16,))
-        _matrix(w, "w", (torch.bfloat16,), 3)
-        out = _grouped_out((dy.shape[0], w.shape[2]), dy, out_dtype, stream)
+        rows, _ = _sizes(dy, "dy", 2)
+        _, _, k = _sizes(w, "w", 3)
+        out = _empty((rows, k), _out_type(out_dtype), dy.device, stream)
     _grouped(MOE_GROUPED_DGRAD, out, w, dy, row_offset, expected_rows, False, tile, stream)
     return out
 
@@ -339,9 +329,9 @@ def grouped_matmul_wgrad(dy, x, row_offset, out=None, out_dtype=torch.bfloat16, 
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        _matrix(x, "x", (torch.bfloat16,))
-        _matrix(dy, "dy", (torch.bfloat16,))
-        out = _grouped_out((_offsets(row_offset), dy.shape[1], x.shape[1]), x, out_dtype, stream)
+        _, n = _sizes(dy, "dy", 2)
+        _, k = _sizes(x, "x", 2)
+        out = _empty((_offsets(row_offset), n, k), _out_type(out_dtype), x.device, stream)
     _grouped(MOE_GROUPED_WGRAD, x, out, dy, row_offset, expected_rows, accumulate, tile, stream)
     return out
 
@@ -356,6 +346,14 @@ def _check_gate_up(a, row_weight, row_offset):
     if row_weight is not None:
         _vector(row_weight, "row_weight", rows, torch.float32)
     return rows, cols // 2, lda, 1 if row_offset is None else _offsets(row_offset)
+
+
+def _half(a):
+    """Rows, and columns of gate or up."""
+    rows, cols = _sizes(a, "gate_up", 2)
+    if cols % 2:
+        raise ValueError(f"gate_up: need gate and up columns, got {cols}")
+    return rows, cols // 2
 
 
 def check_swiglu_inputs(a, row_weight, row_offset, h, scales):
@@ -382,20 +380,16 @@ def swiglu(gate_up, row_weight=None, row_offset=None, out=None, scales=None, out
     torch.float8_e4m3fn or uint8) with fp32 ``scales`` [rows, ceil(I/128)], the
     fp32 values quantised as quantize_fp8 does: then (out, scales) is returned.
     With ``row_offset`` only the experts' rows are computed."""
-    if out is None or (scales is None and (out.dtype if out is not None else out_dtype) in _CODES):
-        rows, I, _, _ = _check_gate_up(gate_up, row_weight, row_offset)
-        _need_device(gate_up.device)
-        if out is None:
-            if out_dtype != torch.bfloat16 and out_dtype not in _CODES:
-                raise ValueError(f"out_dtype: need bfloat16, float8_e4m3fn or uint8, got {out_dtype}")
-            out = _empty((rows, I), out_dtype, gate_up.device, stream)
-        if scales is None and out.dtype in _CODES:
-            scales = _empty((rows, _blocks(I)), torch.float32, gate_up.device, stream)
-    p = _plan(("swiglu", _sig(gate_up), _sig(row_weight), _sig(row_offset), _sig(out), _sig(scales)), check_swiglu_inputs,
-              gate_up, row_weight, row_offset, out, scales)
-    _no_grad(gate_up, row_weight, out, scales)
-    _launch("moe_swiglu", gate_up.get_device(), p,
-            (gate_up.data_ptr(), _ptr(row_weight), _ptr(row_offset), out.data_ptr(), _ptr(scales)), stream)
+    if out is None:
+        rows, I = _half(gate_up)
+        if out_dtype != torch.bfloat16 and out_dtype not in _CODES:
+            raise ValueError(f"out_dtype: need bfloat16, float8_e4m3fn or uint8, got {out_dtype}")
+        out = _empty((rows, I), out_dtype, gate_up.device, stream)
+    if scales is None and _type(out) in _CODES:
+        rows, I = _half(gate_up)
+        scales = _empty((rows, _blocks(I)), torch.float32, gate_up.device, stream)
+    _call("moe_swiglu", check_swiglu_inputs, (gate_up, row_weight, row_offset, out, scales), (),
+          (gate_up, row_weight, row_offset, out, scales), stream)
     return out if scales is None else (out, scales)
 
 
@@ -418,19 +412,14 @@ def swiglu_backward(gate_up, dh, row_weight=None, row_offset=None, out=None, dro
     """Gradients of swiglu for dh bf16 [rows, I]: (dgate_up [rows, 2 I] bf16,
     drow_weight fp32 [rows]); the second is None without row_weight and
     drow_weight. ``out`` may be gate_up itself."""
-    if out is None or (drow_weight is None and row_weight is not None):
-        rows, I, _, _ = _check_gate_up(gate_up, row_weight, row_offset)
-        _need_device(gate_up.device)
-        if out is None:
-            out = _empty((rows, 2 * I), torch.bfloat16, gate_up.device, stream)
-        if drow_weight is None and row_weight is not None:
-            drow_weight = _empty((rows,), torch.float32, gate_up.device, stream)
-    p = _plan(("swiglu_backward", _sig(gate_up), _sig(dh), _sig(row_weight), _sig(row_offset), _sig(out), _sig(drow_weight)),
-              check_swiglu_backward_inputs, gate_up, dh, row_weight, row_offset, out, drow_weight)
-    _no_grad(gate_up, dh, row_weight, out, drow_weight)
-    _launch("moe_swiglu_backward", gate_up.get_device(), p,
-            (gate_up.data_ptr(), dh.data_ptr(), _ptr(row_weight), _ptr(row_offset), out.data_ptr(),
-             _ptr(drow_weight)), stream)
+    if out is None:
+        rows, I = _half(gate_up)
+        out = _empty((rows, 2 * I), torch.bfloat16, gate_up.device, stream)
+    if drow_weight is None and row_weight is not None:
+        rows, _ = _sizes(gate_up, "gate_up", 2)
+        drow_weight = _empty((rows,), torch.float32, gate_up.device, stream)
+    _call("moe_swiglu_backward", check_swiglu_backward_inputs, (gate_up, dh, row_weight, row_offset, out, drow_weight), (),
+          (gate_up, dh, row_weight, row_offset, out, drow_weight), stream)
     return out, drow_weight
 
 
@@ -478,15 +467,14 @@ def quantize_fp8(x, block_rows=1, row_offset=None, out=None, scales=None, stream
             raise ValueError(f"block_rows: need 1 or {BLOCK}, got {block_rows}")
         _need_device(x.device)
         if out is None:
-            out = _empty(tuple(x.shape), torch.float8_e4m3fn, x.device, stream)
+            out = _empty(x.shape, torch.float8_e4m3fn, x.device, stream)
         if scales is None:
             scales = _empty(_scale_shape(x, block_rows), torch.float32, x.device, stream)
-    p = _plan(("quantize", _sig(x), block_rows, _sig(row_offset), _sig(out), _sig(scales)), check_quantize_inputs,
-              x, block_rows, row_offset, out, scales)
-    _no_grad(x, out, scales)
-    if x.numel():
-        _launch("moe_quantize_fp8", x.get_device(), p,
-                (x.data_ptr(), _ptr(row_offset), out.data_ptr(), scales.data_ptr()), stream)
+    args = x, block_rows, row_offset, out, scales
+    if isinstance(x, torch.Tensor) and x.numel() == 0:
+        check_quantize_inputs(*args)
+    else:
+        _call("moe_quantize_fp8", check_quantize_inputs, args, (block_rows,), (x, row_offset, out, scales), stream)
     return out, scales
 
 
@@ -527,21 +515,9 @@ def fp8_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=to
     [L, ...], every row times its expert's matrix. out [rows, n] bf16 or fp32.
     ``expected_rows`` and ``tile`` as for grouped_matmul."""
     if out is None:
-        _matrix(x, "x", _CODES)
-        _matrix(w, "w", _CODES, 2 if row_offset is None else 3)
-        if out_dtype not in _OUT:
-            raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
-        _need_device(x.device)
-        out = _empty((x.shape[0], w.shape[-2]), out_dtype, x.device, stream)
-    p = _plan(("fp8", _sig(x), _sig(x_scales), _sig(w), _sig(w_scales), _sig(row_offset), _sig(out), expected_rows, tile),
-              check_fp8_inputs, x, x_scales, w, w_scales, row_offset, out, expected_rows, tile)
-    _no_grad(x, x_scales, w, w_scales, out)
-    _launch("moe_fp8_matmul", x.get_device(), p,
-            (_ptr(row_offset), x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), out.data_ptr()),
-            stream)
+        rows, _ = _sizes(x, "x", 2)
+        n = _sizes(w, "w", 2 if row_offset is None else 3)[-2]
+        out = _empty((rows, n), _out_type(out_dtype), x.device, stream)
+    _call("moe_fp8_matmul", check_fp8_inputs, (x, x_scales, w, w_scales, row_offset, out, expected_rows, tile),
+          (expected_rows, tile), (row_offset, x, x_scales, w, w_scales, out), stream)
     return out
-
-
-# which argument of a check function is its first tensor
-_FIRST_TENSOR = {check_dispatch_inputs: 0, check_combine_rows_inputs: 0, check_grouped_inputs: 1, check_swiglu_inputs: 0,
-                 check_swiglu_backward_inputs: 0, check_quantize_inputs: 0, check_fp8_inputs: 0}

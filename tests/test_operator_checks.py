@@ -256,6 +256,13 @@ def test_streams_of_another_device_are_refused():
             ops._check_stream(stream, 1)
 
 
+def test_negated_views_are_refused():
+    x = torch.zeros(R, 1, dtype=torch.complex64).conj().imag   # fp32, its sign not in memory
+    assert x.is_neg()
+    with pytest.raises(ValueError, match="negation"):
+        ops.check_quantize_inputs(x.as_strided((R, 1), (2, 1)), 1, None, z(R, 1, dtype=F8), z(R, 1, dtype=F32))
+
+
 def test_single_rows_with_huge_strides_count_as_their_length():
     x = torch.empty_strided((1, K), (1 << 40, 1), dtype=BF, device="meta")
     assert ops._matrix(x, "x", (BF,)) == K

@@ -1,6 +1,8 @@
 // Rows of the local experts gathered from the tokens (dispatch) and each
 // token's rows summed (combine): each other's gradients, both one pass over
 // the bytes.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "ops_common.hpp"
 
@@ -35,26 +37,27 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_k(const RowsArgs a) {
   }
 }
 
-// y[n] = sum of the token's rows, ascending slots, fp32. A workgroup of four
-// wavefronts takes a token. A wavefront finds the slots that are local with one
-// load and a ballot, so slots of other GPUs cost nothing, and a lane has eight
-// columns of up to four pieces of the row in flight, of the next slot before
-// this one's are added: 160 us with one piece and one slot at a time, 90 us
-// so (16384 tokens x 7168, 8 slots of which one in the mean is local: 470 MB).
-template <bool BF16>
-__global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool vec) {
-  constexpr int U = 4;
-  const int n = blockIdx.x, lane = threadIdx.x & 63;
+// y[n] = sum of the token's rows, ascending slots, fp32. TPT threads take a
+// token. A wavefront finds the slots that are local with one load and a ballot,
+// so slots of other GPUs cost nothing, and a lane has eight columns of up to U
+// pieces of the row in flight, of the next slot before this one's are added: 160
+// us with one piece and one slot at a time, 90 us so (16384 tokens x 7168, 8
+// slots of which one in the mean is local: 470 MB).
+template <bool BF16, int TPT, int U>
+__global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool vec, int tokens) {
+  const int n = blockIdx.x * (256 / TPT) + uni((int)threadIdx.x / TPT), lane = threadIdx.x & 63;
+  if (n >= tokens) return;
   const int idx = lane < a.k ? a.index[(size_t)n * a.k + lane] : -1;
   const uint64_t local = __ballot(idx >= 0 && idx < a.rows);
   char* yrow = static_cast<char*>(a.out) + (size_t)n * a.ld_out;
-  for (int c0 = threadIdx.x * 8; c0 < a.hidden; c0 += U * 2048) {
+  for (int c0 = threadIdx.x % TPT * 8; c0 < a.hidden; c0 += U * TPT * 8) {
     auto load = [&](int slot, uint4 (&v)[U]) {
       const int r = __builtin_amdgcn_readlane(idx, slot);
       const __bf16* row = reinterpret_cast<const __bf16*>(static_cast<const char*>(a.in) + (size_t)r * a.ld_in);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * 2048, m = a.hidden - c;
+        const int c = c0 + u * TPT * 8, m = a.hidden - c;
+        if (u && uni(c) >= a.hidden) break;   // no lane of this wavefront has any
         if (vec && m >= 8) {
           v[u] = *reinterpret_cast<const uint4*>(row + c);
         } else {
@@ -73,6 +76,7 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool
       if (left) load(__builtin_ctzll(left), v[1]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (u && uni(c0 + u * TPT * 8) >= a.hidden) break;
         float x[8];
         unpack8(v[0][u], x);
 #pragma unroll
@@ -82,7 +86,8 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * 2048, m = min(8, a.hidden - c);
+      const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
+      if (u && uni(c) >= a.hidden) break;
       const bool whole = vec && m == 8;
       if constexpr (BF16) {
         if (m > 0) store8(reinterpret_cast<__bf16*>(yrow) + c, m, whole, s[u]);
@@ -117,9 +122,25 @@ hipError_t launch_dispatch_rows(const RowsArgs& a, hipStream_t s) {
 hipError_t launch_combine_rows(const RowsArgs& a, bool bf16_out, hipStream_t s) {
   const bool vec = (((uintptr_t)a.in | (uintptr_t)a.out | (uintptr_t)a.ld_in | (uintptr_t)a.ld_out) % 16) == 0;
   const int tokens = (int)(a.pairs / a.k);
-  if (bf16_out) moe_combine_rows_k<true><<<tokens, 256, 0, s>>>(a, vec);
-  else moe_combine_rows_k<false><<<tokens, 256, 0, s>>>(a, vec);
-  return hipGetLastError();
+  auto run = [&](auto tpt, auto pieces) {
+    constexpr int T = decltype(tpt)::value, U = decltype(pieces)::value;
+    const int grid = (tokens + 256 / T - 1) / (256 / T);
+    if (bf16_out) moe_combine_rows_k<true, T, U><<<grid, 256, 0, s>>>(a, vec, tokens);
+    else moe_combine_rows_k<false, T, U><<<grid, 256, 0, s>>>(a, vec, tokens);
+    return hipGetLastError();
+  };
+  using std::integral_constant;
+  // Few tokens take a workgroup each, whatever their length (8 slots, 4 tokens x
+  // 4096: 4.7 us, with two wavefronts a token 5.9, with one 10); with many, short
+  // rows take fewer threads, whose lanes all have columns (30000 tokens, one slot
+  // of 8 local: 512 columns 11.4 us, a workgroup each 28.4; 1016: 20.6 and 37.8;
+  // 2056: 39.9 and 56.2; 4096: 96.5 and 98.6; 7168: 167.5 and 165.3).
+  if (tokens > 1024) {
+    if (a.hidden <= 512) return run(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if (a.hidden <= 1024) return run(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    if (a.hidden <= 4096) return run(integral_constant<int, 128>{}, integral_constant<int, 4>{});
+  }
+  return run(integral_constant<int, 256>{}, integral_constant<int, 4>{});
 }
 
 }  // namespace moe

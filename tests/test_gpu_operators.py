@@ -326,6 +326,12 @@ def test_combine_rows(N, k, E, L, H, out_dtype):
     assert torch.equal(lead, got)
 
 
+@pytest.mark.parametrize("H", [37, 512, 520, 1016, 1030, 2056, 4104])
+def test_combine_rows_of_many_tokens(H):
+    # more than 1024 tokens: threads a token by the row's length; an odd number of them
+    test_combine_rows(1101, 3, 4, 2, H, BF)
+
+
 # ---- SwiGLU ------------------------------------------------------------------------
 
 def swiglu_ref(a, weight, dh=None):

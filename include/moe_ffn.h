@@ -417,8 +417,9 @@ int32_t moe_mfma_rate_probe(int32_t format, int32_t blocks, int64_t iters, const
  * inference, as separate operators with their gradients, for training the
  * experts, for activations the fused kernel does not have and for dense layers
  * in the fp8 format. They follow the conventions above and hold no state: no
- * workspace, no allocation, every launch may be captured, and calls on
- * different streams are independent.
+ * allocation, no workspace but the one that a caller gives to the *_split
+ * products, every launch may be captured, and calls on different streams are
+ * independent.
  *
  * `row_offset` is the layout's (device int32 [L+1], row_offset[0] first): rows
  * row_offset[e] .. row_offset[e+1]-1 belong to expert e. `rows` is the number
@@ -483,9 +484,21 @@ typedef struct {
   int32_t accumulate;      /* MOE_GROUPED_WGRAD: add to W instead of overwriting it */
   int32_t tile;            /* kernel configuration; 0 = automatic, an id that does not take
                               the call's operands is MOE_ERR_UNSUPPORTED */
+  int32_t splits;          /* moe_grouped_matmul_split: ranges that the sum is cut into, 1..64; 0 = automatic */
+  int64_t workspace_bytes; /* moe_grouped_matmul_split: of its workspace */
 } moe_grouped_params;
 int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w,
                            void* y, void* stream);
+
+/* The same product with a workspace (device memory, 16-byte aligned, the
+ * call's own until it is done), in which a call with few output tiles and a
+ * long sum may add up ranges of the sum side by side, in fp32, and join them in
+ * their order: results do not depend on timing. moe_grouped_workspace_bytes
+ * says what it takes to do so, 0 where the call gains nothing; with less it is
+ * cut into fewer ranges or none (workspace NULL: none). */
+int64_t moe_grouped_workspace_bytes(const moe_grouped_params* p);
+int32_t moe_grouped_matmul_split(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w,
+                                 void* y, void* workspace, void* stream);
 
 /* SwiGLU of routed rows: h[r, i] = w_r silu(a[r, i]) a[r, I + i], silu(g) =
  * g / (1 + e^-g), as the fused kernel's Linear-1 epilogue (w_r there applied
@@ -562,10 +575,17 @@ typedef struct {
   int64_t expert_stride_w; /* elements */
   int32_t out_dtype;       /* MOE_Y_FP32 or MOE_Y_BF16 */
   int32_t tile;            /* as moe_grouped_params */
+  int32_t splits;          /* moe_fp8_matmul_split: as moe_grouped_params */
+  int64_t workspace_bytes;
 } moe_fp8_params;
 int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const void* x,
                        const float* x_scales, const void* w, const float* w_scales, void* y,
                        void* stream);
+/* With a workspace, as moe_grouped_matmul_split. */
+int64_t moe_fp8_workspace_bytes(const moe_fp8_params* p);
+int32_t moe_fp8_matmul_split(const moe_fp8_params* p, const int32_t* row_offset, const void* x,
+                             const float* x_scales, const void* w, const float* w_scales, void* y,
+                             void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

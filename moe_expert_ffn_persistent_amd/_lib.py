@@ -36,7 +36,9 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_layout_scratch_bytes", "
            "moe_workspace_init", "moe_dispatch_layout", "moe_ffn_forward", "moe_combine_check",
            "moe_store_burst_probe", "moe_predict_schedule", "moe_ffn_forward_noalloc",
            "moe_mfma_rate_probe", "moe_dispatch_rows", "moe_combine_rows", "moe_grouped_matmul",
-           "moe_swiglu", "moe_swiglu_backward", "moe_quantize_fp8", "moe_fp8_matmul")
+           "moe_swiglu", "moe_swiglu_backward", "moe_quantize_fp8", "moe_fp8_matmul",
+           "moe_grouped_workspace_bytes", "moe_grouped_matmul_split", "moe_fp8_workspace_bytes",
+           "moe_fp8_matmul_split")
 MFMA_PROBE_THREADS = 512
 MFMA_PROBE_OPERAND_BYTES = 64 * 64 * 16 * 16
 NOALLOC_WORKSPACE_BYTES = 64 << 20
@@ -105,7 +107,7 @@ class MoeGroupedParams(ctypes.Structure):
     _fields_ = [("op", c_i32), ("num_experts", c_i32), ("rows", c_i64), ("expected_rows", c_i64),
                 ("n", c_i32), ("k", c_i32), ("ld_x", c_i64), ("ld_w", c_i64), ("ld_y", c_i64),
                 ("expert_stride_w", c_i64), ("out_dtype", c_i32), ("accumulate", c_i32),
-                ("tile", c_i32)]
+                ("tile", c_i32), ("splits", c_i32), ("workspace_bytes", c_i64)]
 
 
 class MoeSwigluParams(ctypes.Structure):
@@ -122,7 +124,8 @@ class MoeQuantizeParams(ctypes.Structure):
 class MoeFp8Params(ctypes.Structure):
     _fields_ = [("num_experts", c_i32), ("rows", c_i64), ("expected_rows", c_i64), ("n", c_i32),
                 ("k", c_i32), ("ld_x", c_i64), ("ld_xs", c_i64), ("ld_w", c_i64), ("ld_y", c_i64),
-                ("expert_stride_w", c_i64), ("out_dtype", c_i32), ("tile", c_i32)]
+                ("expert_stride_w", c_i64), ("out_dtype", c_i32), ("tile", c_i32), ("splits", c_i32),
+                ("workspace_bytes", c_i64)]
 
 
 class MoeError(RuntimeError):
@@ -180,10 +183,16 @@ def load(path: str | None = None):
                              ("moe_swiglu", MoeSwigluParams, 5),
                              ("moe_swiglu_backward", MoeSwigluParams, 6),
                              ("moe_quantize_fp8", MoeQuantizeParams, 4),
-                             ("moe_fp8_matmul", MoeFp8Params, 6)):
+                             ("moe_fp8_matmul", MoeFp8Params, 6),
+                             ("moe_grouped_matmul_split", MoeGroupedParams, 5),
+                             ("moe_fp8_matmul_split", MoeFp8Params, 7)):
         f = getattr(lib, fn)
         f.restype = c_i32
         f.argtypes = [P(params)] + [c_vp] * (nptr + 1)
+    for fn, params in (("moe_grouped_workspace_bytes", MoeGroupedParams), ("moe_fp8_workspace_bytes", MoeFp8Params)):
+        f = getattr(lib, fn)
+        f.restype = c_i64
+        f.argtypes = [P(params)]
     _lib = lib
     return lib
 

@@ -26,7 +26,7 @@ ARCH = "gfx950"
 
 SOURCES = ["layout.hip", "ffn_bf16.hip", "ffn_fp8.hip", "ffn_w4a8.hip", "combine.hip", "burst.hip",
            "mfma_probe.hip", "rows.hip", "swiglu.hip", "gemm_any.hip", "gemm_bf16.hip", "gemm_fp8.hip",
-           "api.cpp", "ops_api.cpp", "planner.cpp"]
+           "gemm_split.hip", "api.cpp", "ops_api.cpp", "planner.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -431,28 +431,36 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
   const long long ldt = FWD ? a.ld_x : a.ld_y, ldo = WG ? a.ld_w : FWD ? a.ld_y : a.ld_x;
   const int oe = a.out_bf16 ? 2 : 4;
   const GroupScan<C::TM> scan(a.row_offset, a.L, a.rows);
-  const int total = WG ? a.L * ti * tj : scan.total * tj;
+  const int tiles = WG ? a.L * ti * tj : scan.total * tj, total = tiles * a.splits;
 
   // tile of workgroup slot b: what it is, and the copies of its first stage
   auto start = [&](int b, Work& wk) {
-    const int tile = xcd_tile(b, total);
+    int tile = xcd_tile(b, total);
     if (tile >= total) return false;
+    int s = 0, c0 = 0;
+    if (a.splits > 1) {
+      s = tile / tiles;
+      tile -= s * tiles;
+    }
     if constexpr (WG) {
       const int e = tile / (ti * tj);
       int i, j;
       tile_at(tile - e * ti * tj, ti, tj, i, j);
       const int r0 = uni(clamped_offset(a.row_offset, a.L, a.rows, e));
       const int Me = uni(max(clamped_offset(a.row_offset, a.L, a.rows, e + 1) - r0, 0));
-      wk = Work{i * C::TM, a.n, j * C::TN, Me, static_cast<char*>(a.w) + (long long)e * a.es_w * oe};
-      g.t.setup(y + (long long)r0 * a.ld_y, a.ld_y, wk.i0, a.n);
-      g.f.setup(x + (long long)r0 * a.ld_x, a.ld_x, wk.j0, a.k);
+      const int nc = split_range<kBK>(Me, a.splits, s, c0);
+      wk = Work{i * C::TM, a.n, j * C::TN, nc, static_cast<char*>(a.w) + ((long long)e * a.es_w + s * a.part) * oe};
+      g.t.setup(y + (long long)(r0 + c0) * a.ld_y, a.ld_y, wk.i0, a.n);
+      g.f.setup(x + (long long)(r0 + c0) * a.ld_x, a.ld_x, wk.j0, a.k);
     } else {
       int p, j;
       tile_at(tile, scan.total, tj, p, j);
       const Group gr = scan.find(p);
-      wk = Work{gr.m * C::TM, gr.Me, j * C::TN, FWD ? a.k : a.n, static_cast<char*>(FWD ? a.y : a.x) + (long long)gr.r0 * ldo * oe};
-      g.t.setup((FWD ? x : y) + (long long)gr.r0 * ldt, ldt, wk.i0, wk.ni);
-      g.f.setup(w + (long long)gr.e * a.es_w, a.ld_w, wk.j0, nj);
+      const int nc = split_range<kBK>(FWD ? a.k : a.n, a.splits, s, c0);
+      wk = Work{gr.m * C::TM, gr.Me, j * C::TN, nc,
+                static_cast<char*>(FWD ? a.y : a.x) + ((long long)gr.r0 * ldo + s * a.part) * oe};
+      g.t.setup((FWD ? x : y) + (long long)gr.r0 * ldt + c0, ldt, wk.i0, wk.ni);
+      g.f.setup(w + (long long)gr.e * a.es_w + (FWD ? c0 : (long long)c0 * a.ld_w), a.ld_w, wk.j0, nj);
     }
     g.first(ring, wk.nc, kw);
     return true;
@@ -504,7 +512,7 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
   const long long nj = ((OP == MOE_GROUPED_FORWARD ? a.n : a.k) + C::TN - 1) / C::TN;
   const long long mi = OP == MOE_GROUPED_WGRAD ? (long long)a.L * ((a.n + C::TM - 1) / C::TM)
                                                : ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM;
-  const long long tiles = nj * mi;
+  const long long tiles = nj * mi * a.splits;
   if (tiles >= INT_MAX / 2) return launch_gemm_any(a, false, s);   // the kernel counts tiles in int
   // A workgroup for each place on the GPU; a multiple of 8 keeps one on its XCD.
   // Past a tile for every compute unit all places get one, since the tile order

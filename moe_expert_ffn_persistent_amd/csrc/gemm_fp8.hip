@@ -351,9 +351,9 @@ struct TileQ {
   }
 };
 
-// A tile of the call
+// A tile of the call, and how much of k it adds up
 struct Work {
-  int i0, ni, j0;
+  int i0, ni, j0, nc;
   const float* ws;
   char* out;
 };
@@ -369,32 +369,40 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
   const int oe = a.out_bf16 ? 2 : 4;
   const bool grouped = a.row_offset != nullptr;
   const GroupScan<C::TM> scan(a.row_offset, grouped ? a.L : 0, a.rows);
-  const int ti = grouped ? scan.total : (a.rows + C::TM - 1) / C::TM, total = ti * tj;
+  const int ti = grouped ? scan.total : (a.rows + C::TM - 1) / C::TM;
+  const int tiles = ti * tj, total = tiles * a.splits;
   TileQ<C> g;
 
   auto start = [&](int b, Work& wk) {
-    const int tile = xcd_tile(b, total);
+    int tile = xcd_tile(b, total);
     if (tile >= total) return false;
+    int s = 0, c0 = 0;
+    if (a.splits > 1) {
+      s = tile / tiles;
+      tile -= s * tiles;
+    }
+    const int nc = split_range<128>(a.k, a.splits, s, c0);
     int p, j;
     tile_at(tile, ti, tj, p, j);
     const Group gr = grouped ? scan.find(p) : Group{0, p, 0, a.rows, true};
     const int i0 = gr.m * C::TM, j0 = j * C::TN;
-    g.fbase = static_cast<const char*>(a.w) + (long long)gr.e * a.es_w + (long long)j0 * a.ld_w;
-    g.tbase = static_cast<const char*>(a.x) + (long long)(gr.r0 + i0) * a.ld_x;
+    g.fbase = static_cast<const char*>(a.w) + (long long)gr.e * a.es_w + (long long)j0 * a.ld_w + c0;
+    g.tbase = static_cast<const char*>(a.x) + (long long)(gr.r0 + i0) * a.ld_x + c0;
     g.offsets(g.fv, a.ld_w, a.n - 1 - j0);
     g.offsets(g.tv, a.ld_x, gr.Me - 1 - i0);
     // scales: rows wave * 64 + lane of the tile, behind them the tile's blocks of weights
     const long long wblock = (long long)gr.e * nb + j0 / 128;
     const int srow = g.wave_of() * 64 + lane;
     if (C::KW > 1 || g.wave_of() * 64 < C::TM) {
-      g.sbase = reinterpret_cast<const char*>(a.xs + (long long)(gr.r0 + i0) * a.ld_xs);
+      g.sbase = reinterpret_cast<const char*>(a.xs + (long long)(gr.r0 + i0) * a.ld_xs + c0 / 128);
       g.sv = (uint32_t)min(srow % C::TM, gr.Me - 1 - i0) * (uint32_t)(a.ld_xs * 4);
     } else {
-      g.sbase = reinterpret_cast<const char*>(a.ws + wblock * kb);
+      g.sbase = reinterpret_cast<const char*>(a.ws + wblock * kb + c0 / 128);
       g.sv = (uint32_t)min(srow - C::TM, min(1, nb - 1 - j0 / 128)) * (uint32_t)(kb * 4);
     }
-    wk = Work{i0, gr.Me, j0, a.ws + wblock * kb, static_cast<char*>(a.y) + (long long)gr.r0 * a.ld_y * oe};
-    g.first(ring, a.k, kw);
+    wk = Work{i0, gr.Me, j0, nc, a.ws + wblock * kb + c0 / 128,
+              static_cast<char*>(a.y) + ((long long)gr.r0 * a.ld_y + s * a.part) * oe};
+    g.first(ring, nc, kw);
     return true;
   };
 
@@ -403,7 +411,7 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
   int stores = 0;   // of the previous tile, possibly in flight
   bool more = start(b, cur);
   while (more) {
-    g.multiply(ring, cur.ni - cur.i0, a.k, cur.ws, wf, wt, kw, stores);
+    g.multiply(ring, cur.ni - cur.i0, cur.nc, cur.ws, wf, wt, kw, stores);
     stores = 0;
     b += gridDim.x;
     if constexpr (C::KW == 1) {
@@ -439,7 +447,7 @@ template <class C>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
   const long long nj = (a.n + C::TN - 1) / C::TN;
   const long long mi = a.row_offset ? ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM : (a.rows + C::TM - 1) / C::TM;
-  const long long tiles = nj * mi;
+  const long long tiles = nj * mi * a.splits;
   if (tiles >= INT_MAX / 2) return launch_gemm_any(a, true, s);   // the kernel counts tiles in int
   const long long grid = tiles > kCus ? kCus * C::OCC : (tiles + 7) / 8 * 8;
   moe_gemm_fp8<C><<<(unsigned)grid, C::THREADS, 0, s>>>(a);

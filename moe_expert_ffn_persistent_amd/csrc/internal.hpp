@@ -161,6 +161,10 @@ struct GemmArgs {
   int op, L, rows, n, k;
   bool out_bf16, accumulate;
   int expected;                // rows expected in all experts together
+  // The sum cut into `splits` ranges of whole stages (1: not cut): range s adds
+  // up in fp32 at s * part elements past the output
+  int splits;
+  long long part;
 };
 constexpr int kCus = 256;   // compute units, places for a persistent workgroup
 hipError_t launch_gemm_any(const GemmArgs& a, bool fp8, hipStream_t s);
@@ -172,6 +176,10 @@ struct GemmTile {
   bool once;             // only for calls that give no compute unit a second tile
 };
 extern const GemmTile kBf16GemmTileTable[], kWgradTiles[], kFp8GemmTileTable[];   // id - 1
+// The same call with its sum cut into a.splits ranges, written to `ws` (fp32, one
+// output's elements a range), and the joining of them into a's output
+GemmArgs split_args(const GemmArgs& a, float* ws);
+hipError_t launch_join_splits(const GemmArgs& a, const float* ws, hipStream_t s);
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s);
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s);
 

@@ -15,6 +15,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -25,12 +26,13 @@
 
 namespace {
 
-constexpr int kMaxTensors = 6;
+constexpr int kMaxTensors = 7;
 constexpr Py_ssize_t kMaxParams = 128;
 constexpr size_t kMaxPlans = 2048;   // cleared when full
 
 struct Plan {
   alignas(8) char params[kMaxParams];
+  int64_t workspace;   // bytes of the last pointer, the call's own
 };
 
 std::unordered_map<std::string, Plan>& plans() {
@@ -42,6 +44,7 @@ struct Call {
   std::string key;
   void* ptr[kMaxTensors];
   int n = 0;
+  c10::Device device = c10::kCPU;   // the tensors'
 
   void add(int64_t v) { key.append(reinterpret_cast<const char*>(&v), sizeof v); }
 
@@ -83,6 +86,7 @@ struct Call {
       key.append(reinterpret_cast<const char*>(sizes.data()), sizes.size() * sizeof(int64_t));
       key.append(reinterpret_cast<const char*>(strides.data()), strides.size() * sizeof(int64_t));
       ptr[i] = t.data_ptr();
+      this->device = t.device();
     }
     return true;
   }
@@ -104,9 +108,12 @@ int32_t launch(void* entry, const void* p, void* const* a, int n, void* s) {
     case 5:
       return reinterpret_cast<int32_t (*)(P, void*, void*, void*, void*, void*, void*)>(entry)(p, a[0], a[1], a[2], a[3],
                                                                                                a[4], s);
-    default:
+    case 6:
       return reinterpret_cast<int32_t (*)(P, void*, void*, void*, void*, void*, void*, void*)>(entry)(
           p, a[0], a[1], a[2], a[3], a[4], a[5], s);
+    default:
+      return reinterpret_cast<int32_t (*)(P, void*, void*, void*, void*, void*, void*, void*, void*)>(entry)(
+          p, a[0], a[1], a[2], a[3], a[4], a[5], a[6], s);
   }
 }
 
@@ -126,14 +133,16 @@ int read_call(Call& c, PyObject* entry, PyObject* device, PyObject* plain, PyObj
   return ok ? 1 : 0;
 }
 
-// again(entry, device, stream, plain, *tensors) -> status, or None
+// again(entry, device, stream, current, plain, *tensors) -> status, or None;
+// False where the call takes a workspace and `current` does not say that the
+// stream is the current one: it is allocated for the current stream
 PyObject* again(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs < 7) {
-    PyErr_SetString(PyExc_TypeError, "again(entry, device, stream, plain, *tensors): at least three tensors");
+  if (nargs < 8) {
+    PyErr_SetString(PyExc_TypeError, "again(entry, device, stream, current, plain, *tensors): at least three tensors");
     return nullptr;
   }
   Call& c = scratch();
-  const int got = read_call(c, args[0], args[1], args[3], args + 4, nargs - 4);
+  const int got = read_call(c, args[0], args[1], args[4], args + 5, nargs - 5);
   if (got < 0) return nullptr;
   if (got == 0) Py_RETURN_NONE;
   const auto it = plans().find(c.key);
@@ -145,6 +154,20 @@ PyObject* again(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   void* ptr[kMaxTensors];
   const int n = c.n;
   std::memcpy(ptr, c.ptr, sizeof ptr);
+  at::Tensor workspace;
+  if (plan.workspace > 0) {
+    if (args[3] != Py_True) Py_RETURN_FALSE;
+    try {
+      workspace = at::empty({plan.workspace}, at::TensorOptions().dtype(at::kByte).device(c.device));
+    } catch (const c10::OutOfMemoryError& e) {
+      PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
+      return nullptr;
+    } catch (const std::exception& e) {
+      PyErr_SetString(PyExc_RuntimeError, e.what());
+      return nullptr;
+    }
+    ptr[n - 1] = workspace.data_ptr();
+  }
   int32_t status;
   Py_BEGIN_ALLOW_THREADS
   status = launch(entry, plan.params, ptr, n, stream);
@@ -152,19 +175,23 @@ PyObject* again(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return PyLong_FromLong(status);
 }
 
-// remember(params, entry, device, plain, *tensors): the struct's bytes for
-// calls like this one
+// remember(params, entry, device, workspace, plain, *tensors): the struct's
+// bytes for calls like this one, and the bytes of workspace that they take (in
+// the place of the last tensor)
 PyObject* remember(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs < 7 || !PyBytes_Check(args[0]) || PyBytes_GET_SIZE(args[0]) > kMaxParams) {
-    PyErr_SetString(PyExc_TypeError, "remember(params, entry, device, plain, *tensors): bytes and at least three tensors");
+  if (nargs < 8 || !PyBytes_Check(args[0]) || PyBytes_GET_SIZE(args[0]) > kMaxParams || !PyLong_Check(args[3])) {
+    PyErr_SetString(PyExc_TypeError,
+                    "remember(params, entry, device, workspace, plain, *tensors): bytes and at least three tensors");
     return nullptr;
   }
+  Plan plan{};
+  plan.workspace = PyLong_AsLongLong(args[3]);
+  if (PyErr_Occurred()) return nullptr;
   Call& c = scratch();
-  const int got = read_call(c, args[1], args[2], args[3], args + 4, nargs - 4);
+  const int got = read_call(c, args[1], args[2], args[4], args + 5, nargs - 5);
   if (got < 0) return nullptr;
   if (got == 0) Py_RETURN_FALSE;
   if (plans().size() >= kMaxPlans) plans().clear();
-  Plan plan{};
   std::memcpy(plan.params, PyBytes_AS_STRING(args[0]), (size_t)PyBytes_GET_SIZE(args[0]));
   plans()[c.key] = plan;
   Py_RETURN_TRUE;
@@ -172,10 +199,11 @@ PyObject* remember(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 
 PyMethodDef methods[] = {
     {"again", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(again)), METH_FASTCALL,
-     "again(entry, device, stream, plain, *tensors): the call of a C entry point for sizes that were remembered; "
-     "its status, or None for a call that has to be checked."},
+     "again(entry, device, stream, current, plain, *tensors): the call of a C entry point for sizes that were "
+     "remembered; its status, None for a call that has to be checked, or False for one that takes a workspace on a "
+     "stream that is not the current one."},
     {"remember", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(remember)), METH_FASTCALL,
-     "remember(params, entry, device, plain, *tensors): keep a checked call's parameter struct (bytes)."},
+     "remember(params, entry, device, workspace, plain, *tensors): keep a checked call's parameter struct (bytes)."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_opcall", "Call path of the operators for sizes checked before.", -1,

@@ -60,25 +60,182 @@ double predicted(const GemmTile& t, double tiles, double stages) {
   return pairs * (stages * std::max(one, 2 * t.b) + t.o) + (q - 2 * pairs) * (stages * one + t.o);
 }
 
-int choose(const GemmTile* tiles, int n, const GemmArgs& a, int bk) {
+constexpr double kJoinUs = 4, kJoinRate = 5e6;   // bytes a us
+
+struct Choice {
+  int tile, splits;
+};
+
+// Tile (or the one asked for) and ranges of the sum, up to what `room` fp32
+// elements of workspace hold. Joining costs a launch and a pass over the ranges.
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+constexpr int kMaxSplits = 64;
+constexpr long long kMaxWorkspace = 256ll << 20;
+
+Choice choose(const GemmTile* tiles, int n, const GemmArgs& a, int bk, int tile, int splits, long long room) {
   const bool wgrad = a.op == MOE_GROUPED_WGRAD;
   const int nj = a.op == MOE_GROUPED_FORWARD ? a.n : a.k, nc = a.op == MOE_GROUPED_FORWARD ? a.k : a.n;
-  int best = 1;
+  const long long part = split_args(a, nullptr).part;
+  const double written = wgrad ? (double)part : (double)a.expected * nj;
+  Choice best{tile > 0 ? tile : 1, splits > 0 ? splits : 1};
   double least = 1e300;
-  for (int i = 0; i < n; ++i) {
+  for (int i = tile > 0 ? tile - 1 : 0; i < (tile > 0 ? tile : n); ++i) {
     const GemmTile& t = tiles[i];
     if (t.tm == 0) continue;   // not a tile of this product
     const double blocks = wgrad ? (double)a.L * ((a.n + t.tm - 1) / t.tm) : expected_blocks(a.expected, a.L, t.tm);
     const double stages = wgrad ? (double)a.expected / a.L / bk + 0.5 : std::max(1.0, (double)nc / bk / t.kw);
-    const double count = blocks * ((nj + t.tn - 1) / t.tn);
-    if (t.once && count > kCus) continue;
-    const double us = predicted(t, count, stages);
-    if (us < least) {
-      least = us;
-      best = i + 1;
+    for (const int candidate : kSplits) {
+      const int s = splits > 0 ? splits : candidate;
+      if (splits == 0 && s > 1 && (s * part > room || stages < 4 * s)) continue;
+      const double count = s * blocks * ((nj + t.tn - 1) / t.tn);
+      if (t.once && count > kCus && tile == 0) continue;
+      const double us = predicted(t, count, std::max(1.0, std::ceil(stages / s))) + (s > 1 ? kJoinUs + s * written * 8 / kJoinRate : 0);
+      if (us < least) {
+        least = us;
+        best = Choice{i + 1, s};
+      }
     }
   }
   return best;
+}
+
+// the ranges and workspace of a *_split call
+bool split_ok(int32_t splits, int64_t bytes) { return splits >= 0 && splits <= kMaxSplits && bytes >= 0; }
+
+// One product: whole, or in ranges joined afterwards
+template <class Launch>
+int32_t run(const GemmArgs& a, Choice c, float* ws, hipStream_t s, Launch launch) {
+  if (c.splits == 1) return done(launch(c.tile, a, s));
+  GemmArgs b = a;
+  b.splits = c.splits;
+  const hipError_t e = launch(c.tile, split_args(b, ws), s);
+  return e != hipSuccess ? done(e) : done(launch_join_splits(b, ws, s));
+}
+
+// Bytes that the automatic choice of a call takes
+int64_t workspace_of(const GemmTile* tiles, int n, const GemmArgs& a, int bk, int tile, int splits) {
+  const Choice c = choose(tiles, n, a, bk, tile, splits, kMaxWorkspace / 4);
+  return c.splits > 1 ? c.splits * split_args(a, nullptr).part * 4 : 0;
+}
+
+bool grouped_ok(const moe_grouped_params* p) {
+  return p && p->op >= MOE_GROUPED_FORWARD && p->op <= MOE_GROUPED_WGRAD && p->num_experts >= 1 &&
+         p->num_experts <= MOE_MAX_LOCAL_EXPERTS && p->rows >= 0 && p->rows <= kMaxRows && p->expected_rows >= 0 &&
+         p->n >= 1 && p->n <= kMaxCols && p->k >= 1 && p->k <= kMaxCols && stride_ok(p->ld_x, p->k) &&
+         stride_ok(p->ld_w, p->k) && stride_ok(p->ld_y, p->n) &&
+         matrix_stride_ok(p->expert_stride_w, p->num_experts, p->n, p->ld_w, p->k) && dtype_ok(p->out_dtype) &&
+         p->tile >= 0 && (!p->accumulate || p->op == MOE_GROUPED_WGRAD);
+}
+
+// The 16-byte kernels' sizes: rows of every operand start and end on 16 bytes,
+// and their lane offsets (256 rows of a tile) fit 32 bits.
+bool grouped_fast(const moe_grouped_params* p) {
+  return p->n % 8 == 0 && p->k % 8 == 0 && p->ld_x % 8 == 0 && p->ld_w % 8 == 0 && p->ld_y % 8 == 0 &&
+         p->expert_stride_w % 8 == 0 && std::max(p->ld_x, std::max(p->ld_w, p->ld_y)) <= (1 << 22);
+}
+
+const GemmTile* grouped_tiles(const moe_grouped_params* p) {
+  return p->op == MOE_GROUPED_WGRAD ? kWgradTiles : kBf16GemmTileTable;
+}
+
+// an id the call's sizes can take
+bool grouped_tile_ok(const moe_grouped_params* p) {
+  return p->tile == 0 || (p->tile <= kBf16GemmTiles && grouped_tiles(p)[p->tile - 1].tm > 0);
+}
+
+GemmArgs grouped_args(const moe_grouped_params* p) {
+  GemmArgs a{};
+  a.ld_x = p->ld_x;
+  a.ld_w = p->ld_w;
+  a.ld_y = p->ld_y;
+  a.es_w = p->expert_stride_w;
+  a.op = p->op;
+  a.L = p->num_experts;
+  a.rows = (int)p->rows;
+  a.n = p->n;
+  a.k = p->k;
+  a.out_bf16 = p->out_dtype == MOE_Y_BF16;
+  a.accumulate = p->accumulate != 0;
+  a.expected = expected_rows(p->expected_rows, p->rows);
+  a.splits = 1;
+  return a;
+}
+
+int32_t grouped(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w, void* y, int splits,
+                void* workspace, int64_t bytes, hipStream_t stream) {
+  const bool wgrad = p->op == MOE_GROUPED_WGRAD, fwd = p->op == MOE_GROUPED_FORWARD;
+  if (p->rows == 0 && (!wgrad || p->accumulate)) return MOE_OK;
+  if (!row_offset || !w || (p->rows && (!x || !y))) return MOE_ERR_INVALID_ARG;
+  const size_t oe = p->out_dtype == MOE_Y_BF16 ? 2 : 4;
+  if (!aligned(x, !fwd && !wgrad ? oe : 2) || !aligned(y, fwd ? oe : 2) || !aligned(w, wgrad ? oe : 2) ||
+      !aligned(workspace, 16))
+    return MOE_ERR_INVALID_ARG;
+  GemmArgs a = grouped_args(p);
+  a.row_offset = row_offset;
+  a.x = x;
+  a.w = w;
+  a.y = y;
+  const bool fast = grouped_fast(p) && aligned(x, 16) && aligned(w, 16) && aligned(y, 16);
+  if (!grouped_tile_ok(p) || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
+  if (!fast) return done(launch_gemm_any(a, false, stream));
+  const long long room = workspace ? bytes / 4 : 0;
+  if (splits > 1 && splits * split_args(a, nullptr).part > room) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return run(a, choose(grouped_tiles(p), kBf16GemmTiles, a, 64, p->tile, splits, room), static_cast<float*>(workspace),
+             stream, launch_gemm_bf16);
+}
+
+bool fp8_ok(const moe_fp8_params* p) {
+  return p && p->num_experts >= 1 && p->num_experts <= MOE_MAX_LOCAL_EXPERTS && p->rows >= 0 && p->rows <= kMaxRows &&
+         p->expected_rows >= 0 && p->n >= 1 && p->n <= kMaxCols && p->k >= 1 && p->k <= kMaxCols &&
+         stride_ok(p->ld_x, p->k) && stride_ok(p->ld_w, p->k) && stride_ok(p->ld_y, p->n) &&
+         stride_ok(p->ld_xs, (p->k + 127) / 128) &&
+         matrix_stride_ok(p->expert_stride_w, p->num_experts, p->n, p->ld_w, p->k) && dtype_ok(p->out_dtype) &&
+         p->tile >= 0;
+}
+
+bool fp8_fast(const moe_fp8_params* p) {
+  return p->n % 8 == 0 && p->k % 16 == 0 && p->ld_x % 16 == 0 && p->ld_w % 16 == 0 && p->ld_y % 8 == 0 &&
+         p->expert_stride_w % 16 == 0 && std::max(p->ld_x, std::max(p->ld_w, p->ld_xs)) <= (1 << 22);
+}
+
+GemmArgs fp8_args(const moe_fp8_params* p) {
+  GemmArgs a{};
+  a.ld_x = p->ld_x;
+  a.ld_w = p->ld_w;
+  a.ld_y = p->ld_y;
+  a.es_w = p->expert_stride_w;
+  a.ld_xs = p->ld_xs;
+  a.op = MOE_GROUPED_FORWARD;
+  a.L = p->num_experts;
+  a.rows = (int)p->rows;
+  a.n = p->n;
+  a.k = p->k;
+  a.out_bf16 = p->out_dtype == MOE_Y_BF16;
+  a.expected = expected_rows(p->expected_rows, p->rows);
+  a.splits = 1;
+  return a;
+}
+
+int32_t fp8(const moe_fp8_params* p, const int32_t* row_offset, const void* x, const float* x_scales, const void* w,
+            const float* w_scales, void* y, int splits, void* workspace, int64_t bytes, hipStream_t stream) {
+  if (!row_offset && p->num_experts != 1) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!x || !x_scales || !w || !w_scales || !y || !aligned(y, p->out_dtype == MOE_Y_BF16 ? 2 : 4) || !aligned(workspace, 16))
+    return MOE_ERR_INVALID_ARG;
+  GemmArgs a = fp8_args(p);
+  a.row_offset = row_offset;
+  a.x = const_cast<void*>(x);
+  a.w = const_cast<void*>(w);
+  a.y = y;
+  a.xs = x_scales;
+  a.ws = w_scales;
+  const bool fast = fp8_fast(p) && aligned(x, 16) && aligned(w, 16) && aligned(y, 16);
+  if (p->tile > kFp8GemmTiles || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
+  if (!fast) return done(launch_gemm_any(a, true, stream));
+  const long long room = workspace ? bytes / 4 : 0;
+  if (splits > 1 && splits * split_args(a, nullptr).part > room) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return run(a, choose(kFp8GemmTileTable, kFp8GemmTiles, a, 128, p->tile, splits, room), static_cast<float*>(workspace),
+             stream, launch_gemm_fp8);
 }
 
 }  // namespace
@@ -136,46 +293,19 @@ int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t
 
 int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w, void* y,
                            void* stream) {
-  if (!p || p->op < MOE_GROUPED_FORWARD || p->op > MOE_GROUPED_WGRAD || p->num_experts < 1 ||
-      p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows || p->expected_rows < 0 ||
-      p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || !stride_ok(p->ld_x, p->k) ||
-      !stride_ok(p->ld_w, p->k) || !stride_ok(p->ld_y, p->n) ||
-      !matrix_stride_ok(p->expert_stride_w, p->num_experts, p->n, p->ld_w, p->k) ||
-      !dtype_ok(p->out_dtype) || p->tile < 0)
-    return MOE_ERR_INVALID_ARG;
-  const bool wgrad = p->op == MOE_GROUPED_WGRAD, fwd = p->op == MOE_GROUPED_FORWARD;
-  if (p->accumulate && !wgrad) return MOE_ERR_INVALID_ARG;
-  if (p->rows == 0 && (!wgrad || p->accumulate)) return MOE_OK;
-  if (!row_offset || !w || (p->rows && (!x || !y))) return MOE_ERR_INVALID_ARG;
-  const size_t oe = p->out_dtype == MOE_Y_BF16 ? 2 : 4;
-  if (!aligned(x, !fwd && !wgrad ? oe : 2) || !aligned(y, fwd ? oe : 2) || !aligned(w, wgrad ? oe : 2))
-    return MOE_ERR_INVALID_ARG;
-  GemmArgs a{};
-  a.row_offset = row_offset;
-  a.x = x;
-  a.w = w;
-  a.y = y;
-  a.ld_x = p->ld_x;
-  a.ld_w = p->ld_w;
-  a.ld_y = p->ld_y;
-  a.es_w = p->expert_stride_w;
-  a.op = p->op;
-  a.L = p->num_experts;
-  a.rows = (int)p->rows;
-  a.n = p->n;
-  a.k = p->k;
-  a.out_bf16 = p->out_dtype == MOE_Y_BF16;
-  a.accumulate = p->accumulate != 0;
-  a.expected = expected_rows(p->expected_rows, p->rows);
-  // The 16-byte kernels: rows of every operand start and end on 16 bytes, and
-  // their lane offsets (256 rows of a tile) fit 32 bits.
-  const bool fast = aligned(x, 16) && aligned(w, 16) && aligned(y, 16) && p->n % 8 == 0 && p->k % 8 == 0 &&
-                    p->ld_x % 8 == 0 && p->ld_w % 8 == 0 && p->ld_y % 8 == 0 && p->expert_stride_w % 8 == 0 &&
-                    std::max(p->ld_x, std::max(p->ld_w, p->ld_y)) <= (1 << 22);
-  const GemmTile* tiles = wgrad ? kWgradTiles : kBf16GemmTileTable;
-  if (p->tile > kBf16GemmTiles || (p->tile > 0 && (!fast || tiles[p->tile - 1].tm == 0))) return MOE_ERR_UNSUPPORTED;
-  if (!fast) return done(launch_gemm_any(a, false, (hipStream_t)stream));
-  return done(launch_gemm_bf16(p->tile > 0 ? p->tile : choose(tiles, kBf16GemmTiles, a, 64), a, (hipStream_t)stream));
+  if (!grouped_ok(p)) return MOE_ERR_INVALID_ARG;
+  return grouped(p, row_offset, x, w, y, 1, nullptr, 0, (hipStream_t)stream);
+}
+
+int32_t moe_grouped_matmul_split(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w, void* y,
+                                 void* workspace, void* stream) {
+  if (!grouped_ok(p) || !split_ok(p->splits, p->workspace_bytes)) return MOE_ERR_INVALID_ARG;
+  return grouped(p, row_offset, x, w, y, p->splits, workspace, p->workspace_bytes, (hipStream_t)stream);
+}
+
+int64_t moe_grouped_workspace_bytes(const moe_grouped_params* p) {
+  if (!grouped_ok(p) || !split_ok(p->splits, 0) || !grouped_fast(p) || !grouped_tile_ok(p)) return 0;
+  return workspace_of(grouped_tiles(p), kBf16GemmTiles, grouped_args(p), 64, p->tile, p->splits);
 }
 
 int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_weight, const int32_t* row_offset,
@@ -269,40 +399,19 @@ int32_t moe_quantize_fp8(const moe_quantize_params* p, const void* x, const int3
 
 int32_t moe_fp8_matmul(const moe_fp8_params* p, const int32_t* row_offset, const void* x, const float* x_scales,
                        const void* w, const float* w_scales, void* y, void* stream) {
-  if (!p || p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows ||
-      p->expected_rows < 0 || p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols || !stride_ok(p->ld_x, p->k) ||
-      !stride_ok(p->ld_w, p->k) || !stride_ok(p->ld_y, p->n) || !stride_ok(p->ld_xs, (p->k + 127) / 128) ||
-      !matrix_stride_ok(p->expert_stride_w, p->num_experts, p->n, p->ld_w, p->k) || !dtype_ok(p->out_dtype) || p->tile < 0)
-    return MOE_ERR_INVALID_ARG;
-  if (!row_offset && p->num_experts != 1) return MOE_ERR_INVALID_ARG;
-  if (p->rows == 0) return MOE_OK;
-  if (!x || !x_scales || !w || !w_scales || !y || !aligned(y, p->out_dtype == MOE_Y_BF16 ? 2 : 4))
-    return MOE_ERR_INVALID_ARG;
-  GemmArgs a{};
-  a.row_offset = row_offset;
-  a.x = const_cast<void*>(x);
-  a.w = const_cast<void*>(w);
-  a.y = y;
-  a.xs = x_scales;
-  a.ws = w_scales;
-  a.ld_x = p->ld_x;
-  a.ld_w = p->ld_w;
-  a.ld_y = p->ld_y;
-  a.es_w = p->expert_stride_w;
-  a.ld_xs = p->ld_xs;
-  a.op = MOE_GROUPED_FORWARD;
-  a.L = p->num_experts;
-  a.rows = (int)p->rows;
-  a.n = p->n;
-  a.k = p->k;
-  a.out_bf16 = p->out_dtype == MOE_Y_BF16;
-  a.expected = expected_rows(p->expected_rows, p->rows);
-  const bool fast = aligned(x, 16) && aligned(w, 16) && aligned(y, 16) && p->n % 8 == 0 && p->k % 16 == 0 &&
-                    p->ld_x % 16 == 0 && p->ld_w % 16 == 0 && p->ld_y % 8 == 0 && p->expert_stride_w % 16 == 0 &&
-                    std::max(p->ld_x, std::max(p->ld_w, p->ld_xs)) <= (1 << 22);
-  if (p->tile > kFp8GemmTiles || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
-  if (!fast) return done(launch_gemm_any(a, true, (hipStream_t)stream));
-  return done(launch_gemm_fp8(p->tile > 0 ? p->tile : choose(kFp8GemmTileTable, kFp8GemmTiles, a, 128), a, (hipStream_t)stream));
+  if (!fp8_ok(p)) return MOE_ERR_INVALID_ARG;
+  return fp8(p, row_offset, x, x_scales, w, w_scales, y, 1, nullptr, 0, (hipStream_t)stream);
+}
+
+int32_t moe_fp8_matmul_split(const moe_fp8_params* p, const int32_t* row_offset, const void* x, const float* x_scales,
+                             const void* w, const float* w_scales, void* y, void* workspace, void* stream) {
+  if (!fp8_ok(p) || !split_ok(p->splits, p->workspace_bytes)) return MOE_ERR_INVALID_ARG;
+  return fp8(p, row_offset, x, x_scales, w, w_scales, y, p->splits, workspace, p->workspace_bytes, (hipStream_t)stream);
+}
+
+int64_t moe_fp8_workspace_bytes(const moe_fp8_params* p) {
+  if (!fp8_ok(p) || !split_ok(p->splits, 0) || !fp8_fast(p) || p->tile > kFp8GemmTiles) return 0;
+  return workspace_of(kFp8GemmTileTable, kFp8GemmTiles, fp8_args(p), 128, p->tile, p->splits);
 }
 
 }  // extern "C"

@@ -95,6 +95,17 @@ __device__ __forceinline__ void tile_at(int t, int mi, int ni, int& i, int& j) {
   i = g * 4 + rem - j * h;
 }
 
+// Range s of `splits` of a sum over nc, in whole stages of BK: where it starts
+// and how much it adds up (nothing, if earlier ranges took all)
+template <int BK>
+__device__ __forceinline__ int split_range(int nc, int splits, int s, int& c0) {
+  c0 = 0;
+  if (splits == 1) return nc;
+  const int stages = (nc + BK - 1) / BK, each = (stages + splits - 1) / splits * BK;
+  c0 = min(s * each, nc);
+  return min(nc - c0, each);
+}
+
 // Rows to work on: all of them, or row_offset[0] .. row_offset[L]-1.
 __device__ __forceinline__ void row_range(const int32_t* off, int L, long long rows, int& lo, int& hi) {
   lo = off ? clamped_offset(off, L, (int)rows, 0) : 0;

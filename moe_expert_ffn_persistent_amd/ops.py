@@ -6,8 +6,8 @@ with block scales and the block-scaled e4m3 product.
 Every call checks its tensors on the host (ValueError before anything is
 enqueued), enqueues one or a few kernels on ``stream`` (a torch.cuda.Stream;
 default: the current stream of the tensors' device) and returns without waiting. With
-``out`` given nothing is allocated and the call may be captured in a HIP
-graph. ``out`` must not overlap an input unless a function says it may. When a
+``out`` given nothing is allocated, but for the workspace of a product that cuts
+its sum (see grouped_matmul), and the call may be captured in a HIP graph. ``out`` must not overlap an input unless a function says it may. When a
 call allocates its output, rows that no expert owns hold whatever the memory
 held. Tensors used on a stream other than the one they were allocated on need
 the caller's ``record_stream``, as everywhere in torch.
@@ -163,6 +163,10 @@ def _check_stream(stream, device):
         raise ValueError(f"stream: of device {at}, the tensors are on device {device}")
 
 
+# products that may take a workspace, their last pointer, and what says its size
+_WORKSPACE = {"moe_grouped_matmul_split": "moe_grouped_workspace_bytes", "moe_fp8_matmul_split": "moe_fp8_workspace_bytes"}
+
+
 def _call(name, check, args, plain, tensors, stream):
     """One C entry point, ``tensors`` its pointers in order. ``check(*args)``
     makes its parameters from their sizes and the ``plain`` arguments; for
@@ -172,15 +176,18 @@ def _call(name, check, args, plain, tensors, stream):
     if entry is not None:
         device = _get_device()
         if stream is None:
-            s = _raw_stream(device)
+            st = _again(entry, device, _raw_stream(device), True, plain, *tensors)
+        elif getattr(stream, "device_index", None) == device:
+            st = _again(entry, device, stream.cuda_stream, False, plain, *tensors)
+            if st is False:   # a workspace, from the memory of that stream
+                with torch.cuda.stream(stream):
+                    st = _again(entry, device, stream.cuda_stream, True, plain, *tensors)
         else:
-            s = stream.cuda_stream if getattr(stream, "device_index", None) == device else None
-        if s is not None:
-            st = _again(entry, device, s, plain, *tensors)
-            if st is not None:
-                if st != _lib.MOE_OK:
-                    _lib.check(st, name)
-                return
+            st = None
+        if st is not None:
+            if st != _lib.MOE_OK:
+                _lib.check(st, name)
+            return
     _first_call(name, check, args, plain, tensors, stream)
 
 
@@ -191,17 +198,24 @@ def _first_call(name, check, args, plain, tensors, stream):
     _need_device(device)
     if stream is not None:
         _check_stream(stream, device.index)
-    fn = getattr(_lib.load(), name)
+    lib = _lib.load()
+    fn = getattr(lib, name)
     if _again is None:
         call = _lib.load_opcall()
         _again, _remember = call.again, call.remember
+    pointers = [_ptr(t) for t in tensors]
+    need = 0
+    if name in _WORKSPACE:
+        need = params.workspace_bytes = getattr(lib, _WORKSPACE[name])(ctypes.byref(params))
+        workspace = _empty((need,), torch.uint8, device, stream) if need else None
+        pointers[-1] = _ptr(workspace)
     with torch.cuda.device(device):
         s = _raw_stream(device.index) if stream is None else stream.cuda_stream
-        st = fn(ctypes.byref(params), *map(_ptr, tensors), s)
+        st = fn(ctypes.byref(params), *pointers, s)
     if st != _lib.MOE_OK:
         _lib.check(st, name)
     entry = _ENTRY[name] = ctypes.cast(fn, ctypes.c_void_p).value
-    _remember(bytes(params), entry, device.index, plain, *tensors)
+    _remember(bytes(params), entry, device.index, need, plain, *tensors)
 
 
 # ---- rows to and from the experts -------------------------------------------
@@ -271,7 +285,7 @@ def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stre
 
 # ---- matrix products grouped by expert ---------------------------------------
 
-def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate=False, tile=0):
+def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate=False, tile=0, splits=0):
     """x [rows, k], w [L, n, k], y [rows, n]; the operand that ``op`` writes is
     bf16 or fp32, the others bf16."""
     bf16, out = (torch.bfloat16,), tuple(_OUT)
@@ -287,42 +301,47 @@ def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate
     _on(x.device, ("rows", x), ("weights", w), ("rows", y), ("row_offset", row_offset))
     written = x if op == MOE_GROUPED_DGRAD else w if op == MOE_GROUPED_WGRAD else y
     return MoeGroupedParams(op, L, x.shape[0], _expected(expected_rows), n, k, ldx, ldw, ldy,
-                            _batch_stride(w, "weights", ldw), _OUT[written.dtype], int(accumulate), tile)
+                            _batch_stride(w, "weights", ldw), _OUT[written.dtype], int(accumulate), tile, splits)
 
 
-def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, tile, stream):
-    _call("moe_grouped_matmul", check_grouped_inputs, (op, x, w, y, row_offset, expected_rows, accumulate, tile),
-          (op, expected_rows, accumulate, tile), (row_offset, x, w, y), stream)
+def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, tile, splits, stream):
+    _call("moe_grouped_matmul_split", check_grouped_inputs,
+          (op, x, w, y, row_offset, expected_rows, accumulate, tile, splits),
+          (op, expected_rows, accumulate, tile, splits), (row_offset, x, w, y, None), stream)
 
 
-def grouped_matmul(x, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, tile=0, stream=None):
+def grouped_matmul(x, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, tile=0, splits=0,
+                   stream=None):
     """``out[r] = w[e] @ x[r]`` for the rows r of every expert e (row_offset
     [L+1]): x bf16 [rows, k], w bf16 [L, n, k], out [rows, n] bf16 or fp32.
     ``expected_rows`` (default: all rows of x) is how many rows the experts
     hold together, when the buffers have room for many more: it only chooses
-    the kernel's tile, which ``tile`` (0: automatic) names outright."""
+    the kernel's tile, which ``tile`` (0: automatic) names outright. With few
+    tiles and a long sum the sum is cut into ranges that are added up in a
+    workspace (allocated for the call) and joined; ``splits`` names their number
+    (0: automatic, 1: not cut and no workspace)."""
     if out is None:
         rows, _ = _sizes(x, "x", 2)
         _, n, _ = _sizes(w, "w", 3)
         out = _empty((rows, n), _out_type(out_dtype), x.device, stream)
-    _grouped(MOE_GROUPED_FORWARD, x, w, out, row_offset, expected_rows, False, tile, stream)
+    _grouped(MOE_GROUPED_FORWARD, x, w, out, row_offset, expected_rows, False, tile, splits, stream)
     return out
 
 
 def grouped_matmul_dgrad(dy, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, tile=0,
-                         stream=None):
+                         splits=0, stream=None):
     """Input gradient of grouped_matmul: ``out[r] = w[e].T @ dy[r]``; dy bf16
     [rows, n], out [rows, k] bf16 or fp32."""
     if out is None:
         rows, _ = _sizes(dy, "dy", 2)
         _, _, k = _sizes(w, "w", 3)
         out = _empty((rows, k), _out_type(out_dtype), dy.device, stream)
-    _grouped(MOE_GROUPED_DGRAD, out, w, dy, row_offset, expected_rows, False, tile, stream)
+    _grouped(MOE_GROUPED_DGRAD, out, w, dy, row_offset, expected_rows, False, tile, splits, stream)
     return out
 
 
 def grouped_matmul_wgrad(dy, x, row_offset, out=None, out_dtype=torch.bfloat16, accumulate=False,
-                         expected_rows=None, tile=0, stream=None):
+                         expected_rows=None, tile=0, splits=0, stream=None):
     """Weight gradient of grouped_matmul: ``out[e] = sum over its rows of the
     outer products dy[r] x[r]``, [L, n, k] bf16 or fp32; an expert without rows
     gets zeros. With ``accumulate`` the sums are added to ``out``."""
@@ -332,7 +351,7 @@ def grouped_matmul_wgrad(dy, x, row_offset, out=None, out_dtype=torch.bfloat16, 
         _, n = _sizes(dy, "dy", 2)
         _, k = _sizes(x, "x", 2)
         out = _empty((_offsets(row_offset), n, k), _out_type(out_dtype), x.device, stream)
-    _grouped(MOE_GROUPED_WGRAD, x, out, dy, row_offset, expected_rows, accumulate, tile, stream)
+    _grouped(MOE_GROUPED_WGRAD, x, out, dy, row_offset, expected_rows, accumulate, tile, splits, stream)
     return out
 
 
@@ -478,7 +497,7 @@ def quantize_fp8(x, block_rows=1, row_offset=None, out=None, scales=None, stream
     return out, scales
 
 
-def check_fp8_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None, tile=0):
+def check_fp8_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None, tile=0, splits=0):
     ldx = _matrix(x, "x", _CODES)
     grouped = row_offset is not None
     ldw = _matrix(w, "w", _CODES, 3 if grouped else 2)
@@ -504,20 +523,21 @@ def check_fp8_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None
         es = _batch_stride(w, "w", ldw)
     _on(x.device, ("x", x), ("x_scales", x_scales), ("w", w), ("w_scales", w_scales), ("row_offset", row_offset), ("out", y))
     return MoeFp8Params(L, rows, _expected(expected_rows), n, k, ldx, ldxs, ldw, ldy, es, _OUT[y.dtype],
-                        tile)
+                        tile, splits)
 
 
 def fp8_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=torch.bfloat16, expected_rows=None,
-               tile=0, stream=None):
+               tile=0, splits=0, stream=None):
     """``out = (x * x_scales) @ (w * w_scales).T`` of e4m3 operands: x [rows, k]
     with scales [rows, ceil(k/128)], w [n, k] with scales [ceil(n/128),
     ceil(k/128)]; grouped by expert with ``row_offset``: w [L, n, k], w_scales
     [L, ...], every row times its expert's matrix. out [rows, n] bf16 or fp32.
-    ``expected_rows`` and ``tile`` as for grouped_matmul."""
+    ``expected_rows``, ``tile`` and ``splits`` as for grouped_matmul."""
     if out is None:
         rows, _ = _sizes(x, "x", 2)
         n = _sizes(w, "w", 2 if row_offset is None else 3)[-2]
         out = _empty((rows, n), _out_type(out_dtype), x.device, stream)
-    _call("moe_fp8_matmul", check_fp8_inputs, (x, x_scales, w, w_scales, row_offset, out, expected_rows, tile),
-          (expected_rows, tile), (row_offset, x, x_scales, w, w_scales, out), stream)
+    _call("moe_fp8_matmul_split", check_fp8_inputs,
+          (x, x_scales, w, w_scales, row_offset, out, expected_rows, tile, splits), (expected_rows, tile, splits),
+          (row_offset, x, x_scales, w, w_scales, out, None), stream)
     return out

@@ -95,7 +95,7 @@ def call(op, x, w, y, off, **kw):
     return moe.grouped_matmul_wgrad(y, x, off, out=w, **kw)
 
 
-def run_grouped(op, counts, k, n, out_dtype, seed, first=0, behind=0, pad=0, lead=0, expected_rows=None, tile=0):
+def run_grouped(op, counts, k, n, out_dtype, seed, first=0, behind=0, pad=0, lead=0, expected_rows=None, tile=0, splits=0):
     """One grouped product with NaN in every row that no expert owns and a
     sentinel in the output, checked against 64 bits."""
     g = gen(seed)
@@ -114,7 +114,7 @@ def run_grouped(op, counts, k, n, out_dtype, seed, first=0, behind=0, pad=0, lea
         w = torch.full((L, n, k), 7.0, dtype=out_dtype)
     dx, dw, dy = strided(x, pad, lead), strided(w, pad, lead), strided(y, pad, lead)
     say(f"op={op} counts={counts if L < 9 else L} k={k} n={n} out={out_dtype} first={first} behind={behind} pad={pad} lead={lead}")
-    got = call(op, dx, dw, dy, up(off), expected_rows=expected_rows, tile=tile)
+    got = call(op, dx, dw, dy, up(off), expected_rows=expected_rows, tile=tile, splits=splits)
     torch.cuda.synchronize()
     if op == WGRAD:
         assert_close(got, ref, out_dtype, mag, terms, f"wgrad {counts}")
@@ -564,7 +564,7 @@ def test_fp8_every_tile(counts, R, K, n, tile, out_dtype):
     run_fp8(counts, R, K, n, out_dtype, behind=3 if counts else 0, pad=16, tile=tile)
 
 
-def run_fp8(counts, R, K, n, out_dtype, pad=0, lead=0, behind=0, expected_rows=None, tile=0):
+def run_fp8(counts, R, K, n, out_dtype, pad=0, lead=0, behind=0, expected_rows=None, tile=0, splits=0):
     g = gen(R + K + n)
     rows = R + behind
     L = 0 if counts is None else len(counts)
@@ -578,7 +578,7 @@ def run_fp8(counts, R, K, n, out_dtype, pad=0, lead=0, behind=0, expected_rows=N
     y = torch.full((rows, n), 7.0, dtype=out_dtype)
     say(f"fp8 counts={counts} R={R} K={K} n={n} {out_dtype} pad={pad} lead={lead}")
     got = moe.fp8_matmul(strided(x, pad, lead), strided(xs, 1 if pad else 0), strided(w, pad, lead), up(ws), row_offset=None if counts is None else up(off),
-                         out=strided(y, pad, lead), expected_rows=expected_rows, tile=tile).cpu()
+                         out=strided(y, pad, lead), expected_rows=expected_rows, tile=tile, splits=splits).cpu()
     assert_close(got[:R], ref[:R], out_dtype, mag[:R], K, f"fp8 {counts} {K} {n}", DROP)
     assert (got[R:] == 7).all()
 

@@ -159,12 +159,8 @@ PyObject* again(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     if (args[3] != Py_True) Py_RETURN_FALSE;
     try {
       workspace = at::empty({plan.workspace}, at::TensorOptions().dtype(at::kByte).device(c.device));
-    } catch (const c10::OutOfMemoryError& e) {
-      PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
-      return nullptr;
-    } catch (const std::exception& e) {
-      PyErr_SetString(PyExc_RuntimeError, e.what());
-      return nullptr;
+    } catch (...) {
+      Py_RETURN_NONE;   // the call in Python meets the same and raises it
     }
     ptr[n - 1] = workspace.data_ptr();
   }

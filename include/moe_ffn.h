@@ -536,7 +536,8 @@ int32_t moe_swiglu_backward(const moe_swiglu_params* p, const void* a, const voi
  * format: blocks of block_rows x 128 elements (edge blocks are smaller), scale
  * = fp32(amax / 448), 1 where that is zero; code = the e4m3 value nearest to
  * fp32(x / scale), ties to even. A block with an infinity or NaN gets that as
- * its scale and NaN codes.
+ * its scale and NaN codes. Matrices of 2^23 or more 128 x 128 blocks are
+ * MOE_ERR_UNSUPPORTED.
  *   x       [batch, rows, cols] bf16 or fp32
  *   codes   e4m3 bytes [batch, rows, cols]
  *   scales  fp32 [batch, ceil(rows/block_rows), ceil(cols/128)], contiguous

@@ -381,7 +381,8 @@ int32_t moe_quantize_fp8(const moe_quantize_params* p, const void* x, const int3
   if (!matrix_stride_ok(p->batch_stride_x, p->batch, p->rows, p->ld_x, p->cols) ||
       !matrix_stride_ok(p->batch_stride_codes, p->batch, p->rows, p->ld_codes, p->cols))
     return MOE_ERR_INVALID_ARG;
-  if (p->block_rows == 128 && ((p->rows + 127) / 128) * ((p->cols + 127) / 128) > (1ll << 23))
+  // a workgroup of 512 threads a block, and fewer than 2^32 threads a launch
+  if (p->block_rows == 128 && ((p->rows + 127) / 128) * ((p->cols + 127) / 128) >= (1ll << 23))
     return MOE_ERR_UNSUPPORTED;
   const bool fp32 = p->in_dtype == MOE_Y_FP32;
   const int xe = fp32 ? 4 : 2;

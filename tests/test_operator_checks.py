@@ -397,3 +397,10 @@ def test_c_refuses_sizes_that_would_overflow(name, kw):
     if name == "moe_quantize_fp8":
         args[1] = None
     assert _call(name, params, *args) == _lib.MOE_ERR_INVALID_ARG
+
+
+def test_c_quantize_blocks_of_one_launch():
+    # 2^23 blocks of 512 threads would be 2^32 threads
+    base = dict(rows=1 << 23, batch=1, cols=1 << 14, block_rows=128, in_dtype=1, num_experts=0, ld_x=1 << 14,
+                ld_codes=1 << 14, batch_stride_x=0, batch_stride_codes=0)
+    assert _call("moe_quantize_fp8", _lib.MoeQuantizeParams(*base.values()), 16, None, 16, 16) == _lib.MOE_ERR_UNSUPPORTED

@@ -50,7 +50,7 @@ struct CfgG {
   static constexpr int KW = KW_;
   static constexpr int NW = WT * WF, THREADS = 64 * NW * KW;
   static constexpr int TT = TM / WT, FT = TN / WF; // rows and columns of a wavefront
-  static constexpr int TB = TT / 32, FB = FT / 32;
+  static constexpr int TB = TT > 32 ? TT / 32 : 1, FB = FT / 32;   // 16 rows fill half a block
   static constexpr int T_BYTES = TM * kBK * 2, F_BYTES = TN * kBK * 2;
   static constexpr int STAGE = T_BYTES + F_BYTES;
   static constexpr int NIT = T_BYTES / 1024 / NW, NIF = F_BYTES / 1024 / NW, NI = NIT + NIF;
@@ -58,7 +58,7 @@ struct CfgG {
   static constexpr int RING = NS * STAGE;
   // the epilogue stages behind the next tile's first stage
   static constexpr int LDS = KW > 1 || RING >= STAGE + EPI ? KW * RING : STAGE + EPI;
-  static_assert(KW == 1 || (NW == 1 && TM == 32), "split wavefronts hold the whole tile each");
+  static_assert(KW == 1 || (NW == 1 && TM <= 32), "split wavefronts hold the whole tile each");
   static constexpr int issue_slot(int i, int nm) { return i * nm * SP / (NI * 8); }
   static_assert(T_BYTES % (1024 * NW) == 0 && F_BYTES % (1024 * NW) == 0, "copies split evenly over the wavefronts");
   static_assert(NS >= 2 && NI * (NS - 1) <= 63, "vmcnt range");
@@ -138,8 +138,8 @@ struct Operand {
   __device__ __forceinline__ static bf16x8 frag(const char* stage, int x0, int ks) {
     const int lane = threadIdx.x & 63;
     if constexpr (!TR) {
-      const int r = x0 + (lane & 31);
-      const int c = (2 * ks + (lane >> 5)) ^ swz(lane & 31);   // x0 is a multiple of 32
+      const int r31 = lane & (TX < 32 ? TX - 1 : 31), r = x0 + r31;
+      const int c = (2 * ks + (lane >> 5)) ^ swz(r31);   // x0 is a multiple of 32
       return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(stage + r * RB + c * 16));
     } else {
       // lane 16 q + i addresses row (i / 4) of its group's four, 8 bytes at
@@ -219,7 +219,7 @@ struct TileG {
   // All of c, `nc` of them (with KW > 1, the stages kw, kw + KW, ... of them),
   // the first stage's copies already issued.
   template <int NTB>
-  __device__ __forceinline__ void mainloop(char* lds, int nc, int wf, int wt, int kw) {
+  __device__ __forceinline__ void mainloop(char* lds, int nc, int wf, int wt, int kw, bool fresh) {
 #pragma unroll
     for (int fb = 0; fb < C::FB; ++fb)
 #pragma unroll
@@ -237,10 +237,13 @@ struct TileG {
     };
     if constexpr (C::NS > 2) {
       // The other slots may hold the previous tile's staging: every wavefront is
-      // past it. Its stores are drained with the first stage, so that the counts
-      // below see copies only.
-      vm_wait<0>();
-      if constexpr (C::KW == 1) lds_barrier();
+      // past it. Its stores came after the first stage's copies, and are drained
+      // so that the counts below see copies only; without stores in between
+      // (fresh) all stages are on their way at once.
+      if (!fresh) {
+        vm_wait<0>();
+        if constexpr (C::KW == 1) lds_barrier();
+      }
 #pragma unroll
       for (int s = 1; s < C::NS - 1; ++s) {
         if (s < full) {
@@ -274,18 +277,18 @@ struct TileG {
   // The tile's `rows` rows (at least one): 32-row blocks go to the row
   // wavefronts in turn, so a short tile keeps all of them equally busy with
   // fewer MFMAs.
-  __device__ __forceinline__ void multiply(char* lds, int rows, int nc, int wf, int wt, int kw) {
+  __device__ __forceinline__ void multiply(char* lds, int rows, int nc, int wf, int wt, int kw, bool fresh) {
     const int blocks = (min(rows, C::TM) + 32 * C::WT - 1) / (32 * C::WT);
     if constexpr (C::TB >= 2) {
-      if (blocks == 1) return mainloop<1>(lds, nc, wf, wt, kw);
+      if (blocks == 1) return mainloop<1>(lds, nc, wf, wt, kw, fresh);
     }
     if constexpr (C::TB >= 3) {
-      if (blocks == 2) return mainloop<2>(lds, nc, wf, wt, kw);
+      if (blocks == 2) return mainloop<2>(lds, nc, wf, wt, kw, fresh);
     }
     if constexpr (C::TB >= 4) {
-      if (blocks == 3) return mainloop<3>(lds, nc, wf, wt, kw);
+      if (blocks == 3) return mainloop<3>(lds, nc, wf, wt, kw, fresh);
     }
-    mainloop<C::TB>(lds, nc, wf, wt, kw);
+    mainloop<C::TB>(lds, nc, wf, wt, kw, fresh);
   }
 
   // KW > 1: the wavefronts' sums to LDS, joined in their order and written out.
@@ -303,7 +306,7 @@ struct TileG {
             float4{v[g4 * 4], v[g4 * 4 + 1], v[g4 * 4 + 2], v[g4 * 4 + 3]};
       }
     __syncthreads();
-    for (int idx = threadIdx.x; idx < 32 * NCH; idx += C::THREADS) {
+    for (int idx = threadIdx.x; idx < C::TM * NCH; idx += C::THREADS) {
       const int r = idx / NCH, c = idx - r * NCH, i = i0 + r, col = j0 + c * 4;
       if (i >= ni || col >= nj) continue;
       float4 s = *reinterpret_cast<const float4*>(lds + stage_off<ROWB>(r, c * 16));
@@ -468,9 +471,10 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
 
   Work cur, next;
   int b = blockIdx.x;
-  bool more = start(b, cur);
+  bool more = start(b, cur), fresh = true;
   while (more) {
-    g.multiply(ring, cur.ni - cur.i0, cur.nc, wf, wt, kw);
+    g.multiply(ring, cur.ni - cur.i0, cur.nc, wf, wt, kw, fresh);
+    fresh = C::KW > 1;   // split wavefronts store before they copy
     b += gridDim.x;
     const bool write = !WG || cur.nc > 0 || !a.accumulate;
     if constexpr (C::KW == 1) {
@@ -501,6 +505,7 @@ using Deep = CfgG<128, 128, 2, 4, 4, 4, 1>;
 using Small = CfgG<64, 128, 1, 4, 3, 4, 2>;
 using Split = CfgG<32, 32, 1, 1, 2, 4, 1, 8>;
 using Split64 = CfgG<32, 64, 1, 1, 3, 4, 1, 4>;
+using Few = CfgG<16, 32, 1, 1, 3, 4, 1, 8>;   // few rows: fewer bytes a stage, more stages on their way
 
 template <class C>
 constexpr GemmTile timed(double a, double c, double b, double o, bool once = false) {
@@ -539,6 +544,7 @@ hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
       case 6: return launch<Split, OP>(a, s);
       case 7: return launch<Split64, OP>(a, s);
       case 8: return launch<Deep, OP>(a, s);
+      case 9: return launch<Few, OP>(a, s);
     }
   }
   return hipErrorInvalidValue;
@@ -550,10 +556,10 @@ hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
 const GemmTile kBf16GemmTileTable[] = {
     timed<Large>(0.84, 1.56, 1.56, 4),  timed<Wide>(0.73, 1.27, 1.27, 4),  timed<Medium>(0.48, 0.90, 0.90, 5),
     timed<Square>(0.47, 0.79, 0.54, 2), timed<Small>(0.22, 0.37, 0.32, 4), timed<Split>(0.78, 0.96, 0.96, 1),
-    timed<Split64>(0.52, 0.64, 0.64, 2), timed<Deep>(0.28, 0.48, 0.48, 5, true)};
+    timed<Split64>(0.52, 0.64, 0.64, 2), timed<Deep>(0.28, 0.48, 0.48, 5, true), timed<Few>(0.5, 0.5, 0.5, 1)};
 const GemmTile kWgradTiles[] = {
     timed<Large>(1.10, 1.79, 1.79, 6),  GemmTile{}, timed<Medium>(0.60, 0.96, 0.96, 4),
-    timed<Square>(0.47, 0.70, 0.47, 4), timed<Small>(0.32, 0.32, 0.32, 3), GemmTile{}, GemmTile{}, GemmTile{}};
+    timed<Square>(0.47, 0.70, 0.47, 4), timed<Small>(0.32, 0.32, 0.32, 3), GemmTile{}, GemmTile{}, GemmTile{}, GemmTile{}};
 
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s) {
   switch (a.op) {

@@ -45,24 +45,26 @@ struct CfgQ {
   static constexpr int KW = KW_, NW = WT * WF, THREADS = 64 * NW * KW;
   static constexpr int TT = TM / WT, FT = TN / WF;
   static constexpr int TB = TT / 16, FB = FT / 16, NB = TB * FB;   // 16 x 16 blocks of a wavefront
+  static constexpr int TP = TB > 1 ? TB / 2 : 1;                   // 32-row blocks
   static constexpr int NIT = TM * 128 / 1024 / NW, NIF = TN * 128 / 1024 / NW;
-  static constexpr int NI = NIT + NIF + 1;               // with the row-scale copy
-  static constexpr int F_BYTES = TN * 128, T_BYTES = TM * 128, S_BYTES = NW * 256;
+  static constexpr int NS_COPIES = KW > 1 ? 2 : 1;       // scales: rows', and weights' where no wavefront is left for them
+  static constexpr int NI = NIT + NIF + NS_COPIES;
+  static constexpr int F_BYTES = TN * 128, T_BYTES = TM * 128, S_BYTES = (NW + NS_COPIES - 1) * 256;
   static constexpr int STAGE = F_BYTES + T_BYTES + S_BYTES;
   static constexpr int EPI = NW * 16 * FT * 4;
   static constexpr int RING = NS * STAGE;
   static constexpr int LDS = KW * RING;
   static_assert(RING - STAGE >= EPI || KW > 1, "the epilogue stages behind the next tile's first stage");
-  static_assert(KW == 1 || (NW == 1 && TM == 32), "split wavefronts hold the whole tile each");
+  static_assert(KW == 1 || (NW == 1 && TM <= 32), "split wavefronts hold the whole tile each");
   // copies of a stage when only ntp 32-row blocks a wavefront hold rows, the
-  // row scales' last
-  static constexpr int copies(int ntp) { return NIF + NIT * ntp / (TB / 2) + 1; }
+  // scales' last
+  static constexpr int copies(int ntp) { return NIF + NIT * ntp / TP + NS_COPIES; }
   static constexpr int issue_slot(int i, int nb, int ni) { return i * nb * SP / (ni * 8); }
-  static_assert(NIT % (TB / 2) == 0, "copies of a row block");
-  static constexpr int NP = 4;                           // products in flight
+  static_assert(NIT % TP == 0, "copies of a row block");
+  static constexpr int NP = NB < 4 ? NB : 4;             // products in flight
   static_assert(16 * FT * 2 % 1024 == 0 || KW > 1, "a 16-row piece of the epilogue is whole stores");
   static_assert(FT <= 128 && 128 % FT == 0, "a wavefront's columns lie in one block of weight scales");
-  static_assert(NB % NP == 0 && TB % 2 == 0 && FB >= 2, "blocks of a wavefront");
+  static_assert(NB % NP == 0 && TB == 2 * TP - (TB == 1) && FB >= 2 && (NB > 2 || FB == 2), "blocks of a wavefront");
   static_assert(TM < 64 * NW || KW > 1, "row-scale copies cover the tile, a wavefront is left for the weight scales");
   static_assert((TM * 128) % (1024 * NW) == 0 && (TN * 128) % (1024 * NW) == 0, "copies split evenly");
   static_assert(NS >= 2 && NI * (NS - 1) <= 63, "vmcnt range");
@@ -80,7 +82,7 @@ __device__ __forceinline__ int chunk_in(int r, int p) {
 
 template <class C>
 struct TileQ {
-  const char *fbase, *tbase, *sbase;
+  const char *fbase, *tbase, *sbase, *wbase;
   uint32_t fv[C::NIF], tv[C::NIT], sv;
   f32x4 acc[C::FB][C::TB];
   f32x4 part[C::NP];
@@ -103,7 +105,8 @@ struct TileQ {
     slot = uni(slot);
     if (i < C::NIF) dma16s(fv[i], fbase + kt * 128ll, slot + (wave + C::NW * i) * 1024);
     else if (i < C::NIF + C::NIT) dma16s(tv[i - C::NIF], tbase + kt * 128ll, slot + C::F_BYTES + (wave + C::NW * (i - C::NIF)) * 1024);
-    else dma4s(sv, sbase + kt * 4ll, slot + C::F_BYTES + C::T_BYTES + wave * 256);
+    else if (i == C::NIF + C::NIT) dma4s(sv, sbase + kt * 4ll, slot + C::F_BYTES + C::T_BYTES + wave * 256);
+    else dma4s(0, wbase + kt * 4ll, slot + C::F_BYTES + C::T_BYTES + 256);
   }
 
   // the last block when it holds only `left` < 128 k: lanes past it write zeros
@@ -117,7 +120,8 @@ struct TileQ {
       if (in) issue(i, kt, (uint32_t)(uintptr_t)slot);
       else *reinterpret_cast<uint4*>(slot + (i < C::NIF ? 0 : C::F_BYTES) + (wave + C::NW * j) * 1024 + lane * 16) = uint4{0, 0, 0, 0};
     }
-    issue(C::NI - 1, kt, (uint32_t)(uintptr_t)slot);
+#pragma unroll
+    for (int i = C::NIF + C::NIT; i < C::NI; ++i) issue(i, kt, (uint32_t)(uintptr_t)slot);
   }
 
   __device__ __forceinline__ static i32x8 frag(const char* stage, int r, int c) {
@@ -127,19 +131,19 @@ struct TileQ {
     return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
   }
 
-  // One K block; sw: its weight scale (KW > 1; else it lies behind the row
-  // scales). The products of the stage's last two blocks are added during the
-  // first two MFMAs of the next one. Only the first NTP of the wavefront's
+  // One K block. The products of the stage's last two blocks are added during
+  // the first two MFMAs of the next one. Only the first NTP of the wavefront's
   // 32-row blocks are multiplied.
   template <bool COPY, int NTP>
-  __device__ __forceinline__ void compute(const char* stage, int wf, int wt, float sw, int kt_next, uint32_t slot) {
-    constexpr int TB = 2 * NTP, NB = C::FB * TB, NI = C::copies(NTP);
+  __device__ __forceinline__ void compute(const char* stage, int wf, int wt, int kt_next, uint32_t slot) {
+    constexpr int TB = C::TB == 1 ? 1 : 2 * NTP, NB = C::FB * TB, NI = C::copies(NTP);
     // row of 16-row block j: 32-row blocks go to the row wavefronts in turn
     auto row = [&](int j) { return ((j >> 1) * C::WT + wt) * 32 + (j & 1) * 16; };
     const int lane = threadIdx.x & 63, r16 = lane & 15, c0 = 2 * (lane >> 4);
     const char* ts = stage + C::F_BYTES;
     const float* sx = reinterpret_cast<const float*>(ts + C::T_BYTES) + r16;
-    if constexpr (C::KW == 1) sw = *(reinterpret_cast<const float*>(ts + C::T_BYTES) + C::TM + wf * C::FT / 128);
+    // behind the row scales, or (KW > 1) behind their 256 bytes
+    const float sw = *(reinterpret_cast<const float*>(ts + C::T_BYTES) + (C::KW > 1 ? 64 : C::TM + wf * C::FT / 128));
     i32x8 af[C::FB], bf[2];
     float st[2];
     bf[0] = frag(ts, row(0) + r16, c0);
@@ -151,9 +155,14 @@ struct TileQ {
       const int j = b / C::FB, i = b % C::FB;
       if (b + 1 < C::FB) af[b + 1] = frag(stage, wf * C::FT + (b + 1) * 16 + r16, c0);
       if (i == 0 && j + 1 < TB) bf[(j + 1) & 1] = frag(ts, row(j + 1) + r16, c0);
+      if constexpr (NB == 2) {   // before its place is taken
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[b][0][v] += part[b][v] * s_tail[b];
+      }
       part[b % C::NP] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j & 1], f32x4{}, 0, 0, 0, 127, 0, 127);
       const int q = b - 2;
-      if (q >= 0) {
+      if constexpr (NB == 2) {
+      } else if (q >= 0) {
         const float s = st[(q / C::FB) & 1];
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[q % C::FB][q / C::FB][v] += part[q % C::NP][v] * s;
@@ -166,7 +175,7 @@ struct TileQ {
       if constexpr (COPY) {
 #pragma unroll
         for (int k = 0; k < NI; ++k)
-          if (C::issue_slot(k, NB, NI) == b) issue(k + 1 == NI ? C::NI - 1 : k, kt_next, slot);
+          if (C::issue_slot(k, NB, NI) == b) issue(k + C::NS_COPIES >= NI ? C::NI - NI + k : k, kt_next, slot);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -186,7 +195,7 @@ struct TileQ {
   // All of K (with KW > 1, blocks kw, kw + KW, ...), the first stage's copies
   // already issued
   template <int NTP>
-  __device__ __forceinline__ void mainloop(char* lds, int K, const float* ws, int wf, int wt, int kw, int stores) {
+  __device__ __forceinline__ void mainloop(char* lds, int K, int wf, int wt, int kw, int stores, bool fresh) {
     constexpr int NI = C::copies(NTP);
 #pragma unroll
     for (int i = 0; i < C::FB; ++i)
@@ -196,55 +205,50 @@ struct TileQ {
 #pragma unroll
     for (int i = 0; i < C::NP; ++i) part[i] = f32x4{};
     s_tail[0] = s_tail[1] = 0.f;
-    const int lane = threadIdx.x & 63;
     const uint32_t ring = (uint32_t)(uintptr_t)lds;
-    const int all = K / 128, kb = (K + 127) / 128;
+    const int all = K / 128;
     const int left = all % C::KW == kw ? K % 128 : 0;
     const int full = C::KW == 1 ? all : (all - kw + C::KW - 1) / C::KW;
     const int nk = full + (left != 0);
     auto at = [&](int s) { return C::KW == 1 ? s : kw + C::KW * s; };
-    wait_first(stores);
+    // without stores since the first stage's copies (fresh) all stages are on
+    // their way at once, and counted below
+    if (!fresh) wait_first(stores);
     if constexpr (C::NS > 2) {
       // past the previous tile's staging
-      if constexpr (C::KW == 1) lds_barrier();
+      if constexpr (C::KW == 1) {
+        if (!fresh) lds_barrier();
+      }
 #pragma unroll
       for (int s = 1; s < C::NS - 1; ++s) {
         if (s < full) {
 #pragma unroll
-          for (int i = 0; i < NI; ++i) issue(i + 1 == NI ? C::NI - 1 : i, at(s), ring + s * C::STAGE);
+          for (int i = 0; i < NI; ++i) issue(i + C::NS_COPIES >= NI ? C::NI - NI + i : i, at(s), ring + s * C::STAGE);
         } else if (s < nk) {
           issue_tail(at(s), left, lds + s * C::STAGE);
         }
       }
     }
-    float wsv = 0.f;
-    auto scale = [&](int s) {
-      if constexpr (C::KW == 1) return 0.f;
-      if ((s & 63) == 0) wsv = ws[min(at(s + lane), kb - 1)];
-      return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv), s & 63));
-    };
     int slot = 0;
     const int nmain = full - (C::NS - 1);
     for (int s = 0; s < nmain; ++s) {
-      const float sw = scale(s);
-      if (s) vm_wait<NI * (C::NS - 2)>();   // the stage has landed (later ones may not have)
+      if (s || fresh) vm_wait<NI * (C::NS - 2)>();   // the stage has landed (later ones may not have)
       if constexpr (C::KW == 1) lds_barrier();
       const int nslot = slot == 0 ? C::NS - 1 : slot - 1;
-      compute<true, NTP>(lds + slot * C::STAGE, wf, wt, sw, at(s + C::NS - 1), ring + nslot * C::STAGE);
+      compute<true, NTP>(lds + slot * C::STAGE, wf, wt, at(s + C::NS - 1), ring + nslot * C::STAGE);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
     for (int s = max(nmain, 0); s < nk; ++s) {
-      const float sw = scale(s);
-      if (s == 0) {
+      if (s == 0 && !fresh) {
       } else if (left) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       else vm_wait_ahead<NI, C::NS - 2>(nk - 1 - s);
       if constexpr (C::KW == 1) lds_barrier();
       if (left && s + C::NS - 1 == full) issue_tail(at(full), left, lds + (full % C::NS) * C::STAGE);
-      compute<false, NTP>(lds + slot * C::STAGE, wf, wt, sw, 0, 0);
+      compute<false, NTP>(lds + slot * C::STAGE, wf, wt, 0, 0);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
     }
     if (nk > 0) {
-      constexpr int TB = 2 * NTP, NB = C::FB * TB;
+      constexpr int TB = C::TB == 1 ? 1 : 2 * NTP, NB = C::FB * TB;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         acc[C::FB - 2][TB - 1][v] += part[(NB - 2) % C::NP][v] * s_tail[0];
@@ -254,18 +258,19 @@ struct TileQ {
   }
 
   // The tile's `rows` rows (at least one)
-  __device__ __forceinline__ void multiply(char* lds, int rows, int K, const float* ws, int wf, int wt, int kw, int stores) {
+  __device__ __forceinline__ void multiply(char* lds, int rows, int K, int wf, int wt, int kw, int stores,
+                                           bool fresh) {
     const int blocks = (min(rows, C::TM) + 32 * C::WT - 1) / (32 * C::WT);
     if constexpr (C::TB >= 4) {
-      if (blocks == 1) return mainloop<1>(lds, K, ws, wf, wt, kw, stores);
+      if (blocks == 1) return mainloop<1>(lds, K, wf, wt, kw, stores, fresh);
     }
     if constexpr (C::TB >= 6) {
-      if (blocks == 2) return mainloop<2>(lds, K, ws, wf, wt, kw, stores);
+      if (blocks == 2) return mainloop<2>(lds, K, wf, wt, kw, stores, fresh);
     }
     if constexpr (C::TB >= 8) {
-      if (blocks == 3) return mainloop<3>(lds, K, ws, wf, wt, kw, stores);
+      if (blocks == 3) return mainloop<3>(lds, K, wf, wt, kw, stores, fresh);
     }
-    mainloop<C::TB / 2>(lds, K, ws, wf, wt, kw, stores);
+    mainloop<C::TP>(lds, K, wf, wt, kw, stores, fresh);
   }
 
   // The first stage's copies have landed. They were issued before the previous
@@ -292,7 +297,7 @@ struct TileQ {
         *reinterpret_cast<float4*>(mine + stage_off<ROWB>(j * 16 + (lane & 15), (i * 16 + 4 * (lane >> 4)) * 4)) =
             float4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
     __syncthreads();
-    for (int idx = threadIdx.x; idx < 32 * NCH; idx += C::THREADS) {
+    for (int idx = threadIdx.x; idx < C::TM * NCH; idx += C::THREADS) {
       const int r = idx / NCH, c = idx - r * NCH, i = i0 + r, col = j0 + c * 4;
       if (i >= ni || col >= nj) continue;
       float4 s = *reinterpret_cast<const float4*>(lds + stage_off<ROWB>(r, c * 16));
@@ -354,7 +359,6 @@ struct TileQ {
 // A tile of the call, and how much of k it adds up
 struct Work {
   int i0, ni, j0, nc;
-  const float* ws;
   char* out;
 };
 
@@ -400,7 +404,8 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
       g.sbase = reinterpret_cast<const char*>(a.ws + wblock * kb + c0 / 128);
       g.sv = (uint32_t)min(srow - C::TM, min(1, nb - 1 - j0 / 128)) * (uint32_t)(kb * 4);
     }
-    wk = Work{i0, gr.Me, j0, nc, a.ws + wblock * kb + c0 / 128,
+    g.wbase = reinterpret_cast<const char*>(a.ws + wblock * kb + c0 / 128);
+    wk = Work{i0, gr.Me, j0, nc,
               static_cast<char*>(a.y) + ((long long)gr.r0 * a.ld_y + s * a.part) * oe};
     g.first(ring, nc, kw);
     return true;
@@ -409,9 +414,10 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
   Work cur, next;
   int b = blockIdx.x;
   int stores = 0;   // of the previous tile, possibly in flight
-  bool more = start(b, cur);
+  bool more = start(b, cur), fresh = true;
   while (more) {
-    g.multiply(ring, cur.ni - cur.i0, cur.nc, cur.ws, wf, wt, kw, stores);
+    g.multiply(ring, cur.ni - cur.i0, cur.nc, wf, wt, kw, stores, fresh);
+    fresh = C::KW > 1;   // split wavefronts store before they copy
     stores = 0;
     b += gridDim.x;
     if constexpr (C::KW == 1) {
@@ -437,6 +443,7 @@ using Deep = CfgQ<128, 128, 2, 4, 4, 4, 1>;   // for calls that give no compute 
 using Small = CfgQ<64, 128, 1, 4, 3, 4, 2>;
 using Split = CfgQ<32, 32, 1, 1, 2, 4, 1, 8>;
 using Split64 = CfgQ<32, 64, 1, 1, 3, 4, 1, 4>;
+using Few = CfgQ<16, 32, 1, 1, 3, 4, 1, 8>;   // few rows: fewer bytes a stage, more stages on their way
 
 template <class C>
 constexpr GemmTile timed(double a, double c, double b, double o, bool once = false) {
@@ -459,7 +466,7 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
 const GemmTile kFp8GemmTileTable[] = {
     timed<Large>(0.73, 1.67, 1.67, 6),  timed<Wide>(0.68, 1.36, 1.36, 5),  timed<Medium>(0.60, 0.96, 0.96, 5),
     timed<Square>(0.37, 0.79, 0.54, 4), timed<Small>(0.28, 0.42, 0.32, 4), timed<Split>(0.68, 0.68, 0.68, 2),
-    timed<Split64>(0.60, 0.68, 0.68, 2), timed<Deep>(0.37, 0.56, 0.56, 5, true)};
+    timed<Split64>(0.60, 0.68, 0.68, 2), timed<Deep>(0.37, 0.56, 0.56, 5, true), timed<Few>(0.5, 0.5, 0.5, 2)};
 
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
   switch (id) {
@@ -471,6 +478,7 @@ hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
     case 6: return launch<Split>(a, s);
     case 7: return launch<Split64>(a, s);
     case 8: return launch<Deep>(a, s);
+    case 9: return launch<Few>(a, s);
   }
   return hipErrorInvalidValue;
 }

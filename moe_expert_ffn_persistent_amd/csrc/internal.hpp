@@ -169,7 +169,7 @@ struct GemmArgs {
 constexpr int kCus = 256;   // compute units, places for a persistent workgroup
 hipError_t launch_gemm_any(const GemmArgs& a, bool fp8, hipStream_t s);
 // tiles 1 .. kBf16GemmTiles (kFp8GemmTiles) of the 16-byte kernels
-constexpr int kBf16GemmTiles = 8, kFp8GemmTiles = 8;
+constexpr int kBf16GemmTiles = 9, kFp8GemmTiles = 9;
 struct GemmTile {
   int tm, tn, occ, kw;   // rows, columns, workgroups per compute unit, wavefronts that split the sum
   double a, c, b, o;     // us: a stage alone, with a workgroup on every compute unit, with occ of them, a tile's ends

@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 OPS = pytest.mark.parametrize("op", [FWD, DGRAD, WGRAD], ids=["forward", "dgrad", "wgrad"])
 
 
-TILES = [(op, tile) for op in (FWD, DGRAD, WGRAD) for tile in ((1, 3, 4, 5) if op == WGRAD else range(1, 9))]
+TILES = [(op, tile) for op in (FWD, DGRAD, WGRAD) for tile in ((1, 3, 4, 5) if op == WGRAD else range(1, 10))]
 
 
 @pytest.mark.parametrize("splits", [2, 3, 64])
@@ -27,7 +27,7 @@ def test_grouped_every_tile_in_ranges(op, tile, splits):
 
 
 @pytest.mark.parametrize("splits", [2, 5, 64])
-@pytest.mark.parametrize("tile", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("tile", range(1, 10))
 def test_fp8_every_tile_in_ranges(tile, splits):
     run_fp8([0, 33, 290, 1], 324, 1040, 136, BF, behind=4, pad=16, tile=tile, splits=splits)
     run_fp8(None, 70, 272, 264, F32, tile=tile, splits=splits)

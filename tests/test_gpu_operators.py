@@ -166,12 +166,12 @@ def test_grouped_tile_choice_changes_no_result(op, expected):
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("tile", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("tile", range(1, 10))
 @pytest.mark.parametrize("op", [FWD, DGRAD, WGRAD], ids=["forward", "dgrad", "wgrad"])
 @pytest.mark.parametrize("counts,k,n", [([0, 33, 290, 1], 264, 328), ([70, 257], 64, 8), ([3, 0, 200], 8, 64), ([64, 128], 512, 256),
                                         ([191, 129], 1032, 136), ([1, 700], 2056, 72)])
 def test_grouped_every_tile(counts, k, n, op, tile, out_dtype):
-    if op == WGRAD and tile in (2, 6, 7, 8):   # not tiles of this product
+    if op == WGRAD and tile in (2, 6, 7, 8, 9):   # not tiles of this product
         with pytest.raises(_lib.MoeError) as err:
             run_grouped(op, counts, k, n, out_dtype, seed=1, tile=tile)
         assert err.value.status == _lib.MOE_ERR_UNSUPPORTED
@@ -556,7 +556,7 @@ def test_fp8_tile_choice_changes_no_result(expected):
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("tile", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("tile", range(1, 10))
 @pytest.mark.parametrize("counts,R,K,n", [([0, 33, 290, 1], 324, 272, 328), (None, 300, 64, 8), ([3, 0, 200], 203, 16, 64),
                                           ([64, 128], 192, 512, 256), (None, 1, 8336, 136), (None, 257, 1040, 520)],
                          ids=lambda v: str(v).replace(" ", ""))

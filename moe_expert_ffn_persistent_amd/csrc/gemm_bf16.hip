@@ -552,11 +552,16 @@ hipError_t launch_tile(int id, const GemmArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// forward and dgrad; wgrad (whose operands both go through transposing reads)
+// forward; dgrad, whose narrow tiles read half lines of the weights; wgrad (both
+// operands through transposing reads)
 const GemmTile kBf16GemmTileTable[] = {
     timed<Large>(0.84, 1.56, 1.56, 4),  timed<Wide>(0.73, 1.27, 1.27, 4),  timed<Medium>(0.48, 0.90, 0.90, 5),
     timed<Square>(0.47, 0.79, 0.54, 2), timed<Small>(0.22, 0.37, 0.32, 4), timed<Split>(0.78, 0.96, 0.96, 1),
-    timed<Split64>(0.52, 0.64, 0.64, 2), timed<Deep>(0.28, 0.48, 0.48, 5, true), timed<Few>(0.5, 0.5, 0.5, 1)};
+    timed<Split64>(0.52, 0.64, 0.64, 2), timed<Deep>(0.28, 0.48, 0.48, 5, true), timed<Few>(0.64, 0.64, 0.64, 1)};
+const GemmTile kDgradTiles[] = {
+    timed<Large>(0.78, 1.56, 1.56, 5),  timed<Wide>(0.73, 1.27, 1.27, 5),  timed<Medium>(0.48, 0.90, 0.90, 6),
+    timed<Square>(0.54, 0.79, 0.54, 2), timed<Small>(0.25, 0.37, 0.32, 4), timed<Split>(0.78, 1.18, 1.18, 1),
+    timed<Split64>(0.56, 0.73, 0.73, 2), timed<Deep>(0.30, 0.52, 0.52, 4, true), timed<Few>(0.73, 1.03, 1.03, 1)};
 const GemmTile kWgradTiles[] = {
     timed<Large>(1.10, 1.79, 1.79, 6),  GemmTile{}, timed<Medium>(0.60, 0.96, 0.96, 4),
     timed<Square>(0.47, 0.70, 0.47, 4), timed<Small>(0.32, 0.32, 0.32, 3), GemmTile{}, GemmTile{}, GemmTile{}, GemmTile{}};

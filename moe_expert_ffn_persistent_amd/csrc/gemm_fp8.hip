@@ -466,7 +466,7 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
 const GemmTile kFp8GemmTileTable[] = {
     timed<Large>(0.73, 1.67, 1.67, 6),  timed<Wide>(0.68, 1.36, 1.36, 5),  timed<Medium>(0.60, 0.96, 0.96, 5),
     timed<Square>(0.37, 0.79, 0.54, 4), timed<Small>(0.28, 0.42, 0.32, 4), timed<Split>(0.68, 0.68, 0.68, 2),
-    timed<Split64>(0.60, 0.68, 0.68, 2), timed<Deep>(0.37, 0.56, 0.56, 5, true), timed<Few>(0.5, 0.5, 0.5, 2)};
+    timed<Split64>(0.60, 0.68, 0.68, 2), timed<Deep>(0.37, 0.56, 0.56, 5, true), timed<Few>(0.50, 0.64, 0.64, 2)};
 
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s) {
   switch (id) {

@@ -175,7 +175,7 @@ struct GemmTile {
   double a, c, b, o;     // us: a stage alone, with a workgroup on every compute unit, with occ of them, a tile's ends
   bool once;             // only for calls that give no compute unit a second tile
 };
-extern const GemmTile kBf16GemmTileTable[], kWgradTiles[], kFp8GemmTileTable[];   // id - 1
+extern const GemmTile kBf16GemmTileTable[], kDgradTiles[], kWgradTiles[], kFp8GemmTileTable[];   // id - 1
 // The same call with its sum cut into a.splits ranges, written to `ws` (fp32, one
 // output's elements a range), and the joining of them into a's output
 GemmArgs split_args(const GemmArgs& a, float* ws);

@@ -48,10 +48,10 @@ double expected_blocks(double rows, int L, int tm) {
 // each. A stage's time grows from the tile's when few compute units work (a) to
 // that with all of them at work (c: clock, L2 and memory are shared then); with
 // two workgroups on a compute unit a stage of one of them takes 2 b.
-// Fitted to 198 bf16 and 66 e4m3 calls of 1 to 16384 rows, 1 to 32 experts and
-// 600 to 7168 features, each timed with every tile; over 222 and 74 calls the
-// tile chosen took 1.1% and 1.7% longer than the best one in the mean, 26% at
-// worst (a few rows to many experts).
+// Fitted to calls of 1 to 16384 rows, 1 to 128 experts and 80 to 28672 features,
+// each timed with every tile: over 88 calls of each product the tile chosen took
+// 1.8% (forward), 2.3% (dgrad), 0.9% (wgrad) and 1.6% (e4m3) longer than the best
+// one in the mean, 45% at worst (wgrad of 256 rows; a few rows to many experts).
 double predicted(const GemmTile& t, double tiles, double stages) {
   const double q = std::max(1.0, std::ceil(tiles / kCus - 0.02));
   const double one = t.a + (t.c - t.a) * std::min(1.0, tiles / kCus);
@@ -143,7 +143,7 @@ bool grouped_fast(const moe_grouped_params* p) {
 }
 
 const GemmTile* grouped_tiles(const moe_grouped_params* p) {
-  return p->op == MOE_GROUPED_WGRAD ? kWgradTiles : kBf16GemmTileTable;
+  return p->op == MOE_GROUPED_WGRAD ? kWgradTiles : p->op == MOE_GROUPED_DGRAD ? kDgradTiles : kBf16GemmTileTable;
 }
 
 // an id the call's sizes can take

@@ -85,17 +85,19 @@ __device__ __forceinline__ int logical_instance(int G, int xcd_group, int xcd_bx
 // One 1 KiB global->LDS copy for the wavefront: lane l's 16 bytes from src
 // land at LDS byte address m0 + 16*l. Issued from inline assembly so the
 // compiler does not serialise later LDS reads behind it; completion is
-// awaited explicitly with vm_wait and published with lds_barrier.
+// awaited explicitly with vm_wait and published with lds_barrier. A copy reads
+// m0 one wait state after an SALU write of it at the earliest; the compiler does
+// not see into the statement, so the s_nop keeps that distance.
 template <int POL>
 __device__ __forceinline__ void dma16(const char* src, uint32_t m0) {
   if constexpr (POL == kStream)
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(src), "s"(m0)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(src), "s"(m0)
                  : "memory", "m0");
   else if constexpr (POL == kCoherent)
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off sc1" ::"v"(src), "s"(m0)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off sc1" ::"v"(src), "s"(m0)
                  : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(m0)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(m0)
                  : "memory", "m0");
 }
 
@@ -169,14 +171,14 @@ __device__ __forceinline__ int opaque(int v) {
 }
 
 // Four-byte direct-to-LDS copy: lane l's word lands at m0 + 4*l (inactive
-// lanes write nothing).
+// lanes write nothing); m0's wait state as in dma16.
 template <int POL>
 __device__ __forceinline__ void dma4(const char* src, uint32_t m0) {
   if constexpr (POL == kCoherent)
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off sc1" ::"v"(src), "s"(m0)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off sc1" ::"v"(src), "s"(m0)
                  : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(m0)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(m0)
                  : "memory", "m0");
 }
 

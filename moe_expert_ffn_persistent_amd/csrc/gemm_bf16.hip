@@ -34,9 +34,10 @@ constexpr int kBK = 64;   // c per stage
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// 16 bytes a lane from base + voff (bytes) to LDS m0 + 16 * lane
+// 16 bytes a lane from base + voff (bytes) to LDS m0 + 16 * lane;
+// s_nop: m0's wait state (see dma16 in ffn_common.hpp)
 __device__ __forceinline__ void dma16s(uint32_t voff, const char* base, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
 }
 
 // KW > 1: the workgroup's KW wavefronts share one small tile and split c: each

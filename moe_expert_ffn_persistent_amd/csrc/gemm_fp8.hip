@@ -30,12 +30,13 @@
 namespace moe {
 namespace {
 
-// 16 (or 4) bytes a lane from base + voff (bytes) to LDS m0 + 16 (4) * lane
+// 16 (or 4) bytes a lane from base + voff (bytes) to LDS m0 + 16 (4) * lane;
+// s_nop: m0's wait state (see dma16 in ffn_common.hpp)
 __device__ __forceinline__ void dma16s(uint32_t voff, const char* base, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4s(uint32_t voff, const char* base, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
 }
 
 // KW > 1: KW wavefronts split K (see the bf16 kernel): a ring each, sums joined in LDS.

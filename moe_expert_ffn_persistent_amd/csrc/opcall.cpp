@@ -9,13 +9,15 @@
 // key without the checks: reading six tensors from Python took 2.5 us of a
 // call's 6.8, reading them here takes 0.4 of 3.9 (the rest is the launch), where
 // a decode step's kernel runs for 2 to 4 us. What shapes do not settle (a tensor
-// that requires grad while grad mode is on, another current device, a view with
-// a pending negation) is looked at in every call; `again` returns None for it,
-// and for anything it does not know, and the checks speak.
+// that requires grad while grad mode is on, one with a forward-mode tangent,
+// another current device, a view with a pending negation) is looked at in every
+// call; `again` returns None for it, and for anything it does not know, and the
+// checks speak.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -71,6 +73,7 @@ struct Call {
       }
     }
     const bool grad = c10::GradMode::is_enabled();
+    const bool forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
     for (int i = 0; i < n; ++i) {
       if (tensors[i] == Py_None) {
         ptr[i] = nullptr;
@@ -80,6 +83,7 @@ struct Call {
       if (!THPVariable_Check(tensors[i])) return false;
       const at::Tensor& t = THPVariable_Unpack(tensors[i]);
       if (t.layout() != c10::kStrided || t.get_device() != device || t.is_neg() || (grad && t.requires_grad())) return false;
+      if (forward && t._fw_grad(0).defined()) return false;   // the only level there is
       const auto sizes = t.sizes();
       const auto strides = t.strides();
       add((int64_t)t.device().type() << 48 | (int64_t)t.scalar_type() << 32 | (int64_t)sizes.size());

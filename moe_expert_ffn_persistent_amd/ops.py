@@ -13,15 +13,17 @@ held. Tensors used on a stream other than the one they were allocated on need
 the caller's ``record_stream``, as everywhere in torch.
 
 The functions record nothing for autograd; gradients are the operators named
-so. Given an input that requires grad while grad mode is on they raise, rather
-than return a tensor that silently cuts the graph: call them inside a
-torch.autograd.Function or under torch.no_grad().
+so. Given a tensor that requires grad while grad mode is on, or one that carries
+a forward-mode tangent, they raise rather than return a tensor that silently cuts
+the graph: call them inside a torch.autograd.Function or, where no tangents are,
+under torch.no_grad().
 """
 from __future__ import annotations
 
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._lib import (MOE_GROUPED_DGRAD, MOE_GROUPED_FORWARD, MOE_GROUPED_WGRAD, MOE_MAX_LOCAL_EXPERTS,
@@ -38,7 +40,7 @@ def _blocks(n: int) -> int:
 
 
 def _on(device, *named):
-    """Every tensor given is on ``device``, and grad mode would not be cut."""
+    """Every tensor given is on ``device``, and neither grad mode would be cut."""
     grad = torch.is_grad_enabled()
     for what, t in named:
         if t is None:
@@ -50,6 +52,9 @@ def _on(device, *named):
         if grad and t.requires_grad:
             raise ValueError(f"{what} requires grad, and this operator records nothing for autograd: "
                              "call it in a torch.autograd.Function or under torch.no_grad()")
+        if t.is_floating_point() and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{what} carries a forward-mode tangent, and this operator records nothing for autograd: "
+                             "call it in a torch.autograd.Function with a jvp")
 
 
 def _matrix(t, what, dtypes, dims=2):

@@ -12,7 +12,8 @@
 // that requires grad while grad mode is on, one with a forward-mode tangent,
 // another current device, a view with a pending negation) is looked at in every
 // call; `again` returns None for it, and for anything it does not know, and the
-// checks speak.
+// checks speak. What a call writes gets a new version, as from torch's own
+// in-place operations: its check of tensors saved for a backward pass relies on it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -35,6 +36,7 @@ constexpr size_t kMaxPlans = 2048;   // cleared when full
 struct Plan {
   alignas(8) char params[kMaxParams];
   int64_t workspace;   // bytes of the last pointer, the call's own
+  unsigned written;    // bit i: tensor i is written
 };
 
 std::unordered_map<std::string, Plan>& plans() {
@@ -137,6 +139,16 @@ int read_call(Call& c, PyObject* entry, PyObject* device, PyObject* plain, PyObj
   return ok ? 1 : 0;
 }
 
+// A new version for the tensors of `written` (none is kept of tensors made in
+// inference mode). They were read before the call and are still referenced.
+void new_versions(unsigned written, PyObject* const* tensors, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!(written >> i & 1) || tensors[i] == Py_None) continue;
+    const at::Tensor& t = THPVariable_Unpack(tensors[i]);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+}
+
 // again(entry, device, stream, current, plain, *tensors) -> status, or None;
 // False where the call takes a workspace and `current` does not say that the
 // stream is the current one: it is allocated for the current stream
@@ -172,20 +184,24 @@ PyObject* again(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   Py_BEGIN_ALLOW_THREADS
   status = launch(entry, plan.params, ptr, n, stream);
   Py_END_ALLOW_THREADS
+  if (status == 0) new_versions(plan.written, args + 5, n);
   return PyLong_FromLong(status);
 }
 
-// remember(params, entry, device, workspace, plain, *tensors): the struct's
-// bytes for calls like this one, and the bytes of workspace that they take (in
-// the place of the last tensor)
-PyObject* remember(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs < 8 || !PyBytes_Check(args[0]) || PyBytes_GET_SIZE(args[0]) > kMaxParams || !PyLong_Check(args[3])) {
-    PyErr_SetString(PyExc_TypeError,
-                    "remember(params, entry, device, workspace, plain, *tensors): bytes and at least three tensors");
+// remember(params, entry, device, workspace, plain, *tensors, written=0): the
+// struct's bytes for calls like this one, the bytes of workspace that they take
+// (in the place of the last tensor), and which tensors they write (bit i: tensor i)
+PyObject* remember(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* names) {
+  const Py_ssize_t named = names ? PyTuple_GET_SIZE(names) : 0;
+  if (nargs < 8 || !PyBytes_Check(args[0]) || PyBytes_GET_SIZE(args[0]) > kMaxParams || !PyLong_Check(args[3]) ||
+      named > 1 || (named == 1 && PyUnicode_CompareWithASCIIString(PyTuple_GET_ITEM(names, 0), "written") != 0)) {
+    PyErr_SetString(PyExc_TypeError, "remember(params, entry, device, workspace, plain, *tensors, written=0): bytes and "
+                                     "at least three tensors");
     return nullptr;
   }
   Plan plan{};
   plan.workspace = PyLong_AsLongLong(args[3]);
+  if (named) plan.written = (unsigned)PyLong_AsUnsignedLong(args[nargs]);
   if (PyErr_Occurred()) return nullptr;
   Call& c = scratch();
   const int got = read_call(c, args[1], args[2], args[4], args + 5, nargs - 5);
@@ -202,8 +218,9 @@ PyMethodDef methods[] = {
      "again(entry, device, stream, current, plain, *tensors): the call of a C entry point for sizes that were "
      "remembered; its status, None for a call that has to be checked, or False for one that takes a workspace on a "
      "stream that is not the current one."},
-    {"remember", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(remember)), METH_FASTCALL,
-     "remember(params, entry, device, workspace, plain, *tensors): keep a checked call's parameter struct (bytes)."},
+    {"remember", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(remember)), METH_FASTCALL | METH_KEYWORDS,
+     "remember(params, entry, device, workspace, plain, *tensors, written=0): keep a checked call's parameter struct "
+     "(bytes); bit i of written: tensor i is written."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_opcall", "Call path of the operators for sizes checked before.", -1,

@@ -16,7 +16,8 @@ The functions record nothing for autograd; gradients are the operators named
 so. Given a tensor that requires grad while grad mode is on, or one that carries
 a forward-mode tangent, they raise rather than return a tensor that silently cuts
 the graph: call them inside a torch.autograd.Function or, where no tangents are,
-under torch.no_grad().
+under torch.no_grad(). What a call writes gets a new version, so torch notices
+when that was saved for a backward pass.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ import ctypes
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._lib import (MOE_GROUPED_DGRAD, MOE_GROUPED_FORWARD, MOE_GROUPED_WGRAD, MOE_MAX_LOCAL_EXPERTS,
@@ -172,8 +174,9 @@ def _check_stream(stream, device):
 _WORKSPACE = {"moe_grouped_matmul_split": "moe_grouped_workspace_bytes", "moe_fp8_matmul_split": "moe_fp8_workspace_bytes"}
 
 
-def _call(name, check, args, plain, tensors, stream):
-    """One C entry point, ``tensors`` its pointers in order. ``check(*args)``
+def _call(name, check, args, plain, tensors, written, stream):
+    """One C entry point, ``tensors`` its pointers in order, of which it writes
+    those whose bit is set in ``written``. ``check(*args)``
     makes its parameters from their sizes and the ``plain`` arguments; for
     sizes that it has seen the call is made again without it (csrc/opcall.cpp:
     a call costs the host 3.9 us, 3.4 of them the launch)."""
@@ -193,10 +196,10 @@ def _call(name, check, args, plain, tensors, stream):
             if st != _lib.MOE_OK:
                 _lib.check(st, name)
             return
-    _first_call(name, check, args, plain, tensors, stream)
+    _first_call(name, check, args, plain, tensors, written, stream)
 
 
-def _first_call(name, check, args, plain, tensors, stream):
+def _first_call(name, check, args, plain, tensors, written, stream):
     global _again, _remember
     params = check(*args)
     device = next(t for t in tensors if t is not None).device
@@ -219,8 +222,9 @@ def _first_call(name, check, args, plain, tensors, stream):
         st = fn(ctypes.byref(params), *pointers, s)
     if st != _lib.MOE_OK:
         _lib.check(st, name)
+    increment_version([t for i, t in enumerate(tensors) if written >> i & 1 and t is not None])
     entry = _ENTRY[name] = ctypes.cast(fn, ctypes.c_void_p).value
-    _remember(bytes(params), entry, device.index, need, plain, *tensors)
+    _remember(bytes(params), entry, device.index, need, plain, *tensors, written=written)
 
 
 # ---- rows to and from the experts -------------------------------------------
@@ -255,7 +259,7 @@ def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
         _indices(row_pair, "row_pair")
         out = _empty((row_pair.numel(), H), x.dtype, x.device, stream)
     _call("moe_dispatch_rows", check_dispatch_inputs, (x, row_pair, row_offset, top_k, out), (top_k,),
-          (x, row_pair, row_offset, out), stream)
+          (x, row_pair, row_offset, out), 0b1000, stream)
     return out
 
 
@@ -284,7 +288,7 @@ def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stre
         _indices(pair_row, "pair_row")
         out = _empty((pair_row.numel() // max(1, top_k), H), _out_type(out_dtype), rows.device, stream)
     _call("moe_combine_rows", check_combine_rows_inputs, (rows, pair_row, top_k, out), (top_k,), (rows, pair_row, out),
-          stream)
+          0b100, stream)
     return out
 
 
@@ -309,10 +313,13 @@ def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate
                             _batch_stride(w, "weights", ldw), _OUT[written.dtype], int(accumulate), tile, splits)
 
 
+_GROUPED_WRITES = {MOE_GROUPED_FORWARD: 0b1000, MOE_GROUPED_DGRAD: 0b10, MOE_GROUPED_WGRAD: 0b100}   # of row_offset, x, w, y
+
+
 def _grouped(op, x, w, y, row_offset, expected_rows, accumulate, tile, splits, stream):
     _call("moe_grouped_matmul_split", check_grouped_inputs,
           (op, x, w, y, row_offset, expected_rows, accumulate, tile, splits),
-          (op, expected_rows, accumulate, tile, splits), (row_offset, x, w, y, None), stream)
+          (op, expected_rows, accumulate, tile, splits), (row_offset, x, w, y, None), _GROUPED_WRITES[op], stream)
 
 
 def grouped_matmul(x, w, row_offset, out=None, out_dtype=torch.bfloat16, expected_rows=None, tile=0, splits=0,
@@ -413,7 +420,7 @@ def swiglu(gate_up, row_weight=None, row_offset=None, out=None, scales=None, out
         rows, I = _half(gate_up)
         scales = _empty((rows, _blocks(I)), torch.float32, gate_up.device, stream)
     _call("moe_swiglu", check_swiglu_inputs, (gate_up, row_weight, row_offset, out, scales), (),
-          (gate_up, row_weight, row_offset, out, scales), stream)
+          (gate_up, row_weight, row_offset, out, scales), 0b11000, stream)
     return out if scales is None else (out, scales)
 
 
@@ -443,7 +450,7 @@ def swiglu_backward(gate_up, dh, row_weight=None, row_offset=None, out=None, dro
         rows, _ = _sizes(gate_up, "gate_up", 2)
         drow_weight = _empty((rows,), torch.float32, gate_up.device, stream)
     _call("moe_swiglu_backward", check_swiglu_backward_inputs, (gate_up, dh, row_weight, row_offset, out, drow_weight), (),
-          (gate_up, dh, row_weight, row_offset, out, drow_weight), stream)
+          (gate_up, dh, row_weight, row_offset, out, drow_weight), 0b110000, stream)
     return out, drow_weight
 
 
@@ -498,7 +505,7 @@ def quantize_fp8(x, block_rows=1, row_offset=None, out=None, scales=None, stream
     if isinstance(x, torch.Tensor) and x.numel() == 0:
         check_quantize_inputs(*args)
     else:
-        _call("moe_quantize_fp8", check_quantize_inputs, args, (block_rows,), (x, row_offset, out, scales), stream)
+        _call("moe_quantize_fp8", check_quantize_inputs, args, (block_rows,), (x, row_offset, out, scales), 0b1100, stream)
     return out, scales
 
 
@@ -544,5 +551,5 @@ def fp8_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=to
         out = _empty((rows, n), _out_type(out_dtype), x.device, stream)
     _call("moe_fp8_matmul_split", check_fp8_inputs,
           (x, x_scales, w, w_scales, row_offset, out, expected_rows, tile, splits), (expected_rows, tile, splits),
-          (row_offset, x, x_scales, w, w_scales, out, None), stream)
+          (row_offset, x, x_scales, w, w_scales, out, None), 0b100000, stream)
     return out

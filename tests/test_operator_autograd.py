@@ -92,3 +92,27 @@ def test_tangents_are_refused_for_sizes_seen_before():
         finally:
             torch._C._set_fwd_grad_enabled(before)
     assert opcall.again(entry.address, HOST, 0, True, (), a, b, c) == 0
+
+
+@pytest.mark.skipif(not os.path.exists(build.OPCALL), reason="_opcall.so not built")
+def test_what_a_call_of_known_sizes_writes_gets_a_new_version():
+    opcall = _lib.load_opcall()
+    entry, ts = Entry(4), [torch.zeros(4, 8) for _ in range(3)]
+    opcall.remember(b"12345678", entry.address, HOST, 0, (), *ts, None, written=0b1110)
+    for i in range(1, 4):
+        assert opcall.again(entry.address, HOST, 0, True, (), *ts, None) == 0
+        assert [t._version for t in ts] == [0, i, i]
+    view = ts[2][1:3]
+    assert view._version == 3   # a view shares its base's
+    entry.status = -2           # a call that was refused wrote nothing
+    assert opcall.again(entry.address, HOST, 0, True, (), *ts, None) == -2
+    assert [t._version for t in ts] == [0, 3, 3]
+    with torch.inference_mode():
+        made = torch.zeros(4, 8)
+    entry.status = 0
+    assert opcall.again(entry.address, HOST, 0, True, (), ts[0], made, ts[2], None) == 0
+    assert ts[2]._version == 4
+    for call in (lambda: opcall.remember(b"1", entry.address, HOST, 0, (), *ts, writes=1),
+                 lambda: opcall.remember(b"1", entry.address, HOST, 0, (), *ts, written="1")):
+        with pytest.raises(TypeError):
+            call()

@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(256) moe_gemm_any(const GemmArgs a) {
     i0 = (blockIdx.x - g.e * nt) * kAnyTile;
     g.r0 = clamped_offset(a.row_offset, a.L, a.rows, g.e);
     g.Me = max(clamped_offset(a.row_offset, a.L, a.rows, g.e + 1) - g.r0, 0);
+    if (a.accumulate && g.Me == 0) return;   // an expert without rows keeps what accumulates, to the bit
   } else if (a.row_offset) {
     g = GroupScan<kAnyTile>(a.row_offset, a.L, a.rows).find(blockIdx.x);
     if (!g.ok) return;

@@ -424,8 +424,8 @@ int32_t moe_mfma_rate_probe(int32_t format, int32_t blocks, int64_t iters, const
  * `row_offset` is the layout's (device int32 [L+1], row_offset[0] first): rows
  * row_offset[e] .. row_offset[e+1]-1 belong to expert e. `rows` is the number
  * of rows the row buffers have room for (at most 2^28); hidden, n, k, inter and
- * cols are at most 2^20, row strides at most 2^32 elements. Offsets are read on
- * the device; they must not decrease, and any past `rows` (or below 0) is
+ * cols are at most 2^20, row strides at most 2^32 elements, tokens at most 2^40
+ * (moe_combine_rows: 2^23 in a call). Offsets are read on the device; they must not decrease, and any past `rows` (or below 0) is
  * taken as `rows` (0), so no access leaves the buffers. Rows outside
  * row_offset[0] .. row_offset[L]-1 are neither read nor written. Leading
  * dimensions (ld_*) count elements between rows, at least the row's length.

@@ -15,6 +15,9 @@ constexpr int kMaxCols = 1 << 20;
 // elements between rows or matrices: the checks below multiply by up to
 // kMaxRows, the kernels' byte offsets stay inside 64 bits
 constexpr long long kMaxStride = 1ll << 32, kMaxMatrix = 1ll << 52;
+// tokens: dispatch only multiplies by them; combine has a workgroup of 256
+// threads for a token at most, and fewer than 2^32 threads a launch
+constexpr long long kMaxTokens = 1ll << 40, kMaxCombineTokens = 1ll << 23;
 
 int32_t done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
@@ -255,7 +258,7 @@ int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t
   if (!p || p->tokens < 0 || p->rows < 0 || p->rows > kMaxRows || p->top_k < 1 || p->top_k > 16 || p->hidden < 1 ||
       p->hidden > kMaxCols || (p->elem_bytes != 1 && p->elem_bytes != 2 && p->elem_bytes != 4) ||
       p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || !stride_ok(p->ld_tokens, p->hidden) ||
-      !stride_ok(p->ld_rows, p->hidden) || p->tokens > (1ll << 30) / p->top_k)
+      !stride_ok(p->ld_rows, p->hidden) || p->tokens > kMaxTokens)
     return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
   if (!row_pair || !row_offset || !out || (p->tokens && !x)) return MOE_ERR_INVALID_ARG;
@@ -279,7 +282,7 @@ int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t
 int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row, void* y, void* stream) {
   if (!p || p->tokens < 0 || p->rows < 0 || p->rows > kMaxRows || p->top_k < 1 || p->top_k > 16 || p->hidden < 1 ||
       p->hidden > kMaxCols || p->elem_bytes != 2 || !dtype_ok(p->out_dtype) || !stride_ok(p->ld_tokens, p->hidden) ||
-      !stride_ok(p->ld_rows, p->hidden) || p->tokens > (1ll << 23))
+      !stride_ok(p->ld_rows, p->hidden) || p->tokens > kMaxCombineTokens)
     return MOE_ERR_INVALID_ARG;
   if (p->tokens == 0) return MOE_OK;
   if (!pair_row || !y || (p->rows && !in)) return MOE_ERR_INVALID_ARG;

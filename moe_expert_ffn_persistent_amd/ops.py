@@ -263,6 +263,13 @@ def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
     return out
 
 
+_MAX_TOKENS = 1 << 23   # of one moe_combine_rows
+
+
+class _MoreTokens(Exception):
+    """Inputs that are in order but for more tokens than one call takes."""
+
+
 def check_combine_rows_inputs(rows, pair_row, top_k, out):
     ldr = _matrix(rows, "rows", (torch.bfloat16,))
     if not 1 <= top_k <= 16:
@@ -275,6 +282,8 @@ def check_combine_rows_inputs(rows, pair_row, top_k, out):
     if tuple(out.shape) != (N, rows.shape[1]):
         raise ValueError(f"out: need shape {(N, rows.shape[1])}, got {tuple(out.shape)}")
     _on(rows.device, ("rows", rows), ("pair_row", pair_row), ("out", out))
+    if N > _MAX_TOKENS:
+        raise _MoreTokens
     return MoeRowsParams(N, rows.shape[0], top_k, rows.shape[1], 2, 0, _OUT[out.dtype], ldo, ldr)
 
 
@@ -287,8 +296,13 @@ def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stre
         _, H = _sizes(rows, "rows", 2)
         _indices(pair_row, "pair_row")
         out = _empty((pair_row.numel() // max(1, top_k), H), _out_type(out_dtype), rows.device, stream)
-    _call("moe_combine_rows", check_combine_rows_inputs, (rows, pair_row, top_k, out), (top_k,), (rows, pair_row, out),
-          0b100, stream)
+    try:
+        _call("moe_combine_rows", check_combine_rows_inputs, (rows, pair_row, top_k, out), (top_k,), (rows, pair_row, out),
+              0b100, stream)
+    except _MoreTokens:
+        pairs = pair_row.view(-1)
+        for n in range(0, out.shape[0], _MAX_TOKENS):
+            combine_rows(rows, pairs[n * top_k:(n + _MAX_TOKENS) * top_k], top_k, out=out[n:n + _MAX_TOKENS], stream=stream)
     return out
 
 

@@ -35,6 +35,11 @@ from ._lib import (MOE_GROUPED_DGRAD, MOE_GROUPED_FORWARD, MOE_GROUPED_WGRAD, MO
 BLOCK = 128   # columns of one fp32 scale
 _OUT = {torch.bfloat16: MOE_Y_BF16, torch.float32: MOE_Y_FP32}
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+# the C entry points' limits
+_MAX_ROWS, _MAX_COLS, _MAX_STRIDE, _MAX_MATRIX = 1 << 28, 1 << 20, 1 << 32, 1 << 52
+_MAX_TOKENS = 1 << 23    # of one moe_combine_rows
+_MAX_BATCH, _MAX_BLOCKS = 65535, (1 << 23) - 1   # quantisation: matrices; 128 x 128 blocks of one
+_MAX_SPLITS = 64
 
 
 def _blocks(n: int) -> int:
@@ -59,9 +64,10 @@ def _on(device, *named):
                              "call it in a torch.autograd.Function with a jvp")
 
 
-def _matrix(t, what, dtypes, dims=2):
+def _matrix(t, what, dtypes, dims=2, most=_MAX_COLS):
     """A tensor of ``dims`` dimensions and one of ``dtypes`` whose rows are
-    contiguous and do not overlap; returns the row stride."""
+    contiguous, of at most ``most`` elements, and do not overlap; returns the row
+    stride."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{what}: need a tensor, got {type(t).__name__}")
     if t.dim() != dims:
@@ -71,13 +77,22 @@ def _matrix(t, what, dtypes, dims=2):
     rows, cols = t.shape[-2:]
     if cols < 1:
         raise ValueError(f"{what}: rows of no elements")
+    if cols > most:
+        raise ValueError(f"{what}: rows of {cols} elements, at most {most} are taken")
     st = t.stride()
     if cols > 1 and st[-1] != 1:
         raise ValueError(f"{what}: rows must be contiguous (last stride 1, got {st[-1]})")
     ld = st[-2] if rows > 1 else cols
     if ld < cols:
         raise ValueError(f"{what}: rows overlap (row stride {ld} under {cols} columns)")
+    if ld > _MAX_STRIDE:
+        raise ValueError(f"{what}: row stride {ld}, at most {_MAX_STRIDE} is taken")
     return ld
+
+
+def _at_most(n, what, most):
+    if n > most:
+        raise ValueError(f"{what}: {n}, at most {most} are taken")
 
 
 def _batch_stride(t, what, ld):
@@ -85,6 +100,8 @@ def _batch_stride(t, what, ld):
     need = (t.shape[1] - 1) * ld + t.shape[2]
     if t.shape[0] > 1 and t.stride(0) < need:
         raise ValueError(f"{what}: matrices overlap (stride {t.stride(0)} under {need} elements)")
+    if t.shape[0] > 1 and t.stride(0) > _MAX_MATRIX:
+        raise ValueError(f"{what}: stride {t.stride(0)} between matrices, at most {_MAX_MATRIX} is taken")
     return t.stride(0) if t.shape[0] > 1 else need
 
 
@@ -115,6 +132,14 @@ def _expected(expected_rows):
     if expected_rows < 1:
         raise ValueError(f"expected_rows: need at least 1, got {expected_rows}")
     return int(expected_rows)
+
+
+def _choice(tile, splits):
+    """Numbers that name a kernel (an id that a call cannot take is MoeError)."""
+    if tile < 0:
+        raise ValueError(f"tile: need an id, or 0 for automatic, got {tile}")
+    if not 0 <= splits <= _MAX_SPLITS:
+        raise ValueError(f"splits: need 1 to {_MAX_SPLITS}, or 0 for automatic, got {splits}")
 
 
 def _need_device(device):
@@ -243,6 +268,7 @@ def check_dispatch_inputs(x, row_pair, row_offset, top_k, out):
     ldo = _matrix(out, "out", (x.dtype,))
     if out.shape[1] != H:
         raise ValueError(f"out: rows of {out.shape[1]} elements, x has {H}")
+    _at_most(out.shape[0], "rows of out", _MAX_ROWS)
     if row_pair.numel() < out.shape[0]:
         raise ValueError(f"row_pair: {row_pair.numel()} entries for {out.shape[0]} rows")
     _on(x.device, ("x", x), ("row_pair", row_pair), ("row_offset", row_offset), ("out", out))
@@ -263,15 +289,13 @@ def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
     return out
 
 
-_MAX_TOKENS = 1 << 23   # of one moe_combine_rows
-
-
 class _MoreTokens(Exception):
     """Inputs that are in order but for more tokens than one call takes."""
 
 
 def check_combine_rows_inputs(rows, pair_row, top_k, out):
     ldr = _matrix(rows, "rows", (torch.bfloat16,))
+    _at_most(rows.shape[0], "rows", _MAX_ROWS)
     if not 1 <= top_k <= 16:
         raise ValueError(f"top_k: need 1 to 16, got {top_k}")
     _indices(pair_row, "pair_row")
@@ -316,6 +340,9 @@ def check_grouped_inputs(op, x, w, y, row_offset, expected_rows=None, accumulate
     ldw = _matrix(w, "w" if op != MOE_GROUPED_WGRAD else "out", out if op == MOE_GROUPED_WGRAD else bf16, 3)
     ldy = _matrix(y, "dy" if op != MOE_GROUPED_FORWARD else "out", out if op == MOE_GROUPED_FORWARD else bf16)
     L, n, k = w.shape
+    _at_most(x.shape[0], "rows", _MAX_ROWS)
+    _at_most(n, "output features", _MAX_COLS)
+    _choice(tile, splits)
     if _offsets(row_offset) != L:
         raise ValueError(f"row_offset: {row_offset.numel() - 1} experts, the weights have {L}")
     if x.shape[0] != y.shape[0] or x.shape[1] != k or y.shape[1] != n:
@@ -384,8 +411,9 @@ def grouped_matmul_wgrad(dy, x, row_offset, out=None, out_dtype=torch.bfloat16, 
 # ---- SwiGLU -------------------------------------------------------------------
 
 def _check_gate_up(a, row_weight, row_offset):
-    lda = _matrix(a, "gate_up", (torch.bfloat16,))
+    lda = _matrix(a, "gate_up", (torch.bfloat16,), most=2 * _MAX_COLS)
     rows, cols = a.shape
+    _at_most(rows, "rows", _MAX_ROWS)
     if cols % 2:
         raise ValueError(f"gate_up: need gate and up columns, got {cols}")
     if row_weight is not None:
@@ -441,7 +469,7 @@ def swiglu(gate_up, row_weight=None, row_offset=None, out=None, scales=None, out
 def check_swiglu_backward_inputs(a, dh, row_weight, row_offset, da, drow_weight):
     rows, I, lda, L = _check_gate_up(a, row_weight, row_offset)
     ldh = _matrix(dh, "dh", (torch.bfloat16,))
-    ldda = _matrix(da, "out", (torch.bfloat16,))
+    ldda = _matrix(da, "out", (torch.bfloat16,), most=2 * _MAX_COLS)
     if tuple(dh.shape) != (rows, I):
         raise ValueError(f"dh: need shape {(rows, I)}, got {tuple(dh.shape)}")
     if tuple(da.shape) != (rows, 2 * I):
@@ -484,6 +512,10 @@ def check_quantize_inputs(x, block_rows, row_offset, codes, scales):
     if codes.shape != x.shape:
         raise ValueError(f"out: need shape {tuple(x.shape)}, got {tuple(codes.shape)}")
     shape = _scale_shape(x, block_rows)
+    _at_most(x.shape[-2], "rows", _MAX_ROWS)
+    _at_most(x.shape[0] if x.dim() == 3 else 1, "matrices", _MAX_BATCH)
+    if block_rows != 1:
+        _at_most(shape[-2] * shape[-1], f"blocks of {BLOCK} x {BLOCK}", _MAX_BLOCKS)
     if not isinstance(scales, torch.Tensor) or tuple(scales.shape) != shape:
         raise ValueError(f"scales: need shape {shape}")
     _vector(scales, "scales", scales.numel(), torch.float32)
@@ -533,6 +565,9 @@ def check_fp8_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None
     n = w.shape[-2]
     if n < 1:
         raise ValueError("w: no output features")
+    _at_most(rows, "rows", _MAX_ROWS)
+    _at_most(n, "output features", _MAX_COLS)
+    _choice(tile, splits)
     if w.shape[-1] != k or tuple(y.shape) != (rows, n):
         raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, w {tuple(w.shape)}, out {tuple(y.shape)}")
     if tuple(x_scales.shape) != (rows, _blocks(k)):

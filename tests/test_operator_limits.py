@@ -42,3 +42,57 @@ def test_combine_rows_takes_more_tokens_in_pieces(monkeypatch):
     with pytest.raises(ValueError):   # what is wrong with the whole call is said before any piece
         ops.combine_rows(rows, at, 3, out=torch.zeros(231, 16))
     assert len(made) == 3
+
+
+def stretched(shape, strides, dtype=BF):
+    return torch.empty_strided(shape, strides, dtype=dtype, device="meta")
+
+
+def off(n=1):
+    return meta(n + 1, dtype=I32)
+
+
+FWD = _lib.MOE_GROUPED_FORWARD
+ROWS, COLS, STRIDE, MATRIX = 1 << 28, 1 << 20, 1 << 32, 1 << 52
+# name: a check of a size (or stride, or number) that is the limit's with 0, past it with 1
+LIMITS = {
+    "dispatch_rows": lambda d: ops.check_dispatch_inputs(meta(4, 8), meta(ROWS + 1, dtype=I32), off(), 2, meta(ROWS + d, 8)),
+    "dispatch_hidden": lambda d: ops.check_dispatch_inputs(meta(4, COLS + d), meta(8, dtype=I32), off(), 2, meta(8, COLS + d)),
+    "dispatch_stride": lambda d: ops.check_dispatch_inputs(stretched((4, 8), (STRIDE + d, 1)), meta(8, dtype=I32), off(), 2, meta(8, 8)),
+    "combine_rows": lambda d: ops.check_combine_rows_inputs(meta(ROWS + d, 8), meta(8, dtype=I32), 2, meta(4, 8)),
+    "combine_out_stride": lambda d: ops.check_combine_rows_inputs(meta(8, 8), meta(8, dtype=I32), 2, stretched((4, 8), (STRIDE + d, 1))),
+    "grouped_rows": lambda d: ops.check_grouped_inputs(FWD, meta(ROWS + d, 8), meta(1, 8, 8), meta(ROWS + d, 8), off()),
+    "grouped_k": lambda d: ops.check_grouped_inputs(FWD, meta(4, COLS + d), meta(1, 8, COLS + d), meta(4, 8), off()),
+    "grouped_n": lambda d: ops.check_grouped_inputs(FWD, meta(4, 8), meta(1, COLS + d, 8), meta(4, COLS + d), off()),
+    "grouped_expert_stride": lambda d: ops.check_grouped_inputs(
+        FWD, meta(4, 8), stretched((2, 8, 8), (MATRIX + d, 8, 1)), meta(4, 8), off(2)),
+    "grouped_splits": lambda d: ops.check_grouped_inputs(FWD, meta(4, 8), meta(1, 8, 8), meta(4, 8), off(), splits=64 + d),
+    "grouped_no_splits": lambda d: ops.check_grouped_inputs(FWD, meta(4, 8), meta(1, 8, 8), meta(4, 8), off(), splits=-d),
+    "grouped_tile": lambda d: ops.check_grouped_inputs(FWD, meta(4, 8), meta(1, 8, 8), meta(4, 8), off(), tile=-d),
+    "swiglu_rows": lambda d: ops.check_swiglu_inputs(meta(ROWS + d, 16), None, None, meta(ROWS + d, 8), None),
+    "swiglu_inter": lambda d: ops.check_swiglu_inputs(meta(4, 2 * (COLS + d)), None, None, meta(4, COLS + d), None),
+    "swiglu_scale_stride": lambda d: ops.check_swiglu_inputs(
+        meta(4, 16), None, None, meta(4, 8, dtype=F8), stretched((4, 1), (STRIDE + d, 1), F32)),
+    "swiglu_backward_rows": lambda d: ops.check_swiglu_backward_inputs(
+        meta(ROWS + d, 16), meta(ROWS + d, 8), None, None, meta(ROWS + d, 16), None),
+    "quantize_rows": lambda d: ops.check_quantize_inputs(
+        meta(ROWS + d, 8), 1, None, meta(ROWS + d, 8, dtype=F8), meta(ROWS + d, 1, dtype=F32)),
+    "quantize_batch": lambda d: ops.check_quantize_inputs(
+        meta(65535 + d, 1, 8), 1, None, meta(65535 + d, 1, 8, dtype=F8), meta(65535 + d, 1, 1, dtype=F32)),
+    "quantize_blocks": lambda d: ops.check_quantize_inputs(
+        meta(1 << 17, (1 << 20) - 128 * (1 - d)), 128, None, meta(1 << 17, (1 << 20) - 128 * (1 - d), dtype=F8),
+        meta(1 << 10, (1 << 13) - 1 + d, dtype=F32)),
+    "fp8_rows": lambda d: ops.check_fp8_inputs(meta(ROWS + d, 16, dtype=F8), meta(ROWS + d, 1, dtype=F32), meta(8, 16, dtype=F8),
+                                               meta(1, 1, dtype=F32), None, meta(ROWS + d, 8)),
+    "fp8_n": lambda d: ops.check_fp8_inputs(meta(4, 16, dtype=F8), meta(4, 1, dtype=F32), meta(COLS + d, 16, dtype=F8),
+                                            meta(-(-(COLS + d) // 128), 1, dtype=F32), None, meta(4, COLS + d)),
+    "fp8_splits": lambda d: ops.check_fp8_inputs(meta(4, 16, dtype=F8), meta(4, 1, dtype=F32), meta(8, 16, dtype=F8),
+                                                 meta(1, 1, dtype=F32), None, meta(4, 8), splits=64 + d),
+}
+
+
+@pytest.mark.parametrize("name", sorted(LIMITS))
+def test_sizes_past_the_limits_are_refused(name):
+    LIMITS[name](0)
+    with pytest.raises(ValueError):
+        LIMITS[name](1)

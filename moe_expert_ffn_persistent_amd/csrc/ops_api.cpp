@@ -23,6 +23,10 @@ int32_t done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// offsets, indices, fp32 scales and weights
+template <class... P>
+bool words(const P*... p) { return (aligned(p, 4) && ...); }
+
 // a row stride of rows of `cols` elements
 bool stride_ok(long long ld, long long cols) { return ld >= cols && ld <= kMaxStride; }
 
@@ -176,7 +180,7 @@ int32_t grouped(const moe_grouped_params* p, const int32_t* row_offset, void* x,
                 void* workspace, int64_t bytes, hipStream_t stream) {
   const bool wgrad = p->op == MOE_GROUPED_WGRAD, fwd = p->op == MOE_GROUPED_FORWARD;
   if (p->rows == 0 && (!wgrad || p->accumulate)) return MOE_OK;
-  if (!row_offset || !w || (p->rows && (!x || !y))) return MOE_ERR_INVALID_ARG;
+  if (!row_offset || !w || (p->rows && (!x || !y)) || !words(row_offset)) return MOE_ERR_INVALID_ARG;
   const size_t oe = p->out_dtype == MOE_Y_BF16 ? 2 : 4;
   if (!aligned(x, !fwd && !wgrad ? oe : 2) || !aligned(y, fwd ? oe : 2) || !aligned(w, wgrad ? oe : 2) ||
       !aligned(workspace, 16))
@@ -231,7 +235,8 @@ int32_t fp8(const moe_fp8_params* p, const int32_t* row_offset, const void* x, c
             const float* w_scales, void* y, int splits, void* workspace, int64_t bytes, hipStream_t stream) {
   if (!row_offset && p->num_experts != 1) return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
-  if (!x || !x_scales || !w || !w_scales || !y || !aligned(y, p->out_dtype == MOE_Y_BF16 ? 2 : 4) || !aligned(workspace, 16))
+  if (!x || !x_scales || !w || !w_scales || !y || !aligned(y, p->out_dtype == MOE_Y_BF16 ? 2 : 4) || !aligned(workspace, 16) ||
+      !words(row_offset, x_scales, w_scales))
     return MOE_ERR_INVALID_ARG;
   GemmArgs a = fp8_args(p);
   a.row_offset = row_offset;
@@ -261,7 +266,7 @@ int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t
       !stride_ok(p->ld_rows, p->hidden) || p->tokens > kMaxTokens)
     return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
-  if (!row_pair || !row_offset || !out || (p->tokens && !x)) return MOE_ERR_INVALID_ARG;
+  if (!row_pair || !row_offset || !out || (p->tokens && !x) || !words(row_pair, row_offset)) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, p->elem_bytes) || !aligned(out, p->elem_bytes)) return MOE_ERR_INVALID_ARG;
   RowsArgs a{};
   a.in = x;
@@ -285,7 +290,7 @@ int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t
       !stride_ok(p->ld_rows, p->hidden) || p->tokens > kMaxCombineTokens)
     return MOE_ERR_INVALID_ARG;
   if (p->tokens == 0) return MOE_OK;
-  if (!pair_row || !y || (p->rows && !in)) return MOE_ERR_INVALID_ARG;
+  if (!pair_row || !y || (p->rows && !in) || !words(pair_row)) return MOE_ERR_INVALID_ARG;
   const size_t out_elem = p->out_dtype == MOE_Y_BF16 ? 2 : 4;
   if (!aligned(in, 2) || !aligned(y, out_elem)) return MOE_ERR_INVALID_ARG;
   RowsArgs a{};
@@ -328,7 +333,9 @@ int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_
   const bool fp8 = p->out_format == MOE_SWIGLU_FP8;
   if (fp8 && !stride_ok(p->ld_scales, (p->inter + 127) / 128)) return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
-  if (!a_ || !h || (fp8 && !h_scales) || !aligned(a_, 2) || (!fp8 && !aligned(h, 2))) return MOE_ERR_INVALID_ARG;
+  if (!a_ || !h || (fp8 && !h_scales) || !aligned(a_, 2) || (!fp8 && !aligned(h, 2)) ||
+      !words(row_weight, row_offset, h_scales))
+    return MOE_ERR_INVALID_ARG;
   SwigluArgs a{};
   a.a = a_;
   a.weight = row_weight;
@@ -352,7 +359,9 @@ int32_t moe_swiglu_backward(const moe_swiglu_params* p, const void* a_, const vo
       (row_offset && (p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS)))
     return MOE_ERR_INVALID_ARG;
   if (p->rows == 0) return MOE_OK;
-  if (!a_ || !dh || !da || !aligned(a_, 2) || !aligned(dh, 2) || !aligned(da, 2)) return MOE_ERR_INVALID_ARG;
+  if (!a_ || !dh || !da || !aligned(a_, 2) || !aligned(dh, 2) || !aligned(da, 2) ||
+      !words(row_weight, row_offset, drow_weight))
+    return MOE_ERR_INVALID_ARG;
   SwigluArgs a{};
   a.a = a_;
   a.dh = dh;
@@ -389,7 +398,7 @@ int32_t moe_quantize_fp8(const moe_quantize_params* p, const void* x, const int3
     return MOE_ERR_UNSUPPORTED;
   const bool fp32 = p->in_dtype == MOE_Y_FP32;
   const int xe = fp32 ? 4 : 2;
-  if (!x || !codes || !scales || !aligned(x, xe)) return MOE_ERR_INVALID_ARG;
+  if (!x || !codes || !scales || !aligned(x, xe) || !words(row_offset, scales)) return MOE_ERR_INVALID_ARG;
   QuantArgs a{};
   a.x = x;
   a.row_offset = row_offset;

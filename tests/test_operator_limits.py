@@ -96,3 +96,24 @@ def test_sizes_past_the_limits_are_refused(name):
     LIMITS[name](0)
     with pytest.raises(ValueError):
         LIMITS[name](1)
+
+
+POINTERS = {   # parameters, and the alignment of each pointer
+    "moe_dispatch_rows": (lambda: _lib.MoeRowsParams(4, 8, 2, 8, 4, 2, 0, 8, 8), (4, 4, 4, 4)),
+    "moe_combine_rows": (lambda: _lib.MoeRowsParams(4, 8, 2, 8, 2, 0, 0, 8, 8), (2, 4, 4)),
+    "moe_grouped_matmul": (lambda: _lib.MoeGroupedParams(0, 2, 4, 0, 8, 16, 16, 16, 8, 128, 0, 0, 0), (4, 2, 2, 4)),
+    "moe_swiglu": (lambda: _lib.MoeSwigluParams(4, 8, 2, 1, 16, 8, 1, 0), (2, 4, 4, 1, 4)),
+    "moe_swiglu_backward": (lambda: _lib.MoeSwigluParams(4, 8, 2, 0, 16, 8, 0, 16), (2, 2, 4, 4, 2, 4)),
+    "moe_quantize_fp8": (lambda: _lib.MoeQuantizeParams(4, 1, 8, 1, 0, 2, 8, 8, 0, 0), (4, 4, 1, 4)),
+    "moe_fp8_matmul": (lambda: _lib.MoeFp8Params(2, 4, 0, 8, 256, 256, 2, 256, 8, 2048, 0, 0), (4, 1, 4, 1, 4, 4)),
+}
+
+
+@pytest.mark.parametrize("name", sorted(POINTERS))
+def test_c_entries_refuse_pointers_off_their_elements(name):
+    params, need = POINTERS[name]
+    for i, n in enumerate(need):
+        for by in range(1, n):
+            ptrs = [1 << 20] * len(need)
+            ptrs[i] += by
+            assert getattr(_lib_or_skip(), name)(ctypes.byref(params()), *ptrs, None) == _lib.MOE_ERR_INVALID_ARG, (i, by)

@@ -3,7 +3,8 @@ _opcall.so in-tree for gfx950.
 
 Each source under csrc/ is compiled to an object under _build/ (in
 parallel), then linked into moe_expert_ffn_persistent_amd/libmoe_ffn.so.
-opcall.cpp is a Python module (host code against torch's headers).
+opcall.cpp is a Python module (host code against torch's headers); where it
+cannot be built the library is, and the operators work without it.
 Run ``python -m moe_expert_ffn_persistent_amd.build``; it always rebuilds.
 """
 from __future__ import annotations
@@ -86,13 +87,19 @@ def build(verbose: bool = True) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
         opcall = ex.submit(_build_opcall)
         objs = list(ex.map(_compile, SOURCES))
-        opcall.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    try:
+        opcall.result()
+    except (RuntimeError, OSError, ImportError) as e:
+        # the operators work without it; one of an earlier build may not fit
+        if os.path.exists(OPCALL):
+            os.remove(OPCALL)
+        print(f"the operators' call path was not built, their calls will take longer: {e}", file=sys.stderr)
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -22,6 +22,7 @@ when that was saved for a backward pass.
 from __future__ import annotations
 
 import ctypes
+import warnings
 
 import torch
 from torch.autograd import forward_ad
@@ -183,7 +184,8 @@ def _ptr(t):
 _ENTRY: dict = {}   # entry point -> its address, once it has been called
 _get_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
-_again = _remember = None
+_again = _remember = None   # the compiled call path, once it is loaded
+_no_call_path = False       # it has not been built
 
 
 def _check_stream(stream, device):
@@ -224,8 +226,18 @@ def _call(name, check, args, plain, tensors, written, stream):
     _first_call(name, check, args, plain, tensors, written, stream)
 
 
+def _load_call_path():
+    global _again, _remember, _no_call_path
+    try:
+        call = _lib.load_opcall()
+    except RuntimeError as e:
+        _no_call_path = True
+        warnings.warn(f"{e}; every call is checked and takes longer until then", RuntimeWarning)
+    else:
+        _again, _remember = call.again, call.remember
+
+
 def _first_call(name, check, args, plain, tensors, written, stream):
-    global _again, _remember
     params = check(*args)
     device = next(t for t in tensors if t is not None).device
     _need_device(device)
@@ -233,9 +245,8 @@ def _first_call(name, check, args, plain, tensors, written, stream):
         _check_stream(stream, device.index)
     lib = _lib.load()
     fn = getattr(lib, name)
-    if _again is None:
-        call = _lib.load_opcall()
-        _again, _remember = call.again, call.remember
+    if _again is None and not _no_call_path:
+        _load_call_path()
     pointers = [_ptr(t) for t in tensors]
     need = 0
     if name in _WORKSPACE:
@@ -248,6 +259,8 @@ def _first_call(name, check, args, plain, tensors, written, stream):
     if st != _lib.MOE_OK:
         _lib.check(st, name)
     increment_version([t for i, t in enumerate(tensors) if written >> i & 1 and t is not None])
+    if _remember is None:
+        return
     entry = _ENTRY[name] = ctypes.cast(fn, ctypes.c_void_p).value
     _remember(bytes(params), entry, device.index, need, plain, *tensors, written=written)
 

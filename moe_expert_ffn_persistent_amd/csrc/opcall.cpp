@@ -209,7 +209,11 @@ PyObject* remember(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject*
   if (got == 0) Py_RETURN_FALSE;
   if (plans().size() >= kMaxPlans) plans().clear();
   std::memcpy(plan.params, PyBytes_AS_STRING(args[0]), (size_t)PyBytes_GET_SIZE(args[0]));
-  plans()[c.key] = plan;
+  try {
+    plans()[c.key] = plan;
+  } catch (...) {
+    Py_RETURN_FALSE;   // no memory for it: the next call is checked again
+  }
   Py_RETURN_TRUE;
 }
 

@@ -92,6 +92,7 @@ struct Call {
       key.append(reinterpret_cast<const char*>(sizes.data()), sizes.size() * sizeof(int64_t));
       key.append(reinterpret_cast<const char*>(strides.data()), strides.size() * sizeof(int64_t));
       ptr[i] = t.data_ptr();
+      if (ptr[i] == nullptr && t.numel() > 0) return false;   // a wrapper without memory would count as absent
       this->device = t.device();
     }
     return true;

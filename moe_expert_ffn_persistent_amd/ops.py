@@ -248,6 +248,9 @@ def _first_call(name, check, args, plain, tensors, written, stream):
     if _again is None and not _no_call_path:
         _load_call_path()
     pointers = [_ptr(t) for t in tensors]
+    for t, p in zip(tensors, pointers):
+        if p == 0 and t.numel():   # it would count as absent
+            raise ValueError(f"a {type(t).__name__} of shape {tuple(t.shape)} holds no memory of its own")
     need = 0
     if name in _WORKSPACE:
         need = params.workspace_bytes = getattr(lib, _WORKSPACE[name])(ctypes.byref(params))

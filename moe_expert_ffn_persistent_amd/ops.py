@@ -203,10 +203,10 @@ _WORKSPACE = {"moe_grouped_matmul_split": "moe_grouped_workspace_bytes", "moe_fp
 
 def _call(name, check, args, plain, tensors, written, stream):
     """One C entry point, ``tensors`` its pointers in order, of which it writes
-    those whose bit is set in ``written``. ``check(*args)``
-    makes its parameters from their sizes and the ``plain`` arguments; for
-    sizes that it has seen the call is made again without it (csrc/opcall.cpp:
-    a call costs the host 3.9 us, 3.4 of them the launch)."""
+    those whose bit is set in ``written``. ``check(*args)`` makes its parameters
+    from their sizes and the ``plain`` arguments; for sizes that it has seen the
+    call is made again without it (csrc/opcall.cpp: a call costs the host 3.9 us,
+    3.4 of them the launch)."""
     entry = _ENTRY.get(name)
     if entry is not None:
         device = _get_device()

@@ -19,10 +19,11 @@ ts = [torch.zeros(2, 2) for _ in range(3)]
 plain = (1,) * (8 << 20)                                       # a key of 128 MiB
 assert opcall.again(entry, -1, 0, True, plain, *ts) is None    # its storage stays
 used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
-resource.setrlimit(resource.RLIMIT_AS, (used + (64 << 20), resource.RLIM_INFINITY))
+limits = resource.getrlimit(resource.RLIMIT_AS)
+resource.setrlimit(resource.RLIMIT_AS, (used + (64 << 20), limits[1]))
 assert not opcall.remember(b"12345678", entry, -1, 0, plain, *ts)   # would keep a copy of the key
 print("not kept", flush=True)
-resource.setrlimit(resource.RLIMIT_AS, (resource.RLIM_INFINITY, resource.RLIM_INFINITY))
+resource.setrlimit(resource.RLIMIT_AS, limits)
 assert opcall.again(entry, -1, 0, True, plain, *ts) is None    # nothing was kept
 assert opcall.remember(b"12345678", entry, -1, 0, (1,), *ts) and opcall.again(entry, -1, 0, True, (1,), *ts) == 0
 print("works", flush=True)

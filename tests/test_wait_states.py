@@ -4,7 +4,7 @@ The copies are inline assembly, whose operands the compiler's hazard pass does
 not look into, so the instructions around them are read back from the
 disassembly. On gfx950 two distances have to be kept:
 
-  an SALU write of m0, then a copy that places its data by m0:  1 wait state
+  a write of m0, then a copy that places its data by m0:  1 wait state
   a VALU write of an SGPR, then a memory operation reading it:  5 wait states"""
 import os
 import re
@@ -30,7 +30,7 @@ def hazards(lines):
     """(rule, instruction, states between) of every distance that is too short,
     and the number of copies seen. An instruction is a state, s_nop n is n + 1."""
     found, copies = [], 0
-    now, m0, written = 0, None, {}   # states so far; when m0 and each SGPR were last written (by an SALU, by a VALU)
+    now, m0, written = 0, None, {}   # states so far; when m0 was last written, and each SGPR by a VALU
     for line in lines:
         if line.rstrip().endswith(">:"):   # another function
             m0, written = None, {}
@@ -54,8 +54,8 @@ def hazards(lines):
         elif op.startswith("s_") and not op.startswith(("s_nop", "s_cmp", "s_bitcmp")):
             for r in sgprs(first):
                 written.pop(r, None)
-            if first.strip() == "m0":
-                m0 = now
+        if first.strip() == "m0" and not op.startswith(MEMORY):
+            m0 = now
     return found, copies
 
 

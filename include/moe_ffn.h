@@ -461,6 +461,31 @@ int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t
 int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row, void* y,
                          void* stream);
 
+/* The same sum with a weight for each pair: y[n] = sum over j of
+ * weights[n*top_k + j] in[pair_row[n*top_k + j]], fp32, one fused multiply-add a
+ * slot in ascending j. weights: device fp32 [tokens, top_k]; those of slots that
+ * add nothing are not looked at. */
+int32_t moe_combine_weighted_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row,
+                                  const float* weights, void* y, void* stream);
+
+/* Its gradients, for slots whose pair_row is 0 .. rows-1 (row r = pair_row[f] of
+ * pair f = n*top_k + j):
+ *   din[r] = weights[f] dy[n]          bf16 [rows, hidden]; other rows stay; may be `in`
+ *   dweights[f] = dy[n] . in[r]        fp32 [tokens, top_k]; 0 for the other slots
+ * A row belongs to one pair, as in a layout's pair_row: of a row named twice,
+ * din holds either pair's gradient. */
+typedef struct {
+  int64_t tokens;        /* at most 2^23 */
+  int64_t rows;
+  int32_t top_k;         /* 1..16 */
+  int32_t hidden;
+  int32_t dy_dtype;      /* MOE_Y_FP32 or MOE_Y_BF16 */
+  int64_t ld_dy, ld_rows, ld_drows;
+} moe_combine_backward_params;
+int32_t moe_combine_rows_backward(const moe_combine_backward_params* p, const void* dy, const void* in,
+                                  const int32_t* pair_row, const float* weights, void* din,
+                                  float* dweights, void* stream);
+
 /* Matrix products grouped by expert, bf16 with fp32 accumulation. For every
  * expert e and its rows r:
  *   MOE_GROUPED_FORWARD  y[r] = W[e] x[r]                 (writes y)
@@ -588,6 +613,115 @@ int64_t moe_fp8_workspace_bytes(const moe_fp8_params* p);
 int32_t moe_fp8_matmul_split(const moe_fp8_params* p, const int32_t* row_offset, const void* x,
                              const float* x_scales, const void* w, const float* w_scales, void* y,
                              void* workspace, void* stream);
+
+/* RMS norm of the residual stream, with its addition:
+ *   s = x + residual (x where residual is NULL), rounded to the stream's type and
+ *       stored in residual_out
+ *   out = s / sqrt(mean of the row's s^2 + eps) * weight     (weight NULL: 1)
+ * in fp32, rounded once, in the format that the next product takes:
+ *   MOE_NORM_BF16, MOE_NORM_FP32
+ *   MOE_NORM_FP8       e4m3 with fp32 scales [rows, ceil(hidden/128)], as
+ *                      moe_quantize_fp8 with 1 x 128 blocks quantises the fp32 values
+ *   MOE_NORM_MX_E4M3,  MX codes with E8M0 scale bytes [rows, ceil(hidden/32)], as
+ *   MOE_NORM_MX_E2M1   moe_quantize_mx does
+ * The squares are fp32: a row with values past 1.8e19 has an infinite mean (its
+ * out is zeros), one with an infinity or NaN an out of NaN.
+ * residual_out may be x or residual (the same rows), and out x where types agree. */
+#define MOE_NORM_BF16 0
+#define MOE_NORM_FP32 1
+#define MOE_NORM_FP8 2
+#define MOE_NORM_MX_E4M3 3
+#define MOE_NORM_MX_E2M1 4
+typedef struct {
+  int64_t rows;
+  int32_t hidden;          /* any size >= 1 */
+  int32_t stream_dtype;    /* MOE_Y_FP32 or MOE_Y_BF16: x, residual, residual_out; dresidual, dx */
+  int32_t weight_dtype;    /* MOE_Y_FP32 or MOE_Y_BF16 */
+  int32_t format;          /* MOE_NORM_* of out; backward: MOE_NORM_BF16 or MOE_NORM_FP32, of dy */
+  int32_t weight_gradient; /* backward: dweight is written */
+  float eps;               /* > 0 */
+  int64_t ld_x;            /* strides in elements; of codes and scale bytes in bytes */
+  int64_t ld_residual, ld_residual_out, ld_out, ld_scales;
+  int64_t ld_dy, ld_dresidual, ld_dx;
+  int64_t workspace_bytes; /* backward */
+} moe_norm_params;
+int32_t moe_rms_norm(const moe_norm_params* p, const void* x, const void* residual, const void* weight,
+                     void* out, void* scales, void* residual_out, void* stream);
+
+/* Gradients of moe_rms_norm (bf16 and fp32 form) for dy [rows, hidden], x being
+ * the stream that was normalised (residual_out, or x where there was no
+ * residual): with r = 1 / sqrt(mean x^2 + eps) and g = dy * weight,
+ *   dx = dresidual + r (g - x r^2 mean(g x))     in the stream's type, rounded once:
+ *        the gradient of x and of residual alike; dresidual is the gradient that
+ *        reaches residual_out from elsewhere, or NULL; dx may be dresidual, dy or x
+ *   dweight = sum over the rows of dy x r        fp32 [hidden], or NULL; zeros
+ *        without rows; the order of the sum goes by sizes alone
+ * The workspace (device memory, 16-byte aligned, the call's own until it is done)
+ * holds partial sums of dweight: moe_rms_norm_workspace_bytes says its size, with
+ * less the call is MOE_ERR_WORKSPACE_TOO_SMALL. */
+int64_t moe_rms_norm_workspace_bytes(const moe_norm_params* p);
+int32_t moe_rms_norm_backward(const moe_norm_params* p, const void* dy, const void* x, const void* weight,
+                              const void* dresidual, void* dx, float* dweight, void* workspace,
+                              void* stream);
+
+/* Quantisation to the OCP Microscaling (MX) formats, the MOE_W4A8 operand format:
+ * blocks of 32 consecutive elements of a row share one E8M0 scale byte s, a value
+ * is code 2^(s - 127). s - 127 = floor(log2(amax)) less the format's largest
+ * exponent (8: e4m3, 2: e2m1), at least -127, 0 for a block of zeros; code = the
+ * value nearest to x / 2^(s - 127), ties to even, at most the largest (448, 6). A
+ * block with an infinity or NaN has the NaN scale 255 (and NaN codes in e4m3,
+ * zeros in e2m1).
+ *   x       [batch, rows, cols] bf16 or fp32
+ *   codes   e4m3: bytes [batch, rows, cols]; e2m1: [batch, rows, ceil(cols/2)], two a
+ *           byte, element 2i in the low bits of byte i (an odd row's last byte has
+ *           zeros in the high ones)
+ *   scales  bytes [batch, rows, ceil(cols/32)]
+ *   row_offset  NULL, or with batch 1: only rows row_offset[0] .. row_offset[L]-1 */
+#define MOE_MX_E4M3 0
+#define MOE_MX_E2M1 1
+typedef struct {
+  int64_t rows;
+  int32_t batch;           /* matrices, 1..65535 */
+  int32_t cols;            /* any size >= 1 */
+  int32_t format;          /* MOE_MX_* */
+  int32_t in_dtype;        /* MOE_Y_FP32 or MOE_Y_BF16 */
+  int32_t num_experts;     /* with row_offset */
+  int64_t ld_x;            /* strides of x in elements, of codes and scales in bytes */
+  int64_t ld_codes, ld_scales;
+  int64_t batch_stride_x, batch_stride_codes, batch_stride_scales;
+} moe_mx_quantize_params;
+int32_t moe_quantize_mx(const moe_mx_quantize_params* p, const void* x, const int32_t* row_offset,
+                        void* codes, void* scales, void* stream);
+
+/* Matrix product of MX operands, dense (row_offset NULL, num_experts 1) or grouped
+ * by expert: y[r, n] = sum over blocks b of 32 along k of
+ *   2^(x_scales[r, b] + w_scales[e, n, b] - 254) sum over k in b of x[r, k] W[e, n, k]
+ *   x [rows, k] e4m3 or e2m1 (two a byte, k even), x_scales [rows, ceil(k/32)];
+ *   w [num_experts, n, ceil(k/2) bytes] e2m1, w_scales [num_experts, n,
+ *   ceil(k/32)]; y bf16 or fp32 [rows, n]
+ * Products and scales are exact and the sums fp32, but for the matrix cores' own
+ * addition (see moe_fp8_matmul). A scale of 255 makes NaN of what it scales.
+ * The tile kernels take x, w and their strides in whole 16 bytes and the scales'
+ * in whole four (as moe_quantize_mx's outputs are when allocated so), a slower
+ * kernel anything else; k and n are any size in both.
+ * The workspace is as moe_grouped_matmul_split's (NULL: none). */
+typedef struct {
+  int32_t num_experts;
+  int64_t rows;
+  int64_t expected_rows;   /* 0 = rows */
+  int32_t n, k;            /* any size >= 1 */
+  int64_t ld_x, ld_x_scales, ld_w, ld_w_scales;   /* bytes */
+  int64_t ld_y;            /* elements */
+  int64_t expert_stride_w, expert_stride_w_scales; /* bytes */
+  int32_t x_format;        /* MOE_MX_* */
+  int32_t out_dtype;       /* MOE_Y_FP32 or MOE_Y_BF16 */
+  int32_t tile;            /* as moe_grouped_params */
+  int32_t splits;
+  int64_t workspace_bytes;
+} moe_mx_params;
+int64_t moe_mx_workspace_bytes(const moe_mx_params* p);
+int32_t moe_mx_matmul(const moe_mx_params* p, const int32_t* row_offset, const void* x, const void* x_scales,
+                      const void* w, const void* w_scales, void* y, void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

@@ -15,13 +15,15 @@ import torch
 from . import _lib
 from ._lib import (MOE_BF16, MOE_FP8_E4M3, MOE_SCHED_EXPERT_WAVE, MOE_SCHED_INTERLEAVED, MOE_W4A8,
                    MoeError, MoeLayout, MoePlan, MoeSchedParams, MoeShape)
-from .ops import (combine_rows, dispatch_rows, fp8_matmul, grouped_matmul, grouped_matmul_dgrad,
-                  grouped_matmul_wgrad, quantize_fp8, swiglu, swiglu_backward)
+from .ops import (combine_rows, combine_rows_backward, dispatch_rows, fp8_matmul, grouped_matmul, grouped_matmul_dgrad,
+                  grouped_matmul_wgrad, mx_matmul, quantize_fp8, quantize_mx, rms_norm, rms_norm_backward, swiglu,
+                  swiglu_backward)
 
 __all__ = ["MoeExpertFFN", "LayoutBuffers", "MoeError", "SCHEDULES", "make_shape", "prediction_dict",
            "make_params", "library", "check_layout_inputs", "check_combine_inputs",
            "dispatch_rows", "combine_rows", "grouped_matmul", "grouped_matmul_dgrad",
-           "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "quantize_fp8", "fp8_matmul"]
+           "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "quantize_fp8", "fp8_matmul",
+           "combine_rows_backward", "rms_norm", "rms_norm_backward", "quantize_mx", "mx_matmul"]
 
 SCHEDULES = {"expert_wave": MOE_SCHED_EXPERT_WAVE, "interleaved": MOE_SCHED_INTERLEAVED}
 SCHEDULE_NAMES = {v: k for k, v in SCHEDULES.items()}

@@ -30,6 +30,13 @@ MOE_GROUPED_DGRAD = 1
 MOE_GROUPED_WGRAD = 2
 MOE_SWIGLU_BF16 = 0
 MOE_SWIGLU_FP8 = 1
+MOE_NORM_BF16 = 0
+MOE_NORM_FP32 = 1
+MOE_NORM_FP8 = 2
+MOE_NORM_MX_E4M3 = 3
+MOE_NORM_MX_E2M1 = 4
+MOE_MX_E4M3 = 0
+MOE_MX_E2M1 = 1
 
 # every symbol include/moe_ffn.h declares
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_layout_scratch_bytes", "moe_ffn_plan",
@@ -38,7 +45,9 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_layout_scratch_bytes", "
            "moe_mfma_rate_probe", "moe_dispatch_rows", "moe_combine_rows", "moe_grouped_matmul",
            "moe_swiglu", "moe_swiglu_backward", "moe_quantize_fp8", "moe_fp8_matmul",
            "moe_grouped_workspace_bytes", "moe_grouped_matmul_split", "moe_fp8_workspace_bytes",
-           "moe_fp8_matmul_split")
+           "moe_fp8_matmul_split", "moe_combine_weighted_rows", "moe_combine_rows_backward", "moe_rms_norm",
+           "moe_rms_norm_workspace_bytes", "moe_rms_norm_backward", "moe_quantize_mx", "moe_mx_workspace_bytes",
+           "moe_mx_matmul")
 MFMA_PROBE_THREADS = 512
 MFMA_PROBE_OPERAND_BYTES = 64 * 64 * 16 * 16
 NOALLOC_WORKSPACE_BYTES = 64 << 20
@@ -128,6 +137,33 @@ class MoeFp8Params(ctypes.Structure):
                 ("workspace_bytes", c_i64)]
 
 
+class MoeCombineBackwardParams(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("rows", c_i64), ("top_k", c_i32), ("hidden", c_i32),
+                ("dy_dtype", c_i32), ("ld_dy", c_i64), ("ld_rows", c_i64), ("ld_drows", c_i64)]
+
+
+class MoeNormParams(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("hidden", c_i32), ("stream_dtype", c_i32), ("weight_dtype", c_i32),
+                ("format", c_i32), ("weight_gradient", c_i32), ("eps", ctypes.c_float),
+                ("ld_x", c_i64), ("ld_residual", c_i64), ("ld_residual_out", c_i64), ("ld_out", c_i64),
+                ("ld_scales", c_i64), ("ld_dy", c_i64), ("ld_dresidual", c_i64), ("ld_dx", c_i64),
+                ("workspace_bytes", c_i64)]
+
+
+class MoeMxQuantizeParams(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("batch", c_i32), ("cols", c_i32), ("format", c_i32), ("in_dtype", c_i32),
+                ("num_experts", c_i32), ("ld_x", c_i64), ("ld_codes", c_i64), ("ld_scales", c_i64),
+                ("batch_stride_x", c_i64), ("batch_stride_codes", c_i64), ("batch_stride_scales", c_i64)]
+
+
+class MoeMxParams(ctypes.Structure):
+    _fields_ = [("num_experts", c_i32), ("rows", c_i64), ("expected_rows", c_i64), ("n", c_i32),
+                ("k", c_i32), ("ld_x", c_i64), ("ld_x_scales", c_i64), ("ld_w", c_i64), ("ld_w_scales", c_i64),
+                ("ld_y", c_i64), ("expert_stride_w", c_i64), ("expert_stride_w_scales", c_i64),
+                ("x_format", c_i32), ("out_dtype", c_i32), ("tile", c_i32), ("splits", c_i32),
+                ("workspace_bytes", c_i64)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} ({status})")
@@ -185,11 +221,18 @@ def load(path: str | None = None):
                              ("moe_quantize_fp8", MoeQuantizeParams, 4),
                              ("moe_fp8_matmul", MoeFp8Params, 6),
                              ("moe_grouped_matmul_split", MoeGroupedParams, 5),
-                             ("moe_fp8_matmul_split", MoeFp8Params, 7)):
+                             ("moe_fp8_matmul_split", MoeFp8Params, 7),
+                             ("moe_combine_weighted_rows", MoeRowsParams, 4),
+                             ("moe_combine_rows_backward", MoeCombineBackwardParams, 6),
+                             ("moe_rms_norm", MoeNormParams, 6),
+                             ("moe_rms_norm_backward", MoeNormParams, 7),
+                             ("moe_quantize_mx", MoeMxQuantizeParams, 4),
+                             ("moe_mx_matmul", MoeMxParams, 7)):
         f = getattr(lib, fn)
         f.restype = c_i32
         f.argtypes = [P(params)] + [c_vp] * (nptr + 1)
-    for fn, params in (("moe_grouped_workspace_bytes", MoeGroupedParams), ("moe_fp8_workspace_bytes", MoeFp8Params)):
+    for fn, params in (("moe_grouped_workspace_bytes", MoeGroupedParams), ("moe_fp8_workspace_bytes", MoeFp8Params),
+                       ("moe_rms_norm_workspace_bytes", MoeNormParams), ("moe_mx_workspace_bytes", MoeMxParams)):
         f = getattr(lib, fn)
         f.restype = c_i64
         f.argtypes = [P(params)]

@@ -124,7 +124,39 @@ struct RowsArgs {
   int k, hidden, elem, L;
 };
 hipError_t launch_dispatch_rows(const RowsArgs& a, hipStream_t s);
-hipError_t launch_combine_rows(const RowsArgs& a, bool bf16_out, hipStream_t s);
+// weights: fp32 of every pair, or nullptr (1)
+hipError_t launch_combine_rows(const RowsArgs& a, const float* weights, bool bf16_out, hipStream_t s);
+
+struct CombineBackwardArgs {
+  const void *dy, *rows;
+  const int32_t* pair_row;
+  const float* weights;
+  void* drows;
+  float* dweights;
+  long long cap, ld_dy, ld_rows, ld_drows;   // rows that the buffers hold; strides in elements
+  int tokens, k, hidden;
+  bool dy_fp32, vec;                         // vec: rows of all three are 16-byte aligned
+};
+hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t s);
+
+// RMS norm (norm.hip), strides in elements (codes and scale bytes in bytes).
+// Forward: stream = x + residual (x without one), out = stream / rms * weight in
+// the format; backward: out (of dy) and dx of the stream, partial sums of dweight.
+struct NormArgs {
+  const void *x, *residual, *weight, *dy;
+  void *out, *scales, *stream, *dx;   // stream: where the sum is stored
+  const void* dresidual;
+  float *dweight, *part;              // part: [groups, hidden], or dweight itself
+  long long rows, ld_x, ld_residual, ld_stream, ld_out, ld_scales, ld_dy, ld_dresidual, ld_dx;
+  int hidden, format;                 // MOE_NORM_*; backward: of dy
+  float eps;
+  bool fp32, weight_fp32;             // type of the stream (x, residual, dx, ...); of weight
+  bool vec;                           // every row and the weight are 16-byte aligned (codes 8, e2m1 codes 4)
+};
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
+// workgroups of the backward pass, each with a partial sum of dweight
+int norm_backward_groups(long long rows, int hidden);
+hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s);
 
 struct SwigluArgs {
   const void *a, *dh;
@@ -150,6 +182,17 @@ struct QuantArgs {
 };
 hipError_t launch_quantize(const QuantArgs& a, int block_rows, bool fp32, hipStream_t s);
 
+// Microscaled formats (mx_quantize.hip); strides of codes and scales in bytes
+struct MxQuantArgs {
+  const void* x;
+  const int32_t* row_offset;
+  uint8_t *codes, *scales;
+  long long rows, ld_x, ld_codes, ld_scales, bs_x, bs_codes, bs_scales;
+  int batch, cols, L;
+  bool vec;                    // rows of x are 16-byte aligned, of codes as whole stores of a lane
+};
+hipError_t launch_quantize_mx(const MxQuantArgs& a, bool e2m1, bool fp32, hipStream_t s);
+
 // Grouped products: x [rows, k], w [L, n, k], y [rows, n], one of them written
 // (op: MOE_GROUPED_*); the block-scaled e4m3 product is the forward form with
 // scales. row_offset nullptr: one expert with every row.
@@ -165,6 +208,9 @@ struct GemmArgs {
   // up in fp32 at s * part elements past the output
   int splits;
   long long part;
+  // The product of MX operands: xs and ws are E8M0 bytes, all strides but ld_y's in bytes
+  long long ld_ws, es_ws;
+  bool x_e2m1, vec_out;        // rows of y are 16-byte aligned
 };
 constexpr int kCus = 256;   // compute units, places for a persistent workgroup
 hipError_t launch_gemm_any(const GemmArgs& a, bool fp8, hipStream_t s);
@@ -182,6 +228,7 @@ GemmArgs split_args(const GemmArgs& a, float* ws);
 hipError_t launch_join_splits(const GemmArgs& a, const float* ws, hipStream_t s);
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s);
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s);
+hipError_t launch_gemm_mx_any(const GemmArgs& a, hipStream_t s);
 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t stream);
 

@@ -1,0 +1,418 @@
+// RMS norm of the residual stream, forward with the stream's addition and the
+// output in the format that the next product takes, and its gradients:
+//
+//   s = x + residual, rounded to the stream's type and stored
+//   r = 1 / sqrt(mean over the row of s^2 + eps),  y = s r w
+//
+//   g = dy w,  dx = dresidual + r (g - s r^2 mean(g s)),  dw = sum over rows of dy s r
+//
+// One pass over the bytes: a row stays in the registers of its threads between
+// its sums and what they scale. fp32 throughout. Bound by HBM when large and by
+// the launch when small.
+#include "internal.hpp"
+#include "mx_common.hpp"
+
+namespace moe {
+namespace {
+
+enum Kind { kPlain, kFp8, kMx };   // outputs without scales, e4m3 with fp32 scales, MX
+
+__device__ __forceinline__ float rms_inv(float squares, int hidden, float eps) {
+  return 1.f / sqrtf(squares / (float)hidden + eps);
+}
+
+// Sums of N values over the tpr threads of a row, to all of them. Rows of more
+// than a wavefront join through `part`; every thread of the workgroup calls.
+template <int N, int THREADS>
+__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float (*part)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    for (int d = 1; d < min(tpr, 64); d <<= 1) v[k] += __shfl_xor(v[k], d, 64);
+  if (tpr > 64) {
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) part[threadIdx.x >> 6][k] = v[k];
+    __syncthreads();
+    const int w0 = (threadIdx.x / tpr) * (tpr >> 6);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = 0.f;
+    for (int i = 0; i < tpr / 64; ++i)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += part[w0 + i][k];
+  }
+}
+
+// v + residual, rounded to the stream's type and stored
+template <class T>
+__device__ __forceinline__ void add_stream(const NormArgs& a, long long r, int c, int m, bool vec, float (&v)[8]) {
+  if (m <= 0) return;
+  float o[8];
+  load8(static_cast<const T*>(a.residual) + r * a.ld_residual + c, m, vec, o);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (float)(T)(v[i] + o[i]);
+}
+
+__device__ __forceinline__ void store8(float* p, int n, bool vec, const float (&x)[8]) {
+  if (vec) {
+    reinterpret_cast<float4*>(p)[0] = float4{x[0], x[1], x[2], x[3]};
+    reinterpret_cast<float4*>(p)[1] = float4{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = x[i];
+  }
+}
+
+// Eight columns of the weight (1 without one, 0 behind the row's end)
+__device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[8]) {
+  const int m = min(8, a.hidden - c);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = i < m ? 1.f : 0.f;
+  if (a.weight == nullptr || m <= 0) return;
+  if (a.weight_fp32) load8(static_cast<const float*>(a.weight) + c, m, a.vec && m == 8, w);
+  else load8(static_cast<const __bf16*>(a.weight) + c, m, a.vec && m == 8, w);
+}
+
+// Eight columns of the output. The lanes of a scale block (16, or 4) call together.
+template <int KIND>
+__device__ __forceinline__ void store_out(const NormArgs& a, long long r, int c, bool vec, const float (&y)[8]) {
+  const int m = min(8, a.hidden - c);
+  if constexpr (KIND == kPlain) {
+    if (m <= 0) return;
+    if (a.format == MOE_NORM_BF16) moe::store8(static_cast<__bf16*>(a.out) + r * a.ld_out + c, m, vec, y);
+    else store8(static_cast<float*>(a.out) + r * a.ld_out + c, m, vec, y);
+  } else {
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = max(mx, i < m ? abs_bits(y[i]) : 0u);
+    uint8_t* row = static_cast<uint8_t*>(a.out) + r * a.ld_out;
+    if constexpr (KIND == kFp8) {
+      const float scale = block_scale(max16(mx));
+      if (m > 0) store_codes(row + c, m, vec, quant8(y, scale));
+      if (c % 128 == 0 && m > 0) static_cast<float*>(a.scales)[r * a.ld_scales + c / 128] = scale;
+    } else {
+      mx = max4(mx);
+      uint8_t byte;
+      if (a.format == MOE_NORM_MX_E2M1) {
+        const MxScale s = mx_scale<true>(mx);
+        store_mx<true, 8>(row, c, a.hidden, vec, y, s);
+        byte = s.byte;
+      } else {
+        const MxScale s = mx_scale<false>(mx);
+        store_mx<false, 8>(row, c, a.hidden, vec, y, s);
+        byte = s.byte;
+      }
+      if (c % 32 == 0 && m > 0) static_cast<uint8_t*>(a.scales)[r * a.ld_scales + c / 32] = byte;
+    }
+  }
+}
+
+// Rows of up to 8 P tpr columns: tpr threads take one, eight neighbouring
+// columns a thread in each of P pieces.
+template <class T, int KIND, int P, int THREADS>
+__global__ void __launch_bounds__(THREADS) moe_rms_norm_k(const NormArgs a, int tpr) {
+  __shared__ float part[2][THREADS / 64][1];
+  const int sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr, rpw = THREADS / tpr;
+  float w[P][8];
+#pragma unroll
+  for (int p = 0; p < P; ++p) load_weight(a, (p * tpr + t) * 8, w[p]);
+  int odd = 0;
+  for (long long base = (long long)blockIdx.x * rpw; base < a.rows; base += (long long)gridDim.x * rpw, odd ^= 1) {
+    const long long r = base + sub;
+    const bool live = r < a.rows;
+    float v[P][8], sum[1] = {0.f};
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
+      if (m > 0) load8(static_cast<const T*>(a.x) + r * a.ld_x + c, m, a.vec && m == 8, v[p]);
+    }
+    if (a.residual) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
+        add_stream<T>(a, r, c, m, a.vec && m == 8, v[p]);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
+      if (a.stream && m > 0) {
+        if constexpr (sizeof(T) == 4) store8(static_cast<float*>(a.stream) + r * a.ld_stream + c, m, a.vec && m == 8, v[p]);
+        else moe::store8(static_cast<__bf16*>(a.stream) + r * a.ld_stream + c, m, a.vec && m == 8, v[p]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(v[p][i], v[p][i], sum[0]);
+    }
+    row_sum<1, THREADS>(sum, tpr, part[odd]);
+    const float inv = rms_inv(sum[0], a.hidden, a.eps);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * tpr + t) * 8;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = v[p][i] * inv * w[p][i];
+      // a row that is not there: its lanes take part in no other row's blocks
+      if (live) store_out<KIND>(a, r, c, a.vec && a.hidden - c >= 8, y);
+    }
+  }
+}
+
+// Rows of any length: two passes over them, the second reads the stored stream.
+template <class T, int KIND>
+__global__ void __launch_bounds__(1024) moe_rms_norm_long_k(const NormArgs a) {
+  __shared__ float part[2][16][1];
+  const T* in = static_cast<const T*>(a.stream ? a.stream : a.x);
+  const long long ld = a.stream ? a.ld_stream : a.ld_x;
+  int odd = 0;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, odd ^= 1) {
+    float sum[1] = {0.f};
+    for (int c = threadIdx.x * 8; c < a.hidden; c += 8192) {
+      const int m = min(8, a.hidden - c);
+      const bool vec = a.vec && m == 8;
+      float v[8] = {};
+      load8(static_cast<const T*>(a.x) + r * a.ld_x + c, m, vec, v);
+      if (a.residual) add_stream<T>(a, r, c, m, vec, v);
+      if (a.stream) {
+        if constexpr (sizeof(T) == 4) store8(static_cast<float*>(a.stream) + r * a.ld_stream + c, m, vec, v);
+        else moe::store8(static_cast<__bf16*>(a.stream) + r * a.ld_stream + c, m, vec, v);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(v[i], v[i], sum[0]);
+    }
+    row_sum<1, 1024>(sum, 1024, part[odd]);
+    const float inv = rms_inv(sum[0], a.hidden, a.eps);
+    for (int c0 = 0; c0 < a.hidden; c0 += 8192) {   // every lane: scale blocks join theirs
+      const int c = c0 + threadIdx.x * 8, m = min(8, a.hidden - c);
+      float v[8] = {}, w[8];
+      if (m > 0) load8(in + r * ld + c, m, a.vec && m == 8, v);
+      load_weight(a, c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
+      store_out<KIND>(a, r, c, a.vec && m == 8, v);
+    }
+  }
+}
+
+// The gradients. A workgroup walks its rows and keeps its part of dw in
+// registers; the parts are joined by a second kernel, in their order.
+template <class T, class D, int P, int THREADS>
+__global__ void __launch_bounds__(THREADS) moe_rms_norm_backward_k(const NormArgs a, int tpr) {
+  __shared__ float part[2][THREADS / 64][2];
+  __shared__ float joined[P == 1 ? THREADS * 8 : 1];
+  const int sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr, rpw = THREADS / tpr;
+  float w[P][8], dw[P][8] = {};
+#pragma unroll
+  for (int p = 0; p < P; ++p) load_weight(a, (p * tpr + t) * 8, w[p]);
+  int odd = 0;
+  for (long long base = (long long)blockIdx.x * rpw; base < a.rows; base += (long long)gridDim.x * rpw, odd ^= 1) {
+    const long long r = base + sub;
+    const bool live = r < a.rows;
+    float v[P][8], d[P][8], sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[p][i] = d[p][i] = 0.f;
+      if (m > 0) {
+        load8(static_cast<const T*>(a.x) + r * a.ld_x + c, m, a.vec && m == 8, v[p]);
+        load8(static_cast<const D*>(a.dy) + r * a.ld_dy + c, m, a.vec && m == 8, d[p]);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum[0] = __builtin_fmaf(v[p][i], v[p][i], sum[0]);
+        sum[1] = __builtin_fmaf(d[p][i] * w[p][i], v[p][i], sum[1]);
+      }
+    row_sum<2, THREADS>(sum, tpr, part[odd]);
+    const float inv = rms_inv(sum[0], a.hidden, a.eps);
+    const float along = inv * inv * (sum[1] / (float)a.hidden);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
+      float g[8], add[8] = {};
+      const bool vec = a.vec && m == 8;
+      if (a.dresidual && m > 0) load8(static_cast<const T*>(a.dresidual) + r * a.ld_dresidual + c, m, vec, add);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] = __builtin_fmaf(inv, d[p][i] * w[p][i] - v[p][i] * along, add[i]);
+        dw[p][i] = __builtin_fmaf(d[p][i], live ? v[p][i] * inv : 0.f, dw[p][i]);
+      }
+      if (m > 0) {
+        if constexpr (sizeof(T) == 4) store8(static_cast<float*>(a.dx) + r * a.ld_dx + c, m, vec, g);
+        else moe::store8(static_cast<__bf16*>(a.dx) + r * a.ld_dx + c, m, vec, g);
+      }
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + (long long)blockIdx.x * a.hidden;
+  if (rpw > 1) {   // the rows of the workgroup that ran side by side (P is 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) joined[threadIdx.x * 8 + i] = dw[0][i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.hidden; c += THREADS) {
+      float sum = 0.f;
+      for (int s = 0; s < rpw; ++s) sum += joined[s * tpr * 8 + c];
+      out[c] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * tpr + t) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < a.hidden) out[c + i] = dw[p][i];
+    }
+  }
+}
+
+template <class T, class D>
+__global__ void __launch_bounds__(1024) moe_rms_norm_backward_long_k(const NormArgs a) {
+  __shared__ float part[2][16][2];
+  float* out = a.part ? a.part + (long long)blockIdx.x * a.hidden : nullptr;
+  int odd = 0;
+  bool first = true;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, odd ^= 1) {
+    const T* x = static_cast<const T*>(a.x) + r * a.ld_x;
+    const D* dy = static_cast<const D*>(a.dy) + r * a.ld_dy;
+    float sum[2] = {0.f, 0.f};
+    for (int c = threadIdx.x * 8; c < a.hidden; c += 8192) {
+      const int m = min(8, a.hidden - c);
+      float v[8], d[8], w[8];
+      load8(x + c, m, a.vec && m == 8, v);
+      load8(dy + c, m, a.vec && m == 8, d);
+      load_weight(a, c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum[0] = __builtin_fmaf(v[i], v[i], sum[0]);
+        sum[1] = __builtin_fmaf(d[i] * w[i], v[i], sum[1]);
+      }
+    }
+    row_sum<2, 1024>(sum, 1024, part[odd]);
+    const float inv = rms_inv(sum[0], a.hidden, a.eps);
+    const float along = inv * inv * (sum[1] / (float)a.hidden);
+    for (int c = threadIdx.x * 8; c < a.hidden; c += 8192) {
+      const int m = min(8, a.hidden - c);
+      const bool vec = a.vec && m == 8;
+      float v[8], d[8], w[8], g[8], add[8] = {};
+      load8(x + c, m, vec, v);
+      load8(dy + c, m, vec, d);
+      load_weight(a, c, w);
+      if (a.dresidual) load8(static_cast<const T*>(a.dresidual) + r * a.ld_dresidual + c, m, vec, add);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] = __builtin_fmaf(inv, d[i] * w[i] - v[i] * along, add[i]);
+        // this thread's own columns of the part
+        if (out && i < m) out[c + i] = __builtin_fmaf(d[i], v[i] * inv, first ? 0.f : out[c + i]);
+      }
+      if constexpr (sizeof(T) == 4) store8(static_cast<float*>(a.dx) + r * a.ld_dx + c, m, vec, g);
+      else moe::store8(static_cast<__bf16*>(a.dx) + r * a.ld_dx + c, m, vec, g);
+    }
+    first = false;
+  }
+}
+
+// dw(c) = sum over the groups of part(g, c), ascending within 16 slices, then
+// the slices: 64 columns a workgroup, four of them a thread.
+__global__ void __launch_bounds__(256) moe_join_dweight_k(const float* part, float* dweight, int groups, int hidden) {
+  __shared__ float slice[16][64];
+  const int c0 = blockIdx.x * 64 + (threadIdx.x & 15) * 4, s = threadIdx.x >> 4;
+  float sum[4] = {};
+  for (int g = s; g < groups; g += 16)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c0 + i < hidden) sum[i] += part[(long long)g * hidden + c0 + i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) slice[s][(threadIdx.x & 15) * 4 + i] = sum[i];
+  __syncthreads();
+  const int c = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x < 64 && c < hidden) {
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) all += slice[i][threadIdx.x];
+    dweight[c] = all;
+  }
+}
+
+constexpr int kHeld = 32768;   // columns that 1024 threads hold in four pieces
+
+// Threads of a row that they hold in one piece: the least power of two, at least
+// the lanes of a scale block. Rows of several pieces take the whole workgroup.
+int threads_for(int hidden, int most) {
+  int t = 16;
+  while (t < most && t * 8 < hidden) t *= 2;
+  return t;
+}
+
+template <class T, int KIND>
+hipError_t forward(const NormArgs& a, hipStream_t s) {
+  if (a.hidden > kHeld) {
+    moe_rms_norm_long_k<T, KIND><<<(unsigned)std::min<long long>(a.rows, 4 * kCus), 1024, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  auto run = [&](auto pieces, auto threads) {
+    constexpr int P = decltype(pieces)::value, THREADS = decltype(threads)::value;
+    const int tpr = P == 1 ? threads_for(a.hidden, THREADS) : THREADS;
+    const long long need = (a.rows + THREADS / tpr - 1) / (THREADS / tpr);
+    moe_rms_norm_k<T, KIND, P, THREADS><<<(unsigned)std::min<long long>(need, 8 * kCus), THREADS, 0, s>>>(a, tpr);
+    return hipGetLastError();
+  };
+  using std::integral_constant;
+  constexpr integral_constant<int, 256> narrow{};
+  constexpr integral_constant<int, 1024> wide{};
+  if (a.hidden <= 2048) return run(integral_constant<int, 1>{}, narrow);
+  if (a.hidden <= 4096) return run(integral_constant<int, 2>{}, narrow);
+  if (a.hidden <= 8192) return run(integral_constant<int, 4>{}, narrow);
+  return run(integral_constant<int, 4>{}, wide);
+}
+
+template <class T>
+hipError_t forward_kind(const NormArgs& a, hipStream_t s) {
+  switch (a.format) {
+    case MOE_NORM_BF16:
+    case MOE_NORM_FP32: return forward<T, kPlain>(a, s);
+    case MOE_NORM_FP8: return forward<T, kFp8>(a, s);
+  }
+  return forward<T, kMx>(a, s);
+}
+
+template <class T, class D>
+hipError_t backward(const NormArgs& a, hipStream_t s) {
+  const int groups = norm_backward_groups(a.rows, a.hidden);
+  if (a.hidden > kHeld) {
+    moe_rms_norm_backward_long_k<T, D><<<groups, 1024, 0, s>>>(a);
+  } else {
+    auto run = [&](auto pieces, auto threads) {
+      constexpr int P = decltype(pieces)::value, THREADS = decltype(threads)::value;
+      moe_rms_norm_backward_k<T, D, P, THREADS><<<groups, THREADS, 0, s>>>(a, P == 1 ? threads_for(a.hidden, THREADS) : THREADS);
+    };
+    using std::integral_constant;
+    if (a.hidden <= 2048) run(integral_constant<int, 1>{}, integral_constant<int, 256>{});
+    else if (a.hidden <= 4096) run(integral_constant<int, 2>{}, integral_constant<int, 256>{});
+    else if (a.hidden <= 8192) run(integral_constant<int, 4>{}, integral_constant<int, 256>{});
+    else run(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
+  }
+  if (a.part && a.part != a.dweight) moe_join_dweight_k<<<(a.hidden + 63) / 64, 256, 0, s>>>(a.part, a.dweight, groups, a.hidden);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int norm_backward_groups(long long rows, int hidden) {
+  const int rpw = hidden <= 2048 ? 256 / threads_for(hidden, 256) : 1;
+  return (int)std::min<long long>((rows + rpw - 1) / rpw, 2 * kCus);
+}
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+  return a.fp32 ? forward_kind<float>(a, s) : forward_kind<__bf16>(a, s);
+}
+
+hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s) {
+  if (a.fp32) return a.format == MOE_NORM_FP32 ? backward<float, float>(a, s) : backward<float, __bf16>(a, s);
+  return a.format == MOE_NORM_FP32 ? backward<__bf16, float>(a, s) : backward<__bf16, __bf16>(a, s);
+}
+
+}  // namespace moe

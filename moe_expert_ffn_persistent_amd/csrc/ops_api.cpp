@@ -254,9 +254,193 @@ int32_t fp8(const moe_fp8_params* p, const int32_t* row_offset, const void* x, c
              stream, launch_gemm_fp8);
 }
 
+bool mx_ok(const moe_mx_params* p) {
+  if (!p || p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS || p->rows < 0 || p->rows > kMaxRows ||
+      p->expected_rows < 0 || p->n < 1 || p->n > kMaxCols || p->k < 1 || p->k > kMaxCols ||
+      (p->x_format != MOE_MX_E4M3 && p->x_format != MOE_MX_E2M1) || !dtype_ok(p->out_dtype) || p->tile < 0 ||
+      !split_ok(p->splits, p->workspace_bytes))
+    return false;
+  const long long wb = (p->k + 1) / 2, kb = (p->k + 31) / 32;
+  return (p->x_format == MOE_MX_E4M3 || p->k % 2 == 0) && stride_ok(p->ld_x, p->x_format == MOE_MX_E2M1 ? wb : p->k) &&
+         stride_ok(p->ld_x_scales, kb) && stride_ok(p->ld_w, wb) && stride_ok(p->ld_w_scales, kb) && stride_ok(p->ld_y, p->n) &&
+         matrix_stride_ok(p->expert_stride_w, p->num_experts, p->n, p->ld_w, wb) &&
+         matrix_stride_ok(p->expert_stride_w_scales, p->num_experts, p->n, p->ld_w_scales, kb);
+}
+
+GemmArgs mx_args(const moe_mx_params* p) {
+  GemmArgs a{};
+  a.ld_x = p->ld_x;
+  a.ld_w = p->ld_w;
+  a.ld_y = p->ld_y;
+  a.es_w = p->expert_stride_w;
+  a.ld_xs = p->ld_x_scales;
+  a.ld_ws = p->ld_w_scales;
+  a.es_ws = p->expert_stride_w_scales;
+  a.op = MOE_GROUPED_FORWARD;
+  a.L = p->num_experts;
+  a.rows = (int)p->rows;
+  a.n = p->n;
+  a.k = p->k;
+  a.out_bf16 = p->out_dtype == MOE_Y_BF16;
+  a.x_e2m1 = p->x_format == MOE_MX_E2M1;
+  a.expected = expected_rows(p->expected_rows, p->rows);
+  a.splits = 1;
+  return a;
+}
+
+bool norm_ok(const moe_norm_params* p, bool backward) {
+  if (!p || p->rows < 0 || p->rows > kMaxRows || p->hidden < 1 || p->hidden > kMaxCols || !dtype_ok(p->stream_dtype) ||
+      !dtype_ok(p->weight_dtype) || p->format < MOE_NORM_BF16 || p->format > (backward ? MOE_NORM_FP32 : MOE_NORM_MX_E2M1) ||
+      !(p->eps > 0) || !std::isfinite(p->eps) || !stride_ok(p->ld_x, p->hidden))
+    return false;
+  if (backward) return stride_ok(p->ld_dy, p->hidden) && stride_ok(p->ld_dx, p->hidden) && p->workspace_bytes >= 0;
+  return stride_ok(p->ld_out, p->format == MOE_NORM_MX_E2M1 ? (p->hidden + 1) / 2 : p->hidden);
+}
+
+size_t elem(int32_t dtype) { return dtype == MOE_Y_BF16 ? 2 : 4; }
+
 }  // namespace
 
 extern "C" {
+
+int32_t moe_rms_norm(const moe_norm_params* p, const void* x, const void* residual, const void* weight, void* out,
+                     void* scales, void* residual_out, void* stream) {
+  if (!norm_ok(p, false) || !residual != !residual_out) return MOE_ERR_INVALID_ARG;
+  const bool fp8 = p->format == MOE_NORM_FP8, e2m1 = p->format == MOE_NORM_MX_E2M1, mx = e2m1 || p->format == MOE_NORM_MX_E4M3;
+  if ((residual && (!stride_ok(p->ld_residual, p->hidden) || !stride_ok(p->ld_residual_out, p->hidden))) ||
+      (fp8 && !stride_ok(p->ld_scales, (p->hidden + 127) / 128)) || (mx && !stride_ok(p->ld_scales, (p->hidden + 31) / 32)))
+    return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  const size_t se = elem(p->stream_dtype), we = elem(p->weight_dtype);
+  const size_t oe = p->format == MOE_NORM_BF16 ? 2 : p->format == MOE_NORM_FP32 ? 4 : 1;
+  if (!x || !out || ((fp8 || mx) && !scales) || !aligned(x, se) || !aligned(residual, se) || !aligned(residual_out, se) ||
+      !aligned(weight, we) || !aligned(out, oe) || (fp8 && !aligned(scales, 4)))
+    return MOE_ERR_INVALID_ARG;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.out = out;
+  a.scales = scales;
+  a.stream = residual_out;
+  a.rows = p->rows;
+  a.ld_x = p->ld_x;
+  a.ld_residual = residual ? p->ld_residual : 0;
+  a.ld_stream = residual ? p->ld_residual_out : 0;
+  a.ld_out = p->ld_out;
+  a.ld_scales = p->ld_scales;
+  a.hidden = p->hidden;
+  a.format = p->format;
+  a.eps = p->eps;
+  a.fp32 = p->stream_dtype == MOE_Y_FP32;
+  a.weight_fp32 = p->weight_dtype == MOE_Y_FP32;
+  // eight columns: 16 bytes of a row, or 8 and 4 bytes of codes
+  const long long piece = oe == 1 ? (e2m1 ? 4 : 8) : 16;
+  a.vec = aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) && aligned(weight, 16) && aligned(out, piece) &&
+          a.ld_x * se % 16 == 0 && a.ld_residual * se % 16 == 0 && a.ld_stream * se % 16 == 0 && a.ld_out * (long long)oe % piece == 0;
+  return done(launch_rms_norm(a, (hipStream_t)stream));
+}
+
+int64_t moe_rms_norm_workspace_bytes(const moe_norm_params* p) {
+  if (!norm_ok(p, true) || !p->weight_gradient || p->rows == 0) return 0;
+  const int groups = norm_backward_groups(p->rows, p->hidden);
+  return groups > 1 ? (int64_t)groups * p->hidden * 4 : 0;
+}
+
+int32_t moe_rms_norm_backward(const moe_norm_params* p, const void* dy, const void* x, const void* weight,
+                              const void* dresidual, void* dx, float* dweight, void* workspace, void* stream) {
+  if (!norm_ok(p, true) || (dresidual && !stride_ok(p->ld_dresidual, p->hidden)) || !p->weight_gradient != !dweight)
+    return MOE_ERR_INVALID_ARG;
+  const size_t se = elem(p->stream_dtype), de = p->format == MOE_NORM_BF16 ? 2 : 4;
+  if (!words(dweight) || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return dweight ? done(launch_zero(dweight, (size_t)p->hidden * 4, (hipStream_t)stream)) : MOE_OK;
+  if (!dy || !x || !dx || !aligned(dy, de) || !aligned(x, se) || !aligned(dresidual, se) || !aligned(dx, se) ||
+      !aligned(weight, elem(p->weight_dtype)))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t need = moe_rms_norm_workspace_bytes(p);
+  if (need && (!workspace || p->workspace_bytes < need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  NormArgs a{};
+  a.x = x;
+  a.dy = dy;
+  a.weight = weight;
+  a.dresidual = dresidual;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.part = need ? static_cast<float*>(workspace) : dweight;
+  a.rows = p->rows;
+  a.ld_x = p->ld_x;
+  a.ld_dy = p->ld_dy;
+  a.ld_dresidual = dresidual ? p->ld_dresidual : 0;
+  a.ld_dx = p->ld_dx;
+  a.hidden = p->hidden;
+  a.format = p->format;
+  a.eps = p->eps;
+  a.fp32 = p->stream_dtype == MOE_Y_FP32;
+  a.weight_fp32 = p->weight_dtype == MOE_Y_FP32;
+  a.vec = aligned(x, 16) && aligned(dy, 16) && aligned(dresidual, 16) && aligned(dx, 16) && aligned(weight, 16) &&
+          a.ld_x * se % 16 == 0 && a.ld_dy * de % 16 == 0 && a.ld_dresidual * se % 16 == 0 && a.ld_dx * se % 16 == 0;
+  return done(launch_rms_norm_backward(a, (hipStream_t)stream));
+}
+
+int32_t moe_quantize_mx(const moe_mx_quantize_params* p, const void* x, const int32_t* row_offset, void* codes,
+                        void* scales, void* stream) {
+  if (!p || p->rows < 0 || p->rows > kMaxRows || p->batch < 1 || p->batch > 65535 || p->cols < 1 || p->cols > kMaxCols ||
+      (p->format != MOE_MX_E4M3 && p->format != MOE_MX_E2M1) || !dtype_ok(p->in_dtype))
+    return MOE_ERR_INVALID_ARG;
+  const bool e2m1 = p->format == MOE_MX_E2M1;
+  const long long bytes = e2m1 ? (p->cols + 1) / 2 : p->cols, kb = (p->cols + 31) / 32;
+  if (!stride_ok(p->ld_x, p->cols) || !stride_ok(p->ld_codes, bytes) || !stride_ok(p->ld_scales, kb) ||
+      (row_offset && (p->batch != 1 || p->num_experts < 1 || p->num_experts > MOE_MAX_LOCAL_EXPERTS)))
+    return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!matrix_stride_ok(p->batch_stride_x, p->batch, p->rows, p->ld_x, p->cols) ||
+      !matrix_stride_ok(p->batch_stride_codes, p->batch, p->rows, p->ld_codes, bytes) ||
+      !matrix_stride_ok(p->batch_stride_scales, p->batch, p->rows, p->ld_scales, kb))
+    return MOE_ERR_INVALID_ARG;
+  const size_t xe = elem(p->in_dtype);
+  if (!x || !codes || !scales || !aligned(x, xe) || !words(row_offset)) return MOE_ERR_INVALID_ARG;
+  MxQuantArgs a{};
+  a.x = x;
+  a.row_offset = row_offset;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = static_cast<uint8_t*>(scales);
+  a.rows = p->rows;
+  a.ld_x = p->ld_x;
+  a.ld_codes = p->ld_codes;
+  a.ld_scales = p->ld_scales;
+  a.bs_x = p->batch > 1 ? p->batch_stride_x : 0;
+  a.bs_codes = p->batch > 1 ? p->batch_stride_codes : 0;
+  a.bs_scales = p->batch > 1 ? p->batch_stride_scales : 0;
+  a.batch = p->batch;
+  a.cols = p->cols;
+  a.L = p->num_experts;
+  // a lane's store: 16 columns of bf16, 8 of fp32
+  const long long piece = (xe == 2 ? 16 : 8) / (e2m1 ? 2 : 1);
+  a.vec = aligned(x, 16) && a.ld_x * xe % 16 == 0 && a.bs_x * xe % 16 == 0 && aligned(codes, piece) && a.ld_codes % piece == 0 &&
+          a.bs_codes % piece == 0;
+  return done(launch_quantize_mx(a, e2m1, xe == 4, (hipStream_t)stream));
+}
+
+int64_t moe_mx_workspace_bytes(const moe_mx_params* p) {
+  return 0;
+}
+
+int32_t moe_mx_matmul(const moe_mx_params* p, const int32_t* row_offset, const void* x, const void* x_scales, const void* w,
+                      const void* w_scales, void* y, void* workspace, void* stream) {
+  if (!mx_ok(p) || (!row_offset && p->num_experts != 1)) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!x || !x_scales || !w || !w_scales || !y || !aligned(y, elem(p->out_dtype)) || !aligned(workspace, 16) || !words(row_offset))
+    return MOE_ERR_INVALID_ARG;
+  GemmArgs a = mx_args(p);
+  a.row_offset = row_offset;
+  a.x = const_cast<void*>(x);
+  a.w = const_cast<void*>(w);
+  a.y = y;
+  a.xs = static_cast<const float*>(x_scales);
+  a.ws = static_cast<const float*>(w_scales);
+  if (p->tile > 0) return MOE_ERR_UNSUPPORTED;
+  return done(launch_gemm_mx_any(a, (hipStream_t)stream));
+}
 
 int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t* row_pair,
                           const int32_t* row_offset, void* out, void* stream) {
@@ -284,13 +468,14 @@ int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t
   return done(launch_dispatch_rows(a, (hipStream_t)stream));
 }
 
-int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row, void* y, void* stream) {
+static int32_t combine(const moe_rows_params* p, const void* in, const int32_t* pair_row, const float* weights, void* y,
+                       void* stream) {
   if (!p || p->tokens < 0 || p->rows < 0 || p->rows > kMaxRows || p->top_k < 1 || p->top_k > 16 || p->hidden < 1 ||
       p->hidden > kMaxCols || p->elem_bytes != 2 || !dtype_ok(p->out_dtype) || !stride_ok(p->ld_tokens, p->hidden) ||
       !stride_ok(p->ld_rows, p->hidden) || p->tokens > kMaxCombineTokens)
     return MOE_ERR_INVALID_ARG;
   if (p->tokens == 0) return MOE_OK;
-  if (!pair_row || !y || (p->rows && !in) || !words(pair_row)) return MOE_ERR_INVALID_ARG;
+  if (!pair_row || !y || (p->rows && !in) || !words(pair_row, weights)) return MOE_ERR_INVALID_ARG;
   const size_t out_elem = p->out_dtype == MOE_Y_BF16 ? 2 : 4;
   if (!aligned(in, 2) || !aligned(y, out_elem)) return MOE_ERR_INVALID_ARG;
   RowsArgs a{};
@@ -304,7 +489,47 @@ int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t
   a.k = p->top_k;
   a.hidden = p->hidden;
   a.elem = 2;
-  return done(launch_combine_rows(a, p->out_dtype == MOE_Y_BF16, (hipStream_t)stream));
+  return done(launch_combine_rows(a, weights, p->out_dtype == MOE_Y_BF16, (hipStream_t)stream));
+}
+
+int32_t moe_combine_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row, void* y, void* stream) {
+  return combine(p, in, pair_row, nullptr, y, stream);
+}
+
+int32_t moe_combine_weighted_rows(const moe_rows_params* p, const void* in, const int32_t* pair_row, const float* weights,
+                                  void* y, void* stream) {
+  if (p && p->tokens > 0 && !weights) return MOE_ERR_INVALID_ARG;
+  return combine(p, in, pair_row, weights, y, stream);
+}
+
+int32_t moe_combine_rows_backward(const moe_combine_backward_params* p, const void* dy, const void* in, const int32_t* pair_row,
+                                  const float* weights, void* din, float* dweights, void* stream) {
+  if (!p || p->tokens < 0 || p->tokens > kMaxCombineTokens || p->rows < 0 || p->rows > kMaxRows || p->top_k < 1 || p->top_k > 16 ||
+      p->hidden < 1 || p->hidden > kMaxCols || !dtype_ok(p->dy_dtype) || !stride_ok(p->ld_dy, p->hidden) ||
+      !stride_ok(p->ld_rows, p->hidden) || !stride_ok(p->ld_drows, p->hidden))
+    return MOE_ERR_INVALID_ARG;
+  if (p->tokens == 0) return MOE_OK;
+  const size_t de = elem(p->dy_dtype);
+  if (!dy || !pair_row || !weights || !dweights || (p->rows && (!in || !din)) || !words(pair_row, weights, dweights) ||
+      !aligned(dy, de) || !aligned(in, 2) || !aligned(din, 2))
+    return MOE_ERR_INVALID_ARG;
+  CombineBackwardArgs a{};
+  a.dy = dy;
+  a.rows = in;
+  a.pair_row = pair_row;
+  a.weights = weights;
+  a.drows = din;
+  a.dweights = dweights;
+  a.cap = p->rows;
+  a.ld_dy = p->ld_dy;
+  a.ld_rows = p->ld_rows;
+  a.ld_drows = p->ld_drows;
+  a.tokens = (int)p->tokens;
+  a.k = p->top_k;
+  a.hidden = p->hidden;
+  a.dy_fp32 = p->dy_dtype == MOE_Y_FP32;
+  a.vec = aligned(dy, 16) && aligned(in, 16) && aligned(din, 16) && a.ld_dy * de % 16 == 0 && a.ld_rows % 8 == 0 && a.ld_drows % 8 == 0;
+  return done(launch_combine_backward(a, (hipStream_t)stream));
 }
 
 int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w, void* y,

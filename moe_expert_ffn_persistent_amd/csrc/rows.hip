@@ -1,6 +1,6 @@
 // Rows of the local experts gathered from the tokens (dispatch) and each
 // token's rows summed (combine): each other's gradients, both one pass over
-// the bytes.
+// the bytes; and the gradients of the sum with a weight for each row.
 #include <type_traits>
 
 #include "internal.hpp"
@@ -38,18 +38,21 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_k(const RowsArgs a) {
   }
 }
 
-// y[n] = sum of the token's rows, ascending slots, fp32. TPT threads take a
+// y[n] = sum of the token's rows, ascending slots, fp32; WEIGHTED: each times its
+// pair's weight, one fused multiply-add. TPT threads take a
 // token. A wavefront finds the slots that are local with one load and a ballot,
 // so slots of other GPUs cost nothing, and a lane has eight columns of up to U
 // pieces of the row in flight, of the next slot before this one's are added: 160
 // us with one piece and one slot at a time, 90 us so (16384 tokens x 7168, 8
 // slots of which one in the mean is local: 470 MB).
-template <bool BF16, int TPT, int U>
-__global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool vec, int tokens) {
+template <bool BF16, int TPT, int U, bool WEIGHTED>
+__global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, const float* weights, bool vec, int tokens) {
   const int n = blockIdx.x * (256 / TPT) + uni((int)threadIdx.x / TPT), lane = threadIdx.x & 63;
   if (n >= tokens) return;
   const int idx = lane < a.k ? a.index[(size_t)n * a.k + lane] : -1;
   const uint64_t local = __ballot(idx >= 0 && idx < a.rows);
+  float weight = 1.f;
+  if constexpr (WEIGHTED) weight = lane < a.k ? weights[(size_t)n * a.k + lane] : 0.f;
   char* yrow = static_cast<char*>(a.out) + (size_t)n * a.ld_out;
   for (int c0 = threadIdx.x % TPT * 8; c0 < a.hidden; c0 += U * TPT * 8) {
     auto load = [&](int slot, uint4 (&v)[U]) {
@@ -73,6 +76,8 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool
     uint4 v[2][U];
     if (left) load(__builtin_ctzll(left), v[0]);
     while (left) {
+      float w = 1.f;
+      if constexpr (WEIGHTED) w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), __builtin_ctzll(left)));
       left &= left - 1;
       if (left) load(__builtin_ctzll(left), v[1]);
 #pragma unroll
@@ -81,7 +86,7 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool
         float x[8];
         unpack8(v[0][u], x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[u][i] += x[i];
+        for (int i = 0; i < 8; ++i) s[u][i] = WEIGHTED ? __builtin_fmaf(w, x[i], s[u][i]) : s[u][i] + x[i];
         v[0][u] = v[1][u];
       }
     }
@@ -107,6 +112,82 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, bool
   }
 }
 
+// Gradients of the weighted sum y[n] = sum over j of w[n, j] rows[p(n, j)]:
+//   drows[p(n, j)] = w[n, j] dy[n],  dw[n, j] = dy[n] . rows[p(n, j)]
+// (0 where the slot is not local). TPT threads take a token: its dy is read
+// once and held while its local rows pass (rows longer than U pieces of the
+// threads read the rest of it again, from the caches), and a slot's dot product
+// is joined over the lanes and, through LDS, over the wavefronts, in an order
+// that sizes settle.
+template <class D, int TPT, int U>
+__global__ void __launch_bounds__(256) moe_combine_backward_k(const CombineBackwardArgs a) {
+  __shared__ float part[4][16];
+  const int sub = uni((int)threadIdx.x / TPT), n = blockIdx.x * (256 / TPT) + sub, lane = threadIdx.x & 63;
+  const bool live = n < a.tokens;
+  const int idx = live && lane < a.k ? a.pair_row[(size_t)n * a.k + lane] : -1;
+  const float weight = live && lane < a.k ? a.weights[(size_t)n * a.k + lane] : 0.f;
+  const uint64_t local = __ballot(idx >= 0 && idx < a.cap);
+  float mine = 0.f;   // lane j: slot j's dot product, of this wavefront's columns
+  if (local) {
+    const D* dy = static_cast<const D*>(a.dy) + (size_t)n * a.ld_dy;
+    const int t0 = threadIdx.x % TPT * 8;
+    float d[U][8];
+    auto load_dy = [&](int c0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[u][i] = 0.f;
+        if (m > 0) load8(dy + c, m, a.vec && m == 8, d[u]);
+      }
+    };
+    load_dy(t0);
+    for (uint64_t left = local; left; left &= left - 1) {
+      const int slot = __builtin_ctzll(left);
+      const int r = __builtin_amdgcn_readlane(idx, slot);
+      const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), slot));
+      const __bf16* row = static_cast<const __bf16*>(a.rows) + (size_t)r * a.ld_rows;
+      __bf16* drow = static_cast<__bf16*>(a.drows) + (size_t)r * a.ld_drows;
+      float dot = 0.f;
+      for (int c0 = t0; c0 < a.hidden; c0 += U * TPT * 8) {
+        if (a.hidden > U * TPT * 8) load_dy(c0);
+        float x[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+          if (m > 0) load8(row + c, m, a.vec && m == 8, x[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
+          float g[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot = __builtin_fmaf(d[u][i], x[u][i], dot);
+            g[i] = w * d[u][i];
+          }
+          if (m > 0) store8(drow + c, m, a.vec && m == 8, g);
+        }
+      }
+#pragma unroll
+      for (int s = 1; s < 64; s <<= 1) dot += __shfl_xor(dot, s, 64);
+      if (lane == slot) mine = dot;
+    }
+  }
+  if constexpr (TPT > 64) {
+    if (lane < 16) part[threadIdx.x >> 6][lane] = mine;
+    __syncthreads();
+    mine = 0.f;
+    if (lane < 16) {
+#pragma unroll
+      for (int i = 0; i < TPT / 64; ++i) mine += part[sub * (TPT / 64) + i][lane];
+    }
+  }
+  if (live && threadIdx.x % TPT < a.k) a.dweights[(size_t)n * a.k + lane] = mine;
+}
+
 }  // namespace
 
 hipError_t launch_dispatch_rows(const RowsArgs& a, hipStream_t s) {
@@ -129,14 +210,19 @@ hipError_t launch_dispatch_rows(const RowsArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_combine_rows(const RowsArgs& a, bool bf16_out, hipStream_t s) {
+hipError_t launch_combine_rows(const RowsArgs& a, const float* weights, bool bf16_out, hipStream_t s) {
   const bool vec = (((uintptr_t)a.in | (uintptr_t)a.out | (uintptr_t)a.ld_in | (uintptr_t)a.ld_out) % 16) == 0;
   const int tokens = (int)(a.pairs / a.k);
   auto run = [&](auto tpt, auto pieces) {
     constexpr int T = decltype(tpt)::value, U = decltype(pieces)::value;
     const int grid = (tokens + 256 / T - 1) / (256 / T);
-    if (bf16_out) moe_combine_rows_k<true, T, U><<<grid, 256, 0, s>>>(a, vec, tokens);
-    else moe_combine_rows_k<false, T, U><<<grid, 256, 0, s>>>(a, vec, tokens);
+    if (weights) {
+      if (bf16_out) moe_combine_rows_k<true, T, U, true><<<grid, 256, 0, s>>>(a, weights, vec, tokens);
+      else moe_combine_rows_k<false, T, U, true><<<grid, 256, 0, s>>>(a, weights, vec, tokens);
+    } else {
+      if (bf16_out) moe_combine_rows_k<true, T, U, false><<<grid, 256, 0, s>>>(a, nullptr, vec, tokens);
+      else moe_combine_rows_k<false, T, U, false><<<grid, 256, 0, s>>>(a, nullptr, vec, tokens);
+    }
     return hipGetLastError();
   };
   using std::integral_constant;
@@ -146,6 +232,23 @@ hipError_t launch_combine_rows(const RowsArgs& a, bool bf16_out, hipStream_t s) 
   // of 8 local: 512 columns 11.4 us, a workgroup each 28.4; 1016: 20.6 and 37.8;
   // 2056: 39.9 and 56.2; 4096: 96.5 and 98.6; 7168: 167.5 and 165.3).
   if (tokens > 1024) {
+    if (a.hidden <= 512) return run(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if (a.hidden <= 1024) return run(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    if (a.hidden <= 4096) return run(integral_constant<int, 128>{}, integral_constant<int, 4>{});
+  }
+  return run(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+}
+
+hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t s) {
+  auto run = [&](auto tpt, auto pieces) {
+    constexpr int T = decltype(tpt)::value, U = decltype(pieces)::value;
+    const int grid = (a.tokens + 256 / T - 1) / (256 / T);
+    if (a.dy_fp32) moe_combine_backward_k<float, T, U><<<grid, 256, 0, s>>>(a);
+    else moe_combine_backward_k<__bf16, T, U><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+  };
+  using std::integral_constant;
+  if (a.tokens > 1024) {
     if (a.hidden <= 512) return run(integral_constant<int, 64>{}, integral_constant<int, 1>{});
     if (a.hidden <= 1024) return run(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     if (a.hidden <= 4096) return run(integral_constant<int, 128>{}, integral_constant<int, 4>{});

@@ -1,13 +1,15 @@
 """Operators around the expert FFN (include/moe_ffn.h, "Operators around the
 expert FFN"): rows dispatched to and combined from the local experts, matrix
 products grouped by expert with their gradients, SwiGLU, quantisation to e4m3
-with block scales and the block-scaled e4m3 product.
+with block scales and the block-scaled e4m3 product, RMS norm of the residual
+stream with its gradients, quantisation to the OCP Microscaling (MX) formats and
+their product.
 
 Every call checks its tensors on the host (ValueError before anything is
 enqueued), enqueues one or a few kernels on ``stream`` (a torch.cuda.Stream;
 default: the current stream of the tensors' device) and returns without waiting. With
 ``out`` given nothing is allocated, but for the workspace of a product that cuts
-its sum (see grouped_matmul), and the call may be captured in a HIP graph. ``out`` must not overlap an input unless a function says it may. When a
+its sum (see grouped_matmul) or of rms_norm_backward, and the call may be captured in a HIP graph. ``out`` must not overlap an input unless a function says it may. When a
 call allocates its output, rows that no expert owns hold whatever the memory
 held. Tensors used on a stream other than the one they were allocated on need
 the caller's ``record_stream``, as everywhere in torch.
@@ -22,6 +24,9 @@ when that was saved for a backward pass.
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
+import struct
 import warnings
 
 import torch
@@ -30,12 +35,19 @@ from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._lib import (MOE_GROUPED_DGRAD, MOE_GROUPED_FORWARD, MOE_GROUPED_WGRAD, MOE_MAX_LOCAL_EXPERTS,
-                   MOE_SWIGLU_BF16, MOE_SWIGLU_FP8, MOE_Y_BF16, MOE_Y_FP32, MoeFp8Params,
-                   MoeGroupedParams, MoeQuantizeParams, MoeRowsParams, MoeSwigluParams)
+                   MOE_MX_E2M1, MOE_MX_E4M3, MOE_NORM_BF16, MOE_NORM_FP32, MOE_NORM_FP8, MOE_NORM_MX_E2M1,
+                   MOE_NORM_MX_E4M3, MOE_SWIGLU_BF16, MOE_SWIGLU_FP8, MOE_Y_BF16, MOE_Y_FP32,
+                   MoeCombineBackwardParams, MoeFp8Params, MoeGroupedParams, MoeMxParams, MoeMxQuantizeParams,
+                   MoeNormParams, MoeQuantizeParams, MoeRowsParams, MoeSwigluParams)
 
 BLOCK = 128   # columns of one fp32 scale
+MX_BLOCK = 32   # elements of one E8M0 scale
 _OUT = {torch.bfloat16: MOE_Y_BF16, torch.float32: MOE_Y_FP32}
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_MX = {"e4m3": MOE_MX_E4M3, "e2m1": MOE_MX_E2M1}
+_PAIRS = tuple(t for t in (torch.uint8, getattr(torch, "float4_e2m1fn_x2", None)) if t is not None)   # two e2m1 codes
+_E8M0 = tuple(t for t in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if t is not None)
+_NORM = {None: MOE_NORM_BF16, "fp8": MOE_NORM_FP8, "mx_e4m3": MOE_NORM_MX_E4M3, "mx_e2m1": MOE_NORM_MX_E2M1}
 # the C entry points' limits
 _MAX_ROWS, _MAX_COLS, _MAX_STRIDE, _MAX_MATRIX = 1 << 28, 1 << 20, 1 << 32, 1 << 52
 _MAX_TOKENS = 1 << 23    # of one moe_combine_rows
@@ -197,8 +209,9 @@ def _check_stream(stream, device):
         raise ValueError(f"stream: of device {at}, the tensors are on device {device}")
 
 
-# products that may take a workspace, their last pointer, and what says its size
-_WORKSPACE = {"moe_grouped_matmul_split": "moe_grouped_workspace_bytes", "moe_fp8_matmul_split": "moe_fp8_workspace_bytes"}
+# calls that may take a workspace, their last pointer, and what says its size
+_WORKSPACE = {"moe_grouped_matmul_split": "moe_grouped_workspace_bytes", "moe_fp8_matmul_split": "moe_fp8_workspace_bytes",
+              "moe_mx_matmul": "moe_mx_workspace_bytes", "moe_rms_norm_backward": "moe_rms_norm_workspace_bytes"}
 
 
 def _call(name, check, args, plain, tensors, written, stream):
@@ -309,7 +322,7 @@ class _MoreTokens(Exception):
     """Inputs that are in order but for more tokens than one call takes."""
 
 
-def check_combine_rows_inputs(rows, pair_row, top_k, out):
+def check_combine_rows_inputs(rows, pair_row, top_k, out, weights=None):
     ldr = _matrix(rows, "rows", (torch.bfloat16,))
     _at_most(rows.shape[0], "rows", _MAX_ROWS)
     if not 1 <= top_k <= 16:
@@ -321,29 +334,78 @@ def check_combine_rows_inputs(rows, pair_row, top_k, out):
     ldo = _matrix(out, "out", tuple(_OUT))
     if tuple(out.shape) != (N, rows.shape[1]):
         raise ValueError(f"out: need shape {(N, rows.shape[1])}, got {tuple(out.shape)}")
-    _on(rows.device, ("rows", rows), ("pair_row", pair_row), ("out", out))
+    if weights is not None:
+        _vector(weights, "weights", N * top_k, torch.float32)
+    _on(rows.device, ("rows", rows), ("pair_row", pair_row), ("weights", weights), ("out", out))
     if N > _MAX_TOKENS:
         raise _MoreTokens
     return MoeRowsParams(N, rows.shape[0], top_k, rows.shape[1], 2, 0, _OUT[out.dtype], ldo, ldr)
 
 
-def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stream=None):
+def combine_rows(rows, pair_row, top_k, out=None, out_dtype=torch.bfloat16, stream=None, weights=None):
     """Each token's rows summed in fp32, in ascending slot order: ``out[n] =
     sum of rows[pair_row[n * top_k + j]]`` over the slots whose pair_row is not
-    negative. rows bf16 [R, H]; out [N, H] bf16 (rounded once) or fp32. The
-    gradient of dispatch_rows."""
+    negative, each times ``weights[n, j]`` (fp32 [N, top_k], a layout's topk_w)
+    where they are given. rows bf16 [R, H]; out [N, H] bf16 (rounded once) or
+    fp32. Without weights the gradient of dispatch_rows; with them
+    combine_rows_backward is its gradient."""
     if out is None:
         _, H = _sizes(rows, "rows", 2)
         _indices(pair_row, "pair_row")
         out = _empty((pair_row.numel() // max(1, top_k), H), _out_type(out_dtype), rows.device, stream)
     try:
-        _call("moe_combine_rows", check_combine_rows_inputs, (rows, pair_row, top_k, out), (top_k,), (rows, pair_row, out),
-              0b100, stream)
+        if weights is None:
+            _call("moe_combine_rows", check_combine_rows_inputs, (rows, pair_row, top_k, out), (top_k,), (rows, pair_row, out),
+                  0b100, stream)
+        else:
+            _call("moe_combine_weighted_rows", check_combine_rows_inputs, (rows, pair_row, top_k, out, weights), (top_k,),
+                  (rows, pair_row, weights, out), 0b1000, stream)
     except _MoreTokens:
         pairs = pair_row.view(-1)
         for n in range(0, out.shape[0], _MAX_TOKENS):
-            combine_rows(rows, pairs[n * top_k:(n + _MAX_TOKENS) * top_k], top_k, out=out[n:n + _MAX_TOKENS], stream=stream)
+            some = slice(n * top_k, (n + _MAX_TOKENS) * top_k)
+            combine_rows(rows, pairs[some], top_k, out=out[n:n + _MAX_TOKENS], stream=stream,
+                         weights=None if weights is None else weights.view(-1)[some])
     return out
+
+
+def check_combine_backward_inputs(dy, rows, pair_row, weights, drows, dweights):
+    ldy = _matrix(dy, "dy", tuple(_OUT))
+    ldr = _matrix(rows, "rows", (torch.bfloat16,))
+    ldd = _matrix(drows, "out", (torch.bfloat16,))
+    N, H = dy.shape
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 2 or weights.shape[0] != N:
+        raise ValueError(f"weights: need a tensor [{N}, top_k]")
+    k = weights.shape[1]
+    if not 1 <= k <= 16:
+        raise ValueError(f"weights: {k} slots a token, need 1 to 16")
+    _vector(weights, "weights", N * k, torch.float32)
+    _vector(dweights, "dweights", N * k, torch.float32)
+    if tuple(dweights.shape) != (N, k):
+        raise ValueError(f"dweights: need shape {(N, k)}, got {tuple(dweights.shape)}")
+    _vector(pair_row, "pair_row", N * k, torch.int32)
+    if rows.shape[1] != H or drows.shape != rows.shape:
+        raise ValueError(f"shapes do not fit: dy {tuple(dy.shape)}, rows {tuple(rows.shape)}, out {tuple(drows.shape)}")
+    _at_most(rows.shape[0], "rows", _MAX_ROWS)
+    _at_most(N, "tokens", _MAX_TOKENS)
+    _on(dy.device, ("dy", dy), ("rows", rows), ("pair_row", pair_row), ("weights", weights), ("out", drows), ("dweights", dweights))
+    return MoeCombineBackwardParams(N, rows.shape[0], k, H, _OUT[dy.dtype], ldy, ldr, ldd)
+
+
+def combine_rows_backward(dy, rows, pair_row, weights, out=None, dweights=None, stream=None):
+    """Gradients of combine_rows with weights for dy [N, H] (bf16 or fp32):
+    (drows bf16 [R, H], dweights fp32 [N, top_k]), ``drows[pair_row[n, j]] =
+    weights[n, j] * dy[n]`` and ``dweights[n, j] = dy[n] . rows[pair_row[n, j]]``,
+    0 for slots whose pair_row is negative (or no row). Rows that no slot names
+    keep what ``out`` held. Each row belongs to one slot, as in a layout. ``out``
+    may be rows itself. At most 2^23 tokens."""
+    if out is None:
+        out = _empty(_sizes(rows, "rows", 2), torch.bfloat16, rows.device, stream)
+    if dweights is None:
+        dweights = _empty(_sizes(weights, "weights", 2), torch.float32, weights.device, stream)
+    _call("moe_combine_rows_backward", check_combine_backward_inputs, (dy, rows, pair_row, weights, out, dweights), (),
+          (dy, rows, pair_row, weights, out, dweights), 0b110000, stream)
+    return out, dweights
 
 
 # ---- matrix products grouped by expert ---------------------------------------
@@ -628,3 +690,280 @@ def fp8_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=to
           (x, x_scales, w, w_scales, row_offset, out, expected_rows, tile, splits), (expected_rows, tile, splits),
           (row_offset, x, x_scales, w, w_scales, out, None), 0b100000, stream)
     return out
+
+
+# ---- microscaled (MX) formats ------------------------------------------------------
+
+def _mx_blocks(n: int) -> int:
+    return -(-n // MX_BLOCK)
+
+
+def _element(element):
+    if element not in _MX:
+        raise ValueError(f"element: need 'e4m3' or 'e2m1', got {element!r}")
+    return _MX[element]
+
+
+def _rows_apart(shape, dtype, step, device, stream):
+    """An output whose rows start a multiple of ``step`` elements apart."""
+    wide = -(-shape[-1] // step) * step
+    return _empty((*shape[:-1], wide), dtype, device, stream)[..., :shape[-1]]
+
+
+def _empty_mx(shape, element, device, stream):
+    """(codes, scales) for elements of ``shape``, as the tile kernels take them."""
+    if element == MOE_MX_E4M3:
+        codes = _rows_apart(shape, torch.float8_e4m3fn, 16, device, stream)
+    else:
+        codes = _rows_apart((*shape[:-1], -(-shape[-1] // 2)), torch.uint8, 16, device, stream)
+    return codes, _rows_apart((*shape[:-1], _mx_blocks(shape[-1])), torch.uint8, 4, device, stream)
+
+
+def _mx_codes(t, what, element, shape):
+    """Codes of elements of ``shape``; returns the row stride in bytes."""
+    ld = _matrix(t, what, _CODES if element == MOE_MX_E4M3 else _PAIRS, len(shape))
+    want = tuple(shape) if element == MOE_MX_E4M3 else tuple(shape[:-1]) + (-(-shape[-1] // 2),)
+    if tuple(t.shape) != want:
+        raise ValueError(f"{what}: need shape {want}, got {tuple(t.shape)}")
+    return ld
+
+
+def _mx_scales(t, what, shape):
+    """Scale bytes of elements of ``shape``; returns the row stride."""
+    ld = _matrix(t, what, _E8M0, len(shape))
+    want = tuple(shape[:-1]) + (_mx_blocks(shape[-1]),)
+    if tuple(t.shape) != want:
+        raise ValueError(f"{what}: need shape {want}, got {tuple(t.shape)}")
+    return ld
+
+
+def check_quantize_mx_inputs(x, element, row_offset, codes, scales):
+    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+        raise ValueError("x: need a matrix or a batch of matrices")
+    ldx = _matrix(x, "x", tuple(_OUT), x.dim())
+    _at_most(x.shape[-2], "rows", _MAX_ROWS)
+    _at_most(x.shape[0] if x.dim() == 3 else 1, "matrices", _MAX_BATCH)
+    ldc = _mx_codes(codes, "out", element, x.shape)
+    lds = _mx_scales(scales, "scales", x.shape)
+    L = 1
+    if row_offset is not None:
+        if x.dim() != 2:
+            raise ValueError("row_offset goes with a matrix")
+        L = _offsets(row_offset)
+    _on(x.device, ("x", x), ("row_offset", row_offset), ("out", codes), ("scales", scales))
+    batch, bs = 1, (0, 0, 0)
+    if x.dim() == 3:
+        batch, bs = x.shape[0], (_batch_stride(x, "x", ldx), _batch_stride(codes, "out", ldc), _batch_stride(scales, "scales", lds))
+    return MoeMxQuantizeParams(x.shape[-2], batch, x.shape[-1], element, _OUT[x.dtype], L, ldx, ldc, lds, *bs)
+
+
+def quantize_mx(x, element="e4m3", row_offset=None, out=None, scales=None, stream=None):
+    """x (bf16 or fp32, [rows, cols] or [batch, rows, cols]) in an OCP Microscaling
+    format, the W4A8 kernels' operands: (codes, scales). Blocks of 32 elements of a
+    row share a power of two, floor(log2(amax)) less the element's largest
+    exponent (8 for "e4m3", 2 for "e2m1"), and codes are the values nearest to x
+    over it, ties to even, at most the largest. codes: "e4m3" float8_e4m3fn (or
+    uint8) [..., cols]; "e2m1" uint8 (or float4_e2m1fn_x2) [..., ceil(cols/2)], two a
+    byte, the first in the low bits. scales: E8M0 bytes, uint8 (or float8_e8m0fnu)
+    [..., ceil(cols/32)]. Both have contiguous rows, allocated 16 (scales: 4) bytes
+    or multiples of that apart. With ``row_offset`` only the experts' rows."""
+    element = _element(element)
+    if out is None or scales is None:
+        if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+            raise ValueError("x: need a matrix or a batch of matrices")
+        _need_device(x.device)
+        c, s = _empty_mx(x.shape, element, x.device, stream)
+        out, scales = c if out is None else out, s if scales is None else scales
+    args = x, element, row_offset, out, scales
+    if isinstance(x, torch.Tensor) and x.numel() == 0:
+        check_quantize_mx_inputs(*args)
+    else:
+        _call("moe_quantize_mx", check_quantize_mx_inputs, args, (element,), (x, row_offset, out, scales), 0b1100, stream)
+    return out, scales
+
+
+def check_mx_inputs(x, x_scales, w, w_scales, row_offset, y, expected_rows=None, tile=0, splits=0):
+    """The type of x says its format: float8_e4m3fn is e4m3, uint8 (or
+    float4_e2m1fn_x2) two e2m1 codes a byte."""
+    ldx = _matrix(x, "x", (torch.float8_e4m3fn,) + _PAIRS)
+    grouped = row_offset is not None
+    ldw = _matrix(w, "w", _PAIRS, 3 if grouped else 2)
+    element = MOE_MX_E4M3 if x.dtype == torch.float8_e4m3fn else MOE_MX_E2M1
+    ldy = _matrix(y, "out", tuple(_OUT))
+    rows, n = x.shape[0], w.shape[-2]
+    k = x.shape[1] if element == MOE_MX_E4M3 else 2 * x.shape[1]
+    if n < 1:
+        raise ValueError("w: no output features")
+    _at_most(rows, "rows", _MAX_ROWS)
+    _at_most(n, "output features", _MAX_COLS)
+    _at_most(k, "elements of a row", _MAX_COLS)
+    _choice(tile, splits)
+    if w.shape[-1] != -(-k // 2) or tuple(y.shape) != (rows, n):
+        raise ValueError(f"shapes do not fit: x {tuple(x.shape)} ({k} elements), w {tuple(w.shape)} (two elements a byte), "
+                         f"out {tuple(y.shape)}")
+    ldxs = _mx_scales(x_scales, "x_scales", (rows, k))
+    ldws = _mx_scales(w_scales, "w_scales", tuple(w.shape[:-1]) + (k,))
+    L, es, ess = 1, 0, 0
+    if grouped:
+        L = _offsets(row_offset)
+        if w.shape[0] != L:
+            raise ValueError(f"row_offset: {L} experts, the weights have {w.shape[0]}")
+        es, ess = _batch_stride(w, "w", ldw), _batch_stride(w_scales, "w_scales", ldws)
+    _on(x.device, ("x", x), ("x_scales", x_scales), ("w", w), ("w_scales", w_scales), ("row_offset", row_offset), ("out", y))
+    return MoeMxParams(L, rows, _expected(expected_rows), n, k, ldx, ldxs, ldw, ldws, ldy, es, ess, element,
+                       _OUT[y.dtype], tile, splits)
+
+
+def mx_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=torch.bfloat16, expected_rows=None,
+              tile=0, splits=0, stream=None):
+    """``out = (x * x_scales) @ (w * w_scales).T`` of MX operands (quantize_mx): x
+    float8_e4m3fn [rows, k] or two e2m1 codes a byte, uint8 [rows, k/2], scales
+    [rows, ceil(k/32)]; w e2m1, uint8 [n, ceil(k/2)], scales [n, ceil(k/32)]; grouped
+    by expert with ``row_offset``: w [L, n, ...], w_scales [L, n, ...], every row
+    times its expert's matrix. out [rows, n] bf16 or fp32. ``expected_rows``,
+    ``tile`` and ``splits`` as for grouped_matmul.
+
+    Scales are the matrix cores' own and exact; sums are fp32 but for the bits that
+    the matrix cores drop (see fp8_matmul). Operands off their 16 bytes (scales off
+    four), or with such strides, take a slower kernel; what quantize_mx allocates
+    is on them for any k."""
+    if out is None:
+        rows, _ = _sizes(x, "x", 2)
+        n = _sizes(w, "w", 2 if row_offset is None else 3)[-2]
+        out = _empty((rows, n), _out_type(out_dtype), x.device, stream)
+    _call("moe_mx_matmul", check_mx_inputs,
+          (x, x_scales, w, w_scales, row_offset, out, expected_rows, tile, splits), (expected_rows, tile, splits),
+          (row_offset, x, x_scales, w, w_scales, out, None), 0b100000, stream)
+    return out
+
+
+# ---- RMS norm of the residual stream -------------------------------------------------
+
+@functools.lru_cache(maxsize=64)
+def _bits(eps):
+    """The fp32 bits of eps, by which a call is remembered."""
+    if not isinstance(eps, (int, float)) or not 0.0 < ctypes.c_float(eps).value < math.inf:
+        raise ValueError(f"eps: need a positive number, got {eps!r}")
+    return struct.unpack("<i", struct.pack("<f", eps))[0]
+
+
+def _eps(bits):
+    return struct.unpack("<f", struct.pack("<i", bits))[0]
+
+
+def _norm_weight(weight, hidden):
+    if weight is None:
+        return MOE_Y_FP32
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in _OUT or not weight.is_contiguous() or tuple(weight.shape) != (hidden,):
+        raise ValueError(f"weight: need a contiguous bfloat16 or float32 tensor of {hidden} elements")
+    return _OUT[weight.dtype]
+
+
+def check_rms_norm_inputs(x, weight, residual, eps, quantize, out, scales, residual_out):
+    ldx = _matrix(x, "x", tuple(_OUT))
+    rows, H = x.shape
+    _at_most(rows, "rows", _MAX_ROWS)
+    wt = _norm_weight(weight, H)
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    ldr = ldo = lds = 0
+    if residual is not None:
+        ldr, ldo = _matrix(residual, "residual", (x.dtype,)), _matrix(residual_out, "residual_out", (x.dtype,))
+        for t, what in ((residual, "residual"), (residual_out, "residual_out")):
+            if t.shape != x.shape:
+                raise ValueError(f"{what}: need shape {tuple(x.shape)}, got {tuple(t.shape)}")
+    if quantize == MOE_NORM_BF16:
+        ldy = _matrix(out, "out", tuple(_OUT))
+        form = MOE_NORM_BF16 if out.dtype == torch.bfloat16 else MOE_NORM_FP32
+        if out.shape != x.shape:
+            raise ValueError(f"out: need shape {tuple(x.shape)}, got {tuple(out.shape)}")
+        if scales is not None:
+            raise ValueError("scales belong to a quantised output")
+    elif quantize == MOE_NORM_FP8:
+        form, ldy, lds = quantize, _matrix(out, "out", _CODES), _matrix(scales, "scales", (torch.float32,))
+        if out.shape != x.shape or tuple(scales.shape) != (rows, _blocks(H)):
+            raise ValueError(f"out, scales: need shapes {tuple(x.shape)} and {(rows, _blocks(H))}, got {tuple(out.shape)} and "
+                             f"{tuple(scales.shape)}")
+    else:
+        form, element = quantize, MOE_MX_E4M3 if quantize == MOE_NORM_MX_E4M3 else MOE_MX_E2M1
+        ldy, lds = _mx_codes(out, "out", element, x.shape), _mx_scales(scales, "scales", x.shape)
+    _on(x.device, ("x", x), ("residual", residual), ("weight", weight), ("out", out), ("scales", scales),
+        ("residual_out", residual_out))
+    return MoeNormParams(rows, H, _OUT[x.dtype], wt, form, 0, _eps(eps), ldx, ldr, ldo, ldy, lds, 0, 0, 0, 0)
+
+
+def rms_norm(x, weight=None, residual=None, eps=1e-6, out=None, scales=None, residual_out=None, quantize=None,
+             out_dtype=torch.bfloat16, stream=None):
+    """RMS norm of the residual stream s = x + residual (x without one), rounded to
+    the stream's type (x and residual both bf16 or both fp32, [rows, hidden]) and
+    stored in ``residual_out``: ``out = s / sqrt(mean(s^2) + eps) * weight``, fp32
+    throughout, weight bf16 or fp32 [hidden] or None (1).
+
+    ``quantize`` None: out bf16 or fp32. "fp8": e4m3 codes with fp32 scales
+    [rows, ceil(hidden/128)], as quantize_fp8 quantises the fp32 values, for
+    fp8_matmul. "mx_e4m3" or "mx_e2m1": codes and E8M0 scale bytes as quantize_mx
+    makes them, for mx_matmul.
+
+    Returns out; (out, scales) when quantised; with residual, residual_out behind
+    them: (out, residual_out) or (out, scales, residual_out). ``residual_out`` may be
+    x or residual, and ``out`` x where the types agree. What ``out`` holds in
+    quantised form is never rounded to bf16 before."""
+    if not isinstance(quantize, (str, type(None))) or quantize not in _NORM:
+        raise ValueError(f"quantize: need None, 'fp8', 'mx_e4m3' or 'mx_e2m1', got {quantize!r}")
+    form = _NORM[quantize]
+    if out is None or (scales is None and quantize is not None) or (residual is not None and residual_out is None):
+        rows, H = _sizes(x, "x", 2)
+        if quantize in ("mx_e4m3", "mx_e2m1"):
+            if out is None or scales is None:
+                c, s = _empty_mx((rows, H), _MX[quantize[3:]], x.device, stream)
+                out, scales = c if out is None else out, s if scales is None else scales
+        elif quantize == "fp8":
+            out = _empty((rows, H), torch.float8_e4m3fn, x.device, stream) if out is None else out
+            scales = _empty((rows, _blocks(H)), torch.float32, x.device, stream) if scales is None else scales
+        elif out is None:
+            out = _empty((rows, H), _out_type(out_dtype), x.device, stream)
+        if residual is not None and residual_out is None:
+            residual_out = _empty((rows, H), x.dtype, x.device, stream)
+    eps = _bits(eps)
+    _call("moe_rms_norm", check_rms_norm_inputs, (x, weight, residual, eps, form, out, scales, residual_out), (form, eps),
+          (x, residual, weight, out, scales, residual_out), 0b111000, stream)
+    got = [out] + ([scales] if scales is not None else []) + ([residual_out] if residual is not None else [])
+    return got[0] if len(got) == 1 else tuple(got)
+
+
+def check_rms_norm_backward_inputs(dy, x, weight, eps, dresidual, dx, dweight):
+    ldy, ldx, ldd = _matrix(dy, "dy", tuple(_OUT)), _matrix(x, "x", tuple(_OUT)), 0
+    rows, H = x.shape
+    _at_most(rows, "rows", _MAX_ROWS)
+    wt = _norm_weight(weight, H)
+    ldo = _matrix(dx, "out", (x.dtype,))
+    if dresidual is not None:
+        ldd = _matrix(dresidual, "dresidual", (x.dtype,))
+    for t, what in ((dy, "dy"), (dx, "out"), (dresidual, "dresidual")):
+        if t is not None and t.shape != x.shape:
+            raise ValueError(f"{what}: need shape {tuple(x.shape)}, got {tuple(t.shape)}")
+    if dweight is not None:
+        _vector(dweight, "dweight", H, torch.float32)
+    _on(dy.device, ("dy", dy), ("x", x), ("weight", weight), ("dresidual", dresidual), ("out", dx), ("dweight", dweight))
+    return MoeNormParams(rows, H, _OUT[x.dtype], wt, MOE_NORM_BF16 if dy.dtype == torch.bfloat16 else MOE_NORM_FP32,
+                         int(dweight is not None), _eps(eps), ldx, 0, 0, 0, 0, ldy, ldd, ldo, 0)
+
+
+def rms_norm_backward(dy, x, weight=None, eps=1e-6, dresidual=None, out=None, dweight=None, stream=None):
+    """Gradients of rms_norm (without quantize) for dy [rows, hidden] bf16 or fp32:
+    (dx, dweight). ``x`` is the stream that was normalised: rms_norm's residual_out,
+    or its x where it had no residual. dx, of x's type and rounded once, is the
+    gradient of x and of residual alike; ``dresidual`` (x's type) is the gradient
+    that reaches residual_out from elsewhere and is added to it. dweight is fp32
+    [hidden], summed in an order that sizes alone settle (partial sums in a
+    workspace, allocated for the call); None without weight and dweight. ``out`` may
+    be dresidual or x, or dy where the types agree."""
+    if out is None:
+        out = _empty(_sizes(x, "x", 2), x.dtype, x.device, stream)
+    if dweight is None and weight is not None:
+        _, H = _sizes(x, "x", 2)
+        dweight = _empty((H,), torch.float32, x.device, stream)
+    eps = _bits(eps)
+    _call("moe_rms_norm_backward", check_rms_norm_backward_inputs, (dy, x, weight, eps, dresidual, out, dweight), (eps,),
+          (dy, x, weight, dresidual, out, dweight, None), 0b110000, stream)
+    return out, dweight

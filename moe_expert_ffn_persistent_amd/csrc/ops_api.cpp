@@ -84,13 +84,14 @@ constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 constexpr int kMaxSplits = 64;
 constexpr long long kMaxWorkspace = 256ll << 20;
 
-Choice choose(const GemmTile* tiles, int n, const GemmArgs& a, int bk, int tile, int splits, long long room) {
+// bk: sum's elements of a stage; eb: bytes an element of both operands, on average
+Choice choose(const GemmTile* tiles, int n, const GemmArgs& a, int bk, double eb, int tile, int splits, long long room) {
   const bool wgrad = a.op == MOE_GROUPED_WGRAD;
   const int nj = a.op == MOE_GROUPED_FORWARD ? a.n : a.k, nc = a.op == MOE_GROUPED_FORWARD ? a.k : a.n;
   const long long part = split_args(a, nullptr).part;
   const double written = wgrad ? (double)part : (double)a.expected * nj;
   const double touched = std::min<double>(a.L, a.expected) * a.n * a.k, rows = (double)a.expected * ((double)a.n + a.k);
-  const double read = (touched + rows) * (bk == 128 ? 1 : 2) / kReadRate;
+  const double read = (touched + rows) * eb / kReadRate;
   Choice best{tile > 0 ? tile : 1, splits > 0 ? splits : 1};
   double least = 1e300;
   for (int i = tile > 0 ? tile - 1 : 0; i < (tile > 0 ? tile : n); ++i) {
@@ -123,13 +124,14 @@ int32_t run(const GemmArgs& a, Choice c, float* ws, hipStream_t s, Launch launch
   if (c.splits == 1) return done(launch(c.tile, a, s));
   GemmArgs b = a;
   b.splits = c.splits;
+  b.vec_out = true;   // the workspace's rows
   const hipError_t e = launch(c.tile, split_args(b, ws), s);
   return e != hipSuccess ? done(e) : done(launch_join_splits(b, ws, s));
 }
 
 // Bytes that the automatic choice of a call takes
-int64_t workspace_of(const GemmTile* tiles, int n, const GemmArgs& a, int bk, int tile, int splits) {
-  const Choice c = choose(tiles, n, a, bk, tile, splits, kMaxWorkspace / 4);
+int64_t workspace_of(const GemmTile* tiles, int n, const GemmArgs& a, int bk, double eb, int tile, int splits) {
+  const Choice c = choose(tiles, n, a, bk, eb, tile, splits, kMaxWorkspace / 4);
   return c.splits > 1 ? c.splits * split_args(a, nullptr).part * 4 : 0;
 }
 
@@ -195,7 +197,7 @@ int32_t grouped(const moe_grouped_params* p, const int32_t* row_offset, void* x,
   if (!fast) return done(launch_gemm_any(a, false, stream));
   const long long room = workspace ? bytes / 4 : 0;
   if (splits > 1 && splits * split_args(a, nullptr).part > room) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  return run(a, choose(grouped_tiles(p), kBf16GemmTiles, a, 64, p->tile, splits, room), static_cast<float*>(workspace),
+  return run(a, choose(grouped_tiles(p), kBf16GemmTiles, a, 64, 2, p->tile, splits, room), static_cast<float*>(workspace),
              stream, launch_gemm_bf16);
 }
 
@@ -250,7 +252,7 @@ int32_t fp8(const moe_fp8_params* p, const int32_t* row_offset, const void* x, c
   if (!fast) return done(launch_gemm_any(a, true, stream));
   const long long room = workspace ? bytes / 4 : 0;
   if (splits > 1 && splits * split_args(a, nullptr).part > room) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  return run(a, choose(kFp8GemmTileTable, kFp8GemmTiles, a, 128, p->tile, splits, room), static_cast<float*>(workspace),
+  return run(a, choose(kFp8GemmTileTable, kFp8GemmTiles, a, 128, 1, p->tile, splits, room), static_cast<float*>(workspace),
              stream, launch_gemm_fp8);
 }
 
@@ -286,6 +288,23 @@ GemmArgs mx_args(const moe_mx_params* p) {
   a.expected = expected_rows(p->expected_rows, p->rows);
   a.splits = 1;
   return a;
+}
+
+// The tile kernels' sizes: rows of the operands on 16 bytes, of scales on four,
+// and lane offsets (256 rows of a tile) in 32 bits. A stride that leads to no
+// second row or matrix counts for nothing.
+bool mx_fast(const moe_mx_params* p) {
+  auto fits = [](long long stride, long long count, int whole, long long most) {
+    return count <= 1 || (stride % whole == 0 && stride <= most);
+  };
+  return fits(p->ld_x, p->rows, 16, 1 << 22) && fits(p->ld_w, p->n, 16, 1 << 22) && fits(p->ld_x_scales, p->rows, 4, kMaxStride) &&
+         fits(p->ld_w_scales, p->n, 4, kMaxStride) && fits(p->expert_stride_w, p->num_experts, 16, kMaxMatrix) &&
+         fits(p->expert_stride_w_scales, p->num_experts, 4, kMaxMatrix);
+}
+
+Choice mx_choice(const moe_mx_params* p, const GemmArgs& a, long long room) {
+  const bool e2m1 = p->x_format == MOE_MX_E2M1;
+  return choose(kMxTiles[e2m1], kMxGemmTiles, a, e2m1 ? 256 : 128, e2m1 ? 0.53 : 0.6, p->tile, p->splits, room);
 }
 
 bool norm_ok(const moe_norm_params* p, bool backward) {
@@ -422,7 +441,11 @@ int32_t moe_quantize_mx(const moe_mx_quantize_params* p, const void* x, const in
 }
 
 int64_t moe_mx_workspace_bytes(const moe_mx_params* p) {
-  return 0;
+  // ranges are joined in whole 16 bytes
+  if (!mx_ok(p) || !mx_fast(p) || p->tile > kMxGemmTiles || p->n % 8 || p->ld_y % 8) return 0;
+  const GemmArgs a = mx_args(p);
+  const Choice c = mx_choice(p, a, kMaxWorkspace / 4);
+  return c.splits > 1 ? c.splits * split_args(a, nullptr).part * 4 : 0;
 }
 
 int32_t moe_mx_matmul(const moe_mx_params* p, const int32_t* row_offset, const void* x, const void* x_scales, const void* w,
@@ -438,8 +461,16 @@ int32_t moe_mx_matmul(const moe_mx_params* p, const int32_t* row_offset, const v
   a.y = y;
   a.xs = static_cast<const float*>(x_scales);
   a.ws = static_cast<const float*>(w_scales);
-  if (p->tile > 0) return MOE_ERR_UNSUPPORTED;
-  return done(launch_gemm_mx_any(a, (hipStream_t)stream));
+  const bool fast = mx_fast(p) && aligned(x, 16) && aligned(w, 16) && words(x_scales, w_scales);
+  if (p->tile > kMxGemmTiles || (p->tile > 0 && !fast)) return MOE_ERR_UNSUPPORTED;
+  if (!fast) return done(launch_gemm_mx_any(a, (hipStream_t)stream));
+  a.vec_out = aligned(y, 16) && p->ld_y * elem(p->out_dtype) % 16 == 0;
+  // ranges of the sum are joined in whole 16 bytes
+  const bool ranges = a.vec_out && p->n % 8 == 0 && p->ld_y % 8 == 0;
+  const long long room = workspace && ranges ? p->workspace_bytes / 4 : 0;
+  if (p->splits > 1 && !ranges) return MOE_ERR_UNSUPPORTED;
+  if (p->splits > 1 && p->splits * split_args(a, nullptr).part > room) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return run(a, mx_choice(p, a, room), static_cast<float*>(workspace), (hipStream_t)stream, launch_gemm_mx);
 }
 
 int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t* row_pair,
@@ -546,7 +577,7 @@ int32_t moe_grouped_matmul_split(const moe_grouped_params* p, const int32_t* row
 
 int64_t moe_grouped_workspace_bytes(const moe_grouped_params* p) {
   if (!grouped_ok(p) || !split_ok(p->splits, 0) || !grouped_fast(p) || !grouped_tile_ok(p)) return 0;
-  return workspace_of(grouped_tiles(p), kBf16GemmTiles, grouped_args(p), 64, p->tile, p->splits);
+  return workspace_of(grouped_tiles(p), kBf16GemmTiles, grouped_args(p), 64, 2, p->tile, p->splits);
 }
 
 int32_t moe_swiglu(const moe_swiglu_params* p, const void* a_, const float* row_weight, const int32_t* row_offset,
@@ -657,7 +688,7 @@ int32_t moe_fp8_matmul_split(const moe_fp8_params* p, const int32_t* row_offset,
 
 int64_t moe_fp8_workspace_bytes(const moe_fp8_params* p) {
   if (!fp8_ok(p) || !split_ok(p->splits, 0) || !fp8_fast(p) || p->tile > kFp8GemmTiles) return 0;
-  return workspace_of(kFp8GemmTileTable, kFp8GemmTiles, fp8_args(p), 128, p->tile, p->splits);
+  return workspace_of(kFp8GemmTileTable, kFp8GemmTiles, fp8_args(p), 128, 1, p->tile, p->splits);
 }
 
 }  // extern "C"

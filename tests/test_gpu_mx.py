@@ -213,6 +213,49 @@ def test_mx_strides_and_alignment(counts, R, K, n, pad, lead, element):
     run_mx(counts, R, K, n, element, BF, pad=pad, lead=lead, behind=9 if counts else 0)
 
 
+@pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("tile", range(1, 11))
+@pytest.mark.parametrize("element", FORMATS)
+@pytest.mark.parametrize("counts,R,K,n", [([0, 33, 290, 1], 324, 272, 328), (None, 300, 64, 8), ([3, 0, 200], 203, 34, 65),
+                                          ([64, 128], 192, 512, 256), (None, 1, 8338, 136), (None, 257, 1056, 523), ([191, 129], 320, 2112, 136)],
+                         ids=lambda v: str(v).replace(" ", ""))
+def test_mx_every_tile(counts, R, K, n, element, tile, out_dtype):
+    run_mx(counts, R, K, n, element, out_dtype, pad=16, tile=tile, behind=3 if counts else 0)
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("tile", range(1, 11))
+@pytest.mark.parametrize("element", FORMATS)
+@pytest.mark.parametrize("splits", [2, 3, 64])
+def test_mx_sums_in_ranges(splits, element, tile, out_dtype):
+    run_mx([0, 40, 3, 70], 113, 1380, 136, element, out_dtype, tile=tile, splits=splits, behind=5, first=1)
+
+
+@pytest.mark.parametrize("element", FORMATS)
+def test_mx_automatic_ranges_and_refusals(element):
+    # few tiles and a long sum, whole and in ranges; ranges need whole 16 bytes of out
+    for n in (64, 61):
+        run_mx(None, 3, 16384, n, element, BF)
+        run_mx([2, 0, 1], 3, 8224, n, element, F32)
+    with pytest.raises(_lib.MoeError) as err:
+        run_mx(None, 3, 512, 61, element, BF, splits=2)
+    assert err.value.status == _lib.MOE_ERR_UNSUPPORTED
+    for kw in (dict(tile=11), dict(tile=1, pad=1)):
+        with pytest.raises(_lib.MoeError) as err:
+            run_mx(None, 3, 512, 64, element, BF, **kw)
+        assert err.value.status == _lib.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("element", FORMATS)
+def test_mx_result_does_not_depend_on_timing(element):
+    g = gen(9)
+    x, xs, _ = operand(g, element, 40, 8192)
+    w, ws, _ = operand(g, "e2m1", 136, 8192)
+    want = moe.mx_matmul(x, xs, w, ws, out_dtype=F32)
+    for _ in range(5):
+        assert torch.equal(moe.mx_matmul(x, xs, w, ws, out_dtype=F32), want)
+
+
 @pytest.mark.parametrize("pad", [0, 1], ids=["aligned", "odd"])
 @pytest.mark.parametrize("K", [1, 3, 33, 127, 129, 1001])
 def test_odd_sums_of_e4m3_rows(K, pad):
@@ -227,9 +270,9 @@ def test_odd_sums_of_e4m3_rows(K, pad):
 
 
 @pytest.mark.parametrize("element", FORMATS)
-@pytest.mark.parametrize("pad", [0, 1], ids=["aligned", "odd"])
-@pytest.mark.parametrize("R,K,n", [(40, 1024, 72), (3, 416, 264)])
-def test_exact_products(R, K, n, element, pad):
+@pytest.mark.parametrize("R,K,n", [(40, 1024, 72), (3, 416, 264), (300, 768, 520)])
+@pytest.mark.parametrize("tile,pad", [(t, 0) for t in range(11)] + [(0, 1)])
+def test_exact_products(R, K, n, element, pad, tile):
     # small whole numbers times powers of two: every sum is exact in fp32 and nothing lies 2^13 below another product,
     # so a wrong element, scale or block shows as a wrong bit
     g = gen(3)
@@ -251,7 +294,7 @@ def test_exact_products(R, K, n, element, pad):
     x = place(mi.e4m3_encode(xv.float().numpy()), 16).view(F8) if element == "e4m3" else place(pairs(xv), 16)
     spread = lambda s: torch.pow(2.0, s.double() - 127).repeat_interleave(32, dim=1)   # noqa: E731
     ref = (xv * spread(xs)) @ (wv * spread(ws)).t()
-    got = moe.mx_matmul(x, place(xs.numpy(), 4), place(pairs(wv), 16), place(ws.numpy(), 4), out_dtype=F32)
+    got = moe.mx_matmul(x, place(xs.numpy(), 4), place(pairs(wv), 16), place(ws.numpy(), 4), out_dtype=F32, tile=tile)
     assert torch.equal(got.cpu().double(), ref)
 
 

@@ -229,7 +229,7 @@ hipError_t launch_join_splits(const GemmArgs& a, const float* ws, hipStream_t s)
 hipError_t launch_gemm_bf16(int id, const GemmArgs& a, hipStream_t s);
 hipError_t launch_gemm_fp8(int id, const GemmArgs& a, hipStream_t s);
 constexpr int kMxGemmTiles = 10;
-extern const GemmTile kMxTiles[2][kMxGemmTiles];   // by the type of x: e4m3, e2m1; id - 1
+extern const GemmTile kMxTiles[2][kMxGemmTiles];   // by the type of x: e4m3, e2m1; id - 1; tm 0: not a tile of it
 hipError_t launch_gemm_mx(int id, const GemmArgs& a, hipStream_t s);
 hipError_t launch_gemm_mx_any(const GemmArgs& a, hipStream_t s);
 

@@ -155,7 +155,7 @@ struct NormArgs {
 };
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
 // workgroups of the backward pass, each with a partial sum of dweight
-int norm_backward_groups(long long rows, int hidden);
+int norm_backward_groups(long long rows, int hidden, bool fp32);
 hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s);
 
 struct SwigluArgs {

@@ -113,34 +113,44 @@ template <class T, int KIND, int P, int THREADS>
 __global__ void __launch_bounds__(THREADS) moe_rms_norm_k(const NormArgs a, int tpr) {
   __shared__ float part[2][THREADS / 64][1];
   const int sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr, rpw = THREADS / tpr;
+  const long long step = (long long)gridDim.x * rpw;
+  struct Row {
+    Raw<T> x[P], res[P];
+  } row, next;
+  auto load = [&](Row& to, long long r) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * tpr + t) * 8, m = r < a.rows ? min(8, a.hidden - c) : 0;
+      to.x[p] = Raw<T>{};
+      to.res[p] = Raw<T>{};
+      if (m <= 0) continue;
+      to.x[p].load(static_cast<const T*>(a.x) + r * a.ld_x + c, m, a.vec);
+      if (a.residual) to.res[p].load(static_cast<const T*>(a.residual) + r * a.ld_residual + c, m, a.vec);
+    }
+  };
+  load(row, (long long)blockIdx.x * rpw + sub);
   float w[P][8];
 #pragma unroll
   for (int p = 0; p < P; ++p) load_weight(a, (p * tpr + t) * 8, w[p]);
   int odd = 0;
-  for (long long base = (long long)blockIdx.x * rpw; base < a.rows; base += (long long)gridDim.x * rpw, odd ^= 1) {
+  for (long long base = (long long)blockIdx.x * rpw; base < a.rows; base += step, odd ^= 1) {
     const long long r = base + sub;
     const bool live = r < a.rows;
+    if (base + step < a.rows) load(next, r + step);
     float v[P][8], sum[1] = {0.f};
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
+      row.x[p].get(v[p]);
+      if (a.residual) {
+        float o[8];
+        row.res[p].get(o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
-      if (m > 0) load8(static_cast<const T*>(a.x) + r * a.ld_x + c, m, a.vec && m == 8, v[p]);
-    }
-    if (a.residual) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
-        add_stream<T>(a, r, c, m, a.vec && m == 8, v[p]);
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
-      if (a.stream && m > 0) {
-        if constexpr (sizeof(T) == 4) store8(static_cast<float*>(a.stream) + r * a.ld_stream + c, m, a.vec && m == 8, v[p]);
-        else moe::store8(static_cast<__bf16*>(a.stream) + r * a.ld_stream + c, m, a.vec && m == 8, v[p]);
+        for (int i = 0; i < 8; ++i) v[p][i] = (float)(T)(v[p][i] + o[i]);
+        if (m > 0) {
+          if constexpr (sizeof(T) == 4) store8(static_cast<float*>(a.stream) + r * a.ld_stream + c, m, a.vec && m == 8, v[p]);
+          else moe::store8(static_cast<__bf16*>(a.stream) + r * a.ld_stream + c, m, a.vec && m == 8, v[p]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(v[p][i], v[p][i], sum[0]);
@@ -156,6 +166,7 @@ __global__ void __launch_bounds__(THREADS) moe_rms_norm_k(const NormArgs a, int 
       // a row that is not there: its lanes take part in no other row's blocks
       if (live) store_out<KIND>(a, r, c, a.vec && a.hidden - c >= 8, y);
     }
+    row = next;
   }
 }
 
@@ -195,76 +206,96 @@ __global__ void __launch_bounds__(1024) moe_rms_norm_long_k(const NormArgs a) {
   }
 }
 
-// The gradients. A workgroup walks its rows and keeps its part of dw in
-// registers; the parts are joined by a second kernel, in their order.
+// The gradients. A workgroup walks its rows, the next one on its way while one is
+// summed, and keeps its part of dw in registers; the parts are joined by a second
+// kernel, in their order.
 template <class T, class D, int P, int THREADS>
 __global__ void __launch_bounds__(THREADS) moe_rms_norm_backward_k(const NormArgs a, int tpr) {
   __shared__ float part[2][THREADS / 64][2];
-  __shared__ float joined[P == 1 ? THREADS * 8 : 1];
+  __shared__ float joined[P == 1 && THREADS == 256 ? THREADS * 8 : 1];
   const int sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr, rpw = THREADS / tpr;
+  const long long step = (long long)gridDim.x * rpw;
+  struct Row {
+    Raw<T> x[P], add[P];
+    Raw<D> dy[P];
+  } row, next;
+  constexpr bool AHEAD = P == 1;   // two pieces and their successors are too many registers
+  auto load = [&](Row& to, long long r) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = (p * tpr + t) * 8, m = r < a.rows ? min(8, a.hidden - c) : 0;
+      to.x[p] = Raw<T>{};
+      to.add[p] = Raw<T>{};
+      to.dy[p] = Raw<D>{};
+      if (m <= 0) continue;
+      to.x[p].load(static_cast<const T*>(a.x) + r * a.ld_x + c, m, a.vec);
+      to.dy[p].load(static_cast<const D*>(a.dy) + r * a.ld_dy + c, m, a.vec);
+      if (a.dresidual) to.add[p].load(static_cast<const T*>(a.dresidual) + r * a.ld_dresidual + c, m, a.vec);
+    }
+  };
+  if constexpr (AHEAD) load(row, (long long)blockIdx.x * rpw + sub);
   float w[P][8], dw[P][8] = {};
 #pragma unroll
   for (int p = 0; p < P; ++p) load_weight(a, (p * tpr + t) * 8, w[p]);
   int odd = 0;
-  for (long long base = (long long)blockIdx.x * rpw; base < a.rows; base += (long long)gridDim.x * rpw, odd ^= 1) {
+  for (long long base = (long long)blockIdx.x * rpw; base < a.rows; base += step, odd ^= 1) {
     const long long r = base + sub;
     const bool live = r < a.rows;
-    float v[P][8], d[P][8], sum[2] = {0.f, 0.f};
+    if constexpr (!AHEAD) load(row, r);
+    else if (base + step < a.rows) load(next, r + step);
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[p][i] = d[p][i] = 0.f;
-      if (m > 0) {
-        load8(static_cast<const T*>(a.x) + r * a.ld_x + c, m, a.vec && m == 8, v[p]);
-        load8(static_cast<const D*>(a.dy) + r * a.ld_dy + c, m, a.vec && m == 8, d[p]);
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p)
+      float v[8], d[8];
+      row.x[p].get(v);
+      row.dy[p].get(d);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum[0] = __builtin_fmaf(v[p][i], v[p][i], sum[0]);
-        sum[1] = __builtin_fmaf(d[p][i] * w[p][i], v[p][i], sum[1]);
+        sum[0] = __builtin_fmaf(v[i], v[i], sum[0]);
+        sum[1] = __builtin_fmaf(d[i] * w[p][i], v[i], sum[1]);
       }
+    }
     row_sum<2, THREADS>(sum, tpr, part[odd]);
     const float inv = rms_inv(sum[0], a.hidden, a.eps);
     const float along = inv * inv * (sum[1] / (float)a.hidden);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = (p * tpr + t) * 8, m = live ? min(8, a.hidden - c) : 0;
-      float g[8], add[8] = {};
-      const bool vec = a.vec && m == 8;
-      if (a.dresidual && m > 0) load8(static_cast<const T*>(a.dresidual) + r * a.ld_dresidual + c, m, vec, add);
+      float v[8], d[8], g[8];
+      row.x[p].get(v);
+      row.dy[p].get(d);
+      row.add[p].get(g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        g[i] = __builtin_fmaf(inv, d[p][i] * w[p][i] - v[p][i] * along, add[i]);
-        dw[p][i] = __builtin_fmaf(d[p][i], live ? v[p][i] * inv : 0.f, dw[p][i]);
+        g[i] = __builtin_fmaf(inv, d[i] * w[p][i] - v[i] * along, g[i]);
+        dw[p][i] = __builtin_fmaf(d[i], live ? v[i] * inv : 0.f, dw[p][i]);
       }
       if (m > 0) {
-        if constexpr (sizeof(T) == 4) store8(static_cast<float*>(a.dx) + r * a.ld_dx + c, m, vec, g);
-        else moe::store8(static_cast<__bf16*>(a.dx) + r * a.ld_dx + c, m, vec, g);
+        if constexpr (sizeof(T) == 4) store8(static_cast<float*>(a.dx) + r * a.ld_dx + c, m, a.vec && m == 8, g);
+        else moe::store8(static_cast<__bf16*>(a.dx) + r * a.ld_dx + c, m, a.vec && m == 8, g);
       }
     }
+    if constexpr (AHEAD) row = next;
   }
   if (!a.part) return;
   float* out = a.part + (long long)blockIdx.x * a.hidden;
   if (rpw > 1) {   // the rows of the workgroup that ran side by side (P is 1)
+    if constexpr (P == 1 && THREADS == 256) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) joined[threadIdx.x * 8 + i] = dw[0][i];
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.hidden; c += THREADS) {
-      float sum = 0.f;
-      for (int s = 0; s < rpw; ++s) sum += joined[s * tpr * 8 + c];
-      out[c] = sum;
+      for (int i = 0; i < 8; ++i) joined[threadIdx.x * 8 + i] = dw[0][i];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.hidden; c += THREADS) {
+        float sum = 0.f;
+        for (int s = 0; s < rpw; ++s) sum += joined[s * tpr * 8 + c];
+        out[c] = sum;
+      }
     }
   } else {
+    const bool vec = a.hidden % 4 == 0 && (uintptr_t)a.part % 16 == 0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = (p * tpr + t) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < a.hidden) out[c + i] = dw[p][i];
+      if (c < a.hidden) store8(out + c, a.hidden - c, vec && c + 8 <= a.hidden, dw[p]);
     }
   }
 }
@@ -315,24 +346,42 @@ __global__ void __launch_bounds__(1024) moe_rms_norm_backward_long_k(const NormA
   }
 }
 
-// dw(c) = sum over the groups of part(g, c), ascending within 16 slices, then
-// the slices: 64 columns a workgroup, four of them a thread.
+// dw(c) = sum over the groups of part(g, c), ascending within 64 slices, then the
+// slices: 16 columns a workgroup, four of them a thread, four groups of a slice in
+// flight (with 16 slices of one at a time 512 groups of 4096 columns took 20 us).
 __global__ void __launch_bounds__(256) moe_join_dweight_k(const float* part, float* dweight, int groups, int hidden) {
-  __shared__ float slice[16][64];
-  const int c0 = blockIdx.x * 64 + (threadIdx.x & 15) * 4, s = threadIdx.x >> 4;
+  __shared__ float slice[64][17];
+  const int c0 = blockIdx.x * 16 + (threadIdx.x & 3) * 4, s = threadIdx.x >> 2;
+  const bool vec = hidden % 4 == 0;
   float sum[4] = {};
-  for (int g = s; g < groups; g += 16)
+  for (int g = s; g < groups; g += 256) {
+    float v[4][4] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c0 + i < hidden) sum[i] += part[(long long)g * hidden + c0 + i];
+    for (int u = 0; u < 4; ++u) {
+      if (g + 64 * u >= groups || c0 >= hidden) continue;
+      const float* src = part + (long long)(g + 64 * u) * hidden + c0;
+      if (vec) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+      } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) slice[s][(threadIdx.x & 15) * 4 + i] = sum[i];
+        for (int i = 0; i < 4; ++i)
+          if (c0 + i < hidden) v[u][i] = src[i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += v[u][i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) slice[s][(threadIdx.x & 3) * 4 + i] = sum[i];
   __syncthreads();
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x < 64 && c < hidden) {
+  const int c = blockIdx.x * 16 + threadIdx.x;
+  if (threadIdx.x < 16 && c < hidden) {
     float all = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) all += slice[i][threadIdx.x];
+    for (int i = 0; i < 64; ++i) all += slice[i][threadIdx.x];
     dweight[c] = all;
   }
 }
@@ -347,26 +396,38 @@ int threads_for(int hidden, int most) {
   return t;
 }
 
+// Threads of a workgroup, and the pieces of a row that each holds: few rows take a
+// thread for each piece (128 x 7168: 4.9 us, with 256 threads of four pieces 6.7),
+// many fewer, so that a compute unit holds several rows (16384 x 7168 forward 179 us,
+// 190 with 1024 threads of one piece, 194 with 256 of four; to MX e4m3 163, 187, 255).
+template <class F>
+hipError_t with_shape(long long rows, int hidden, F f) {
+  using std::integral_constant;
+  constexpr integral_constant<int, 1> one{};
+  constexpr integral_constant<int, 2> two{};
+  if (hidden <= 2048) return f(one, integral_constant<int, 256>{});
+  if (hidden <= 4096) return f(one, integral_constant<int, 512>{});
+  if (hidden <= 8192) {
+    if (rows <= 512) return f(one, integral_constant<int, 1024>{});
+    return f(two, integral_constant<int, 512>{});
+  }
+  if (hidden <= 16384) return f(two, integral_constant<int, 1024>{});
+  return f(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
+}
+
 template <class T, int KIND>
 hipError_t forward(const NormArgs& a, hipStream_t s) {
   if (a.hidden > kHeld) {
     moe_rms_norm_long_k<T, KIND><<<(unsigned)std::min<long long>(a.rows, 4 * kCus), 1024, 0, s>>>(a);
     return hipGetLastError();
   }
-  auto run = [&](auto pieces, auto threads) {
+  return with_shape(a.rows, a.hidden, [&](auto pieces, auto threads) {
     constexpr int P = decltype(pieces)::value, THREADS = decltype(threads)::value;
-    const int tpr = P == 1 ? threads_for(a.hidden, THREADS) : THREADS;
+    const int tpr = P == 1 && THREADS == 256 ? threads_for(a.hidden, THREADS) : THREADS;
     const long long need = (a.rows + THREADS / tpr - 1) / (THREADS / tpr);
-    moe_rms_norm_k<T, KIND, P, THREADS><<<(unsigned)std::min<long long>(need, 8 * kCus), THREADS, 0, s>>>(a, tpr);
+    moe_rms_norm_k<T, KIND, P, THREADS><<<(unsigned)std::min<long long>(need, kCus * 2048ll / THREADS), THREADS, 0, s>>>(a, tpr);
     return hipGetLastError();
-  };
-  using std::integral_constant;
-  constexpr integral_constant<int, 256> narrow{};
-  constexpr integral_constant<int, 1024> wide{};
-  if (a.hidden <= 2048) return run(integral_constant<int, 1>{}, narrow);
-  if (a.hidden <= 4096) return run(integral_constant<int, 2>{}, narrow);
-  if (a.hidden <= 8192) return run(integral_constant<int, 4>{}, narrow);
-  return run(integral_constant<int, 4>{}, wide);
+  });
 }
 
 template <class T>
@@ -381,29 +442,31 @@ hipError_t forward_kind(const NormArgs& a, hipStream_t s) {
 
 template <class T, class D>
 hipError_t backward(const NormArgs& a, hipStream_t s) {
-  const int groups = norm_backward_groups(a.rows, a.hidden);
+  const int groups = norm_backward_groups(a.rows, a.hidden, a.fp32);
   if (a.hidden > kHeld) {
     moe_rms_norm_backward_long_k<T, D><<<groups, 1024, 0, s>>>(a);
   } else {
-    auto run = [&](auto pieces, auto threads) {
+    with_shape(a.rows, a.hidden, [&](auto pieces, auto threads) {
       constexpr int P = decltype(pieces)::value, THREADS = decltype(threads)::value;
-      moe_rms_norm_backward_k<T, D, P, THREADS><<<groups, THREADS, 0, s>>>(a, P == 1 ? threads_for(a.hidden, THREADS) : THREADS);
-    };
-    using std::integral_constant;
-    if (a.hidden <= 2048) run(integral_constant<int, 1>{}, integral_constant<int, 256>{});
-    else if (a.hidden <= 4096) run(integral_constant<int, 2>{}, integral_constant<int, 256>{});
-    else if (a.hidden <= 8192) run(integral_constant<int, 4>{}, integral_constant<int, 256>{});
-    else run(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
+      moe_rms_norm_backward_k<T, D, P, THREADS><<<groups, THREADS, 0, s>>>(a, P == 1 && THREADS == 256 ? threads_for(a.hidden, THREADS) : THREADS);
+      return hipSuccess;
+    });
   }
-  if (a.part && a.part != a.dweight) moe_join_dweight_k<<<(a.hidden + 63) / 64, 256, 0, s>>>(a.part, a.dweight, groups, a.hidden);
+  if (a.part && a.part != a.dweight) moe_join_dweight_k<<<(a.hidden + 15) / 16, 256, 0, s>>>(a.part, a.dweight, groups, a.hidden);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int norm_backward_groups(long long rows, int hidden) {
+// As many as the compute units hold at once by their registers (16384 x 7168 bf16: 186
+// us with two a unit, 217 with one; fp32 8192 x 7168: 171 and 164). Beyond one a unit
+// only with some rows each, since a part is as long as a row in fp32 (1024 x 7168: 23
+// us with 256, 30 with 512).
+int norm_backward_groups(long long rows, int hidden, bool fp32) {
   const int rpw = hidden <= 2048 ? 256 / threads_for(hidden, 256) : 1;
-  return (int)std::min<long long>((rows + rpw - 1) / rpw, 2 * kCus);
+  const int each = hidden <= 2048 ? 4 : hidden <= 4096 ? 2 : hidden <= 8192 && !fp32 ? 2 : 1;
+  const long long need = (rows + rpw - 1) / rpw;
+  return (int)std::min<long long>(each * kCus, std::max(std::min<long long>(need, kCus), need / (hidden <= 2048 ? 2 : 4)));
 }
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {

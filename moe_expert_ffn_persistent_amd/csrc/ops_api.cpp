@@ -370,7 +370,7 @@ int32_t moe_rms_norm(const moe_norm_params* p, const void* x, const void* residu
 
 int64_t moe_rms_norm_workspace_bytes(const moe_norm_params* p) {
   if (!norm_ok(p, true) || !p->weight_gradient || p->rows == 0) return 0;
-  const int groups = norm_backward_groups(p->rows, p->hidden);
+  const int groups = norm_backward_groups(p->rows, p->hidden, p->stream_dtype == MOE_Y_FP32);
   return groups > 1 ? (int64_t)groups * p->hidden * 4 : 0;
 }
 

@@ -160,6 +160,44 @@ __device__ __forceinline__ void store8(__bf16* p, int n, bool vec, const float (
   }
 }
 
+// Eight columns as they lie in memory, so that a row waits in half the registers
+// (bf16), of which the first m exist (the others read as zero)
+template <class T>
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+
+  __device__ __forceinline__ void load(const T* p, int m, bool vec) {
+    if (vec && m >= 8) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+      uint32_t w[2 * sizeof(T)] = {};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < m) {
+          if constexpr (sizeof(T) == 4) w[i] = __builtin_bit_cast(uint32_t, p[i]);
+          else w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (16 * (i & 1));
+        }
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    }
+  }
+
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      unpack8(v[0], x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[4 * i] = __builtin_bit_cast(float, v[i].x);
+        x[4 * i + 1] = __builtin_bit_cast(float, v[i].y);
+        x[4 * i + 2] = __builtin_bit_cast(float, v[i].z);
+        x[4 * i + 3] = __builtin_bit_cast(float, v[i].w);
+      }
+    }
+  }
+};
+
 // Block scale of values whose largest magnitude has the fp32 bits `amax`
 // (taken as an integer maximum, which carries infinities and NaN along):
 // fp32(amax / 448), 1 for a block of zeros or one whose quotient underflows.

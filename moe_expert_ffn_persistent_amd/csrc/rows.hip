@@ -131,46 +131,47 @@ __global__ void __launch_bounds__(256) moe_combine_backward_k(const CombineBackw
   if (local) {
     const D* dy = static_cast<const D*>(a.dy) + (size_t)n * a.ld_dy;
     const int t0 = threadIdx.x % TPT * 8;
-    float d[U][8];
-    auto load_dy = [&](int c0) {
+    Raw<D> d[U];
+    Raw<__bf16> x[2][U];
+    auto load = [&](auto& to, const auto* row, int c0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[u][i] = 0.f;
-        if (m > 0) load8(dy + c, m, a.vec && m == 8, d[u]);
+        to[u] = {};
+        if (m > 0) to[u].load(row + c, m, a.vec);
       }
     };
-    load_dy(t0);
+    auto row_of = [&](int slot) { return static_cast<const __bf16*>(a.rows) + (size_t)__builtin_amdgcn_readlane(idx, slot) * a.ld_rows; };
+    load(x[0], row_of(__builtin_ctzll(local)), t0);
+    load(d, dy, t0);
     for (uint64_t left = local; left; left &= left - 1) {
       const int slot = __builtin_ctzll(left);
-      const int r = __builtin_amdgcn_readlane(idx, slot);
       const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), slot));
-      const __bf16* row = static_cast<const __bf16*>(a.rows) + (size_t)r * a.ld_rows;
-      __bf16* drow = static_cast<__bf16*>(a.drows) + (size_t)r * a.ld_drows;
+      const uint64_t more = left & (left - 1);
+      if (more) load(x[1], row_of(__builtin_ctzll(more)), t0);   // the next row is on its way
+      __bf16* drow = static_cast<__bf16*>(a.drows) + (size_t)__builtin_amdgcn_readlane(idx, slot) * a.ld_drows;
       float dot = 0.f;
       for (int c0 = t0; c0 < a.hidden; c0 += U * TPT * 8) {
-        if (a.hidden > U * TPT * 8) load_dy(c0);
-        float x[U][8];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-          if (m > 0) load8(row + c, m, a.vec && m == 8, x[u]);
+        if (a.hidden > U * TPT * 8) {
+          load(d, dy, c0);
+          if (c0 != t0) load(x[0], row_of(slot), c0);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
-          float g[8];
+          float g[8], z[8];
+          d[u].get(g);
+          x[0][u].get(z);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            dot = __builtin_fmaf(d[u][i], x[u][i], dot);
-            g[i] = w * d[u][i];
+            dot = __builtin_fmaf(g[i], z[i], dot);
+            g[i] *= w;
           }
           if (m > 0) store8(drow + c, m, a.vec && m == 8, g);
         }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[0][u] = x[1][u];
 #pragma unroll
       for (int s = 1; s < 64; s <<= 1) dot += __shfl_xor(dot, s, 64);
       if (lane == slot) mine = dot;

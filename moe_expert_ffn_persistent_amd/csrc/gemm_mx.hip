@@ -29,12 +29,13 @@ namespace moe {
 namespace {
 
 // 16 (or 4) bytes a lane from base + voff (bytes) to LDS m0 + 16 (4) * lane; s_nop: m0's
-// wait state (see dma16 in ffn_common.hpp)
+// wait state (see dma16 in ffn_common.hpp), and the 5 after a base that a lane read wrote
+// (where there are more bases than registers they are read back right before)
 __device__ __forceinline__ void dma16s(uint32_t voff, const char* base, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4s(uint32_t voff, const char* base, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(m0) : "memory", "m0");
 }
 
 // f(0) .. f(N - 1), the numbers as types: whole loops of what is chosen at compile
@@ -179,17 +180,22 @@ struct TileM {
   // 16 bytes at `src` of which `n` e4m3 bytes (PACKED: e2m1 codes) exist
   template <bool PACKED>
   __device__ __forceinline__ static uint4 partial(const char* src, int n) {
-    uint64_t v[2] = {0, 0};
     const int bytes = PACKED ? (n + 1) / 2 : n;
-#pragma unroll 1
-    for (int b = 0; b < bytes; ++b) {
-      uint64_t x = (uint8_t)src[b];
-      if (PACKED && 2 * b + 1 == n) x &= 0x0f;
-      x <<= 8 * (b & 7);
-      if (b < 8) v[0] |= x;
-      else v[1] |= x;
+    uint32_t v[4];
+    // whole words, then the bytes behind them: all on their way at once
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 4 * i + 4 <= bytes ? reinterpret_cast<const uint32_t*>(src)[i] : 0u;
+    uint32_t last = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if ((bytes & ~3) + i < bytes) last |= (uint32_t)(uint8_t)src[(bytes & ~3) + i] << (8 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i == bytes / 4) v[i] = last;
+      // an odd row's last byte holds one code
+      if (PACKED && (n & 1) && i == (bytes - 1) / 4) v[i] &= ~(0xf0u << (8 * ((bytes - 1) & 3)));
     }
-    return uint4{(uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32)};
+    return uint4{v[0], v[1], v[2], v[3]};
   }
 
   template <int copy>
@@ -222,8 +228,9 @@ struct TileM {
         if (C::RB % C::NW != 0 && b >= C::RB) continue;
         const uint8_t* src = reinterpret_cast<const uint8_t*>(scales_of(b, group)) + sv[i];
         uint32_t word = 0x7f7f7f7fu;
-#pragma unroll 1
-        for (int j = 0; j < 4 && w * 128 + j * 32 < k; ++j) word = (word & ~(0xffu << (8 * j))) | (uint32_t)src[j] << (8 * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (w * 128 + j * 32 < k) word = (word & ~(0xffu << (8 * j))) | (uint32_t)src[j] << (8 * j);
         *reinterpret_cast<uint32_t*>(lds + buffer(group) + b * 256 + (threadIdx.x & 63) * 4) = word;
       }
     }

@@ -135,7 +135,7 @@ struct CombineBackwardArgs {
   float* dweights;
   long long cap, ld_dy, ld_rows, ld_drows;   // rows that the buffers hold; strides in elements
   int tokens, k, hidden;
-  bool dy_fp32, vec;                         // vec: rows of all three are 16-byte aligned
+  bool dy_fp32;
 };
 hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t s);
 
@@ -151,7 +151,6 @@ struct NormArgs {
   int hidden, format;                 // MOE_NORM_*; backward: of dy
   float eps;
   bool fp32, weight_fp32;             // type of the stream (x, residual, dx, ...); of weight
-  bool vec;                           // every row and the weight are 16-byte aligned (codes 8, e2m1 codes 4)
 };
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
 // workgroups of the backward pass, each with a partial sum of dweight
@@ -189,7 +188,6 @@ struct MxQuantArgs {
   uint8_t *codes, *scales;
   long long rows, ld_x, ld_codes, ld_scales, bs_x, bs_codes, bs_scales;
   int batch, cols, L;
-  bool vec;                    // rows of x are 16-byte aligned, of codes as whole stores of a lane
 };
 hipError_t launch_quantize_mx(const MxQuantArgs& a, bool e2m1, bool fp32, hipStream_t s);
 

@@ -47,14 +47,16 @@ __device__ __forceinline__ uint32_t mx_e2m1x8(const float* x, const MxScale& s) 
   return s.byte == 255 ? 0u : q;
 }
 
-// E columns of which the first n exist (the others read as zero)
-template <int E, class T>
-__device__ __forceinline__ void load_cols(const T* p, int n, bool vec, float (&x)[E]) {
+// Columns c .. c+E-1 of a row of `cols` elements (zeros past its end)
+template <int E, bool WHOLE, class T>
+__device__ __forceinline__ void load_cols(const T* row, int c, int cols, float (&x)[E]) {
+  Raw<T, WHOLE> r[E / 8];
+#pragma unroll
+  for (int h = 0; h < E / 8; ++h) r[h].load(row, c + 8 * h, cols);
 #pragma unroll
   for (int h = 0; h < E / 8; ++h) {
-    const int m = min(8, n - 8 * h);
-    float v[8] = {};
-    if (m > 0) load8(p + 8 * h, m, vec && m == 8, v);
+    float v[8];
+    r[h].get(v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[8 * h + i] = v[i];
   }
@@ -63,7 +65,7 @@ __device__ __forceinline__ void load_cols(const T* p, int n, bool vec, float (&x
 // Codes of columns c .. c+E-1 (c a multiple of E) of a row of `cols` elements,
 // into the row's bytes. An odd row's last byte has zeros in its high bits.
 template <bool E2M1, int E>
-__device__ __forceinline__ void store_mx(uint8_t* row, int c, int cols, bool vec, const float (&x)[E], const MxScale& s) {
+__device__ __forceinline__ void store_mx(uint8_t* row, int c, int cols, const float (&x)[E], const MxScale& s) {
   const int n = cols - c;
   if (n <= 0) return;
   if constexpr (E2M1) {
@@ -71,9 +73,9 @@ __device__ __forceinline__ void store_mx(uint8_t* row, int c, int cols, bool vec
 #pragma unroll
     for (int h = 0; h < E / 8; ++h) q[h] = mx_e2m1x8(x + 8 * h, s);
     uint8_t* p = row + c / 2;
-    if (vec && n >= E) {
-      if constexpr (E == 16) *reinterpret_cast<uint2*>(p) = uint2{q[0], q[1]};
-      else *reinterpret_cast<uint32_t*>(p) = q[0];
+    if (n >= E) {
+      if constexpr (E == 16) *reinterpret_cast<u32x2u*>(p) = u32x2u{q[0], q[1]};
+      else *reinterpret_cast<u32u*>(p) = q[0];
     } else {
 #pragma unroll
       for (int i = 0; i < E / 2; ++i)
@@ -84,9 +86,9 @@ __device__ __forceinline__ void store_mx(uint8_t* row, int c, int cols, bool vec
 #pragma unroll
     for (int h = 0; h < E / 8; ++h) q[h] = mx_e4m3x8(x + 8 * h, s);
     uint8_t* p = row + c;
-    if (vec && n >= E) {
-      if constexpr (E == 16) *reinterpret_cast<uint4*>(p) = uint4{q[0].x, q[0].y, q[1].x, q[1].y};
-      else *reinterpret_cast<uint2*>(p) = q[0];
+    if (n >= E) {
+      if constexpr (E == 16) *reinterpret_cast<u32x4u*>(p) = u32x4u{q[0].x, q[0].y, q[1].x, q[1].y};
+      else *reinterpret_cast<u32x2u*>(p) = u32x2u{q[0].x, q[0].y};
     } else {
 #pragma unroll
       for (int h = 0; h < E / 8; ++h)

@@ -6,6 +6,8 @@
 //   code = the format's value nearest to x / 2^e, ties to even, at most its largest
 //
 // One pass over the bytes, bound by HBM when large and by the launch when small.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "mx_common.hpp"
 
@@ -14,7 +16,7 @@ namespace {
 
 // A lane holds E columns of a block (32 / E lanes each). bf16 takes E = 16, two
 // 16-byte loads; fp32 takes E = 8, since its loads would else lie 64 bytes apart.
-template <class T, int E, bool E2M1>
+template <class T, int E, bool E2M1, bool WHOLE>
 __global__ void __launch_bounds__(256) moe_quantize_mx_k(const MxQuantArgs a, int tpr) {
   int lo, hi;
   row_range(a.row_offset, a.L, a.rows, lo, hi);
@@ -27,12 +29,12 @@ __global__ void __launch_bounds__(256) moe_quantize_mx_k(const MxQuantArgs a, in
     for (int c = (blockIdx.y * tpr + t) * E; c < kb * 32; c += gridDim.y * tpr * E) {   // alike for the lanes of a block
       float x[E];
       uint32_t mx = 0;
-      load_cols<E>(x0 + r * a.ld_x + c, a.cols - c, a.vec, x);
+      load_cols<E, WHOLE>(x0 + r * a.ld_x, c, a.cols, x);
 #pragma unroll
       for (int i = 0; i < E; ++i) mx = max(mx, abs_bits(x[i]));
       mx = E == 16 ? max2(mx) : max4(mx);
       const MxScale s = mx_scale<E2M1>(mx);
-      store_mx<E2M1, E>(q0 + r * a.ld_codes, c, a.cols, a.vec, x, s);
+      store_mx<E2M1, E>(q0 + r * a.ld_codes, c, a.cols, x, s);
       if (t % (32 / E) == 0) s0[r * a.ld_scales + c / 32] = s.byte;
     }
   }
@@ -47,13 +49,18 @@ hipError_t launch_quantize_mx(const MxQuantArgs& a, bool e2m1, bool fp32, hipStr
   const long long need = (a.rows + 256 / tpr - 1) / (256 / tpr);
   const int y = (int)std::min<long long>((pieces + tpr - 1) / tpr, std::max<long long>(1, 1024 / need));
   const dim3 grid((unsigned)std::min<long long>(need, 4096), y, a.batch);
-  if (fp32) {
-    if (e2m1) moe_quantize_mx_k<float, 8, true><<<grid, 256, 0, s>>>(a, tpr);
-    else moe_quantize_mx_k<float, 8, false><<<grid, 256, 0, s>>>(a, tpr);
-  } else {
-    if (e2m1) moe_quantize_mx_k<__bf16, 16, true><<<grid, 256, 0, s>>>(a, tpr);
-    else moe_quantize_mx_k<__bf16, 16, false><<<grid, 256, 0, s>>>(a, tpr);
-  }
+  auto run = [&](auto whole) {
+    constexpr bool W = decltype(whole)::value;
+    if (fp32) {
+      if (e2m1) moe_quantize_mx_k<float, 8, true, W><<<grid, 256, 0, s>>>(a, tpr);
+      else moe_quantize_mx_k<float, 8, false, W><<<grid, 256, 0, s>>>(a, tpr);
+    } else {
+      if (e2m1) moe_quantize_mx_k<__bf16, 16, true, W><<<grid, 256, 0, s>>>(a, tpr);
+      else moe_quantize_mx_k<__bf16, 16, false, W><<<grid, 256, 0, s>>>(a, tpr);
+    }
+  };
+  if (a.cols % 8 == 0) run(std::true_type{});
+  else run(std::false_type{});
   return hipGetLastError();
 }
 

@@ -361,10 +361,6 @@ int32_t moe_rms_norm(const moe_norm_params* p, const void* x, const void* residu
   a.eps = p->eps;
   a.fp32 = p->stream_dtype == MOE_Y_FP32;
   a.weight_fp32 = p->weight_dtype == MOE_Y_FP32;
-  // eight columns: 16 bytes of a row, or 8 and 4 bytes of codes
-  const long long piece = oe == 1 ? (e2m1 ? 4 : 8) : 16;
-  a.vec = aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) && aligned(weight, 16) && aligned(out, piece) &&
-          a.ld_x * se % 16 == 0 && a.ld_residual * se % 16 == 0 && a.ld_stream * se % 16 == 0 && a.ld_out * (long long)oe % piece == 0;
   return done(launch_rms_norm(a, (hipStream_t)stream));
 }
 
@@ -404,8 +400,6 @@ int32_t moe_rms_norm_backward(const moe_norm_params* p, const void* dy, const vo
   a.eps = p->eps;
   a.fp32 = p->stream_dtype == MOE_Y_FP32;
   a.weight_fp32 = p->weight_dtype == MOE_Y_FP32;
-  a.vec = aligned(x, 16) && aligned(dy, 16) && aligned(dresidual, 16) && aligned(dx, 16) && aligned(weight, 16) &&
-          a.ld_x * se % 16 == 0 && a.ld_dy * de % 16 == 0 && a.ld_dresidual * se % 16 == 0 && a.ld_dx * se % 16 == 0;
   return done(launch_rms_norm_backward(a, (hipStream_t)stream));
 }
 
@@ -441,10 +435,6 @@ int32_t moe_quantize_mx(const moe_mx_quantize_params* p, const void* x, const in
   a.batch = p->batch;
   a.cols = p->cols;
   a.L = p->num_experts;
-  // a lane's store: 16 columns of bf16, 8 of fp32
-  const long long piece = (xe == 2 ? 16 : 8) / (e2m1 ? 2 : 1);
-  a.vec = aligned(x, 16) && a.ld_x * xe % 16 == 0 && a.bs_x * xe % 16 == 0 && aligned(codes, piece) && a.ld_codes % piece == 0 &&
-          a.bs_codes % piece == 0;
   return done(launch_quantize_mx(a, e2m1, xe == 4, (hipStream_t)stream));
 }
 
@@ -567,7 +557,6 @@ int32_t moe_combine_rows_backward(const moe_combine_backward_params* p, const vo
   a.k = p->top_k;
   a.hidden = p->hidden;
   a.dy_fp32 = p->dy_dtype == MOE_Y_FP32;
-  a.vec = aligned(dy, 16) && aligned(in, 16) && aligned(din, 16) && a.ld_dy * de % 16 == 0 && a.ld_rows % 8 == 0 && a.ld_drows % 8 == 0;
   return done(launch_combine_backward(a, (hipStream_t)stream));
 }
 

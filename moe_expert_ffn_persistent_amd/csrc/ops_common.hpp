@@ -160,43 +160,113 @@ __device__ __forceinline__ void store8(__bf16* p, int n, bool vec, const float (
   }
 }
 
-// Eight columns as they lie in memory, so that a row waits in half the registers
-// (bf16), of which the first m exist (the others read as zero)
-template <class T>
-struct Raw {
-  uint4 v[sizeof(T) / 2];
+// Pieces of 16, 8 and 4 bytes at any address: vector memory takes them unaligned
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1), may_alias));
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1), may_alias));
+typedef uint32_t u32u __attribute__((aligned(1), may_alias));
 
-  __device__ __forceinline__ void load(const T* p, int m, bool vec) {
-    if (vec && m >= 8) {
+// Columns c .. c+7 of a row of `cols` elements as they lie in memory, so that a row
+// waits in half the registers (bf16); those past its end read as zero. Rows of any
+// alignment, since element by element they took twice as long (combination of 3318
+// rows of 2692 bf16, which are on 8 bytes: 16.4 us, so 7.2). WHOLE: rows of whole
+// eights. At the end of others the last eight are read and moved down, which waits
+// for them: kernels are built for both, since a branch between the two makes every
+// load wait (combination of 16384 tokens x 7168: 103 us, 90 without).
+template <class T, bool WHOLE>
+struct Raw {
+  static constexpr int N = sizeof(T) / 2;   // of 16 bytes
+  u32x4u v[N];
+
+  __device__ __forceinline__ void load(const T* row, int c, int cols) {
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
-    } else {
-      uint32_t w[2 * sizeof(T)] = {};
+    for (int i = 0; i < N; ++i) v[i] = u32x4u{0, 0, 0, 0};
+    if (WHOLE ? c < cols : c + 8 <= cols) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < m) {
-          if constexpr (sizeof(T) == 4) w[i] = __builtin_bit_cast(uint32_t, p[i]);
-          else w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (16 * (i & 1));
-        }
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+      for (int i = 0; i < N; ++i) v[i] = reinterpret_cast<const u32x4u*>(row + c)[i];
+    } else if (!WHOLE && c < cols) {
+      end(row, c, cols);
     }
   }
 
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    if constexpr (sizeof(T) == 2) {
-      unpack8(v[0], x);
-    } else {
+  __device__ __forceinline__ void end(const T* row, int c, int cols) {
+    uint32_t w[4 * N] = {};
+    if (cols >= 8) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[4 * i] = __builtin_bit_cast(float, v[i].x);
-        x[4 * i + 1] = __builtin_bit_cast(float, v[i].y);
-        x[4 * i + 2] = __builtin_bit_cast(float, v[i].z);
-        x[4 * i + 3] = __builtin_bit_cast(float, v[i].w);
+      for (int i = 0; i < N; ++i) {
+        const u32x4u x = reinterpret_cast<const u32x4u*>(row + cols - 8)[i];
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+      const int by = c + 8 - cols;   // elements to move: 1 .. 7
+      int steps = by;
+      if constexpr (sizeof(T) == 2) {
+        steps = by >> 1;
+        if (by & 1) {
+#pragma unroll
+          for (int i = 0; i < 4 * N; ++i) w[i] = w[i] >> 16 | (i + 1 < 4 * N ? w[i + 1] << 16 : 0u);
+        }
+      }
+#pragma unroll
+      for (int s = 1; s < 4 * N; s *= 2) {
+        if (steps & s) {
+#pragma unroll
+          for (int i = 0; i < 4 * N; ++i) w[i] = i + s < 4 * N ? w[i + s] : 0u;
+        }
+      }
+    } else {   // c is 0
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < cols) {
+          if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(row[i]);
+          else w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, row[i]) << (16 * (i & 1));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = u32x4u{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+  }
+
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(v[0][i]);
+        x[4 + i] = __uint_as_float(v[N - 1][i]);
+      } else {
+        x[2 * i] = bf16_lo(v[0][i]);
+        x[2 * i + 1] = bf16_hi(v[0][i]);
       }
     }
   }
 };
+
+template <class T>
+__device__ __forceinline__ void get8(const T* row, int c, int cols, float (&x)[8]) {
+  Raw<T, false> r;
+  r.load(row, c, cols);
+  r.get(x);
+}
+
+// Eight columns, of which the first m exist, to a row of any alignment
+template <class T>
+__device__ __forceinline__ void put8(T* p, int m, const float (&x)[8]) {
+  if (m >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 v = pack8(x);
+      *reinterpret_cast<u32x4u*>(p) = u32x4u{v.x, v.y, v.z, v.w};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        reinterpret_cast<u32x4u*>(p)[i] = u32x4u{__builtin_bit_cast(uint32_t, x[4 * i]), __builtin_bit_cast(uint32_t, x[4 * i + 1]),
+                                                 __builtin_bit_cast(uint32_t, x[4 * i + 2]), __builtin_bit_cast(uint32_t, x[4 * i + 3])};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < m) p[i] = (T)x[i];
+  }
+}
 
 // Block scale of values whose largest magnitude has the fp32 bits `amax`
 // (taken as an integer maximum, which carries infinities and NaN along):

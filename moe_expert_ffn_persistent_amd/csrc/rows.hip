@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(256) moe_dispatch_rows_k(const RowsArgs a) {
 // pieces of the row in flight, of the next slot before this one's are added: 160
 // us with one piece and one slot at a time, 90 us so (16384 tokens x 7168, 8
 // slots of which one in the mean is local: 470 MB).
-template <bool BF16, int TPT, int U, bool WEIGHTED>
-__global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, const float* weights, bool vec, int tokens) {
+template <bool BF16, int TPT, int U, bool WEIGHTED, bool WHOLE>
+__global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, const float* weights, int tokens) {
   const int n = blockIdx.x * (256 / TPT) + uni((int)threadIdx.x / TPT), lane = threadIdx.x & 63;
   if (n >= tokens) return;
   const int idx = lane < a.k ? a.index[(size_t)n * a.k + lane] : -1;
@@ -55,25 +55,19 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, cons
   if constexpr (WEIGHTED) weight = lane < a.k ? weights[(size_t)n * a.k + lane] : 0.f;
   char* yrow = static_cast<char*>(a.out) + (size_t)n * a.ld_out;
   for (int c0 = threadIdx.x % TPT * 8; c0 < a.hidden; c0 += U * TPT * 8) {
-    auto load = [&](int slot, uint4 (&v)[U]) {
+    auto load = [&](int slot, Raw<__bf16, WHOLE> (&v)[U]) {
       const int r = __builtin_amdgcn_readlane(idx, slot);
       const __bf16* row = reinterpret_cast<const __bf16*>(static_cast<const char*>(a.in) + (size_t)r * a.ld_in);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * TPT * 8, m = a.hidden - c;
+        const int c = c0 + u * TPT * 8;
         if (u && uni(c) >= a.hidden) break;   // no lane of this wavefront has any
-        if (vec && m >= 8) {
-          v[u] = *reinterpret_cast<const uint4*>(row + c);
-        } else {
-          float x[8];
-          load8(row + c, m, false, x);
-          v[u] = pack8(x);   // exact: they are bf16
-        }
+        v[u].load(row, c, a.hidden);
       }
     };
     float s[U][8] = {};
     uint64_t left = local;
-    uint4 v[2][U];
+    Raw<__bf16, WHOLE> v[2][U];
     if (left) load(__builtin_ctzll(left), v[0]);
     while (left) {
       float w = 1.f;
@@ -84,7 +78,7 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, cons
       for (int u = 0; u < U; ++u) {
         if (u && uni(c0 + u * TPT * 8) >= a.hidden) break;
         float x[8];
-        unpack8(v[0][u], x);
+        v[0][u].get(x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[u][i] = WEIGHTED ? __builtin_fmaf(w, x[i], s[u][i]) : s[u][i] + x[i];
         v[0][u] = v[1][u];
@@ -94,20 +88,9 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, cons
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
       if (u && uni(c) >= a.hidden) break;
-      const bool whole = vec && m == 8;
-      if constexpr (BF16) {
-        if (m > 0) store8(reinterpret_cast<__bf16*>(yrow) + c, m, whole, s[u]);
-      } else {
-        float* y = reinterpret_cast<float*>(yrow) + c;
-        if (whole) {
-          reinterpret_cast<float4*>(y)[0] = float4{s[u][0], s[u][1], s[u][2], s[u][3]};
-          reinterpret_cast<float4*>(y)[1] = float4{s[u][4], s[u][5], s[u][6], s[u][7]};
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < m) y[i] = s[u][i];
-        }
-      }
+      if (m <= 0) continue;
+      if constexpr (BF16) put8(reinterpret_cast<__bf16*>(yrow) + c, m, s[u]);
+      else put8(reinterpret_cast<float*>(yrow) + c, m, s[u]);
     }
   }
 }
@@ -119,7 +102,7 @@ __global__ void __launch_bounds__(256) moe_combine_rows_k(const RowsArgs a, cons
 // threads read the rest of it again, from the caches), and a slot's dot product
 // is joined over the lanes and, through LDS, over the wavefronts, in an order
 // that sizes settle.
-template <class D, int TPT, int U>
+template <class D, int TPT, int U, bool WHOLE>
 __global__ void __launch_bounds__(256) moe_combine_backward_k(const CombineBackwardArgs a) {
   __shared__ float part[4][16];
   const int sub = uni((int)threadIdx.x / TPT), n = blockIdx.x * (256 / TPT) + sub, lane = threadIdx.x & 63;
@@ -131,15 +114,11 @@ __global__ void __launch_bounds__(256) moe_combine_backward_k(const CombineBackw
   if (local) {
     const D* dy = static_cast<const D*>(a.dy) + (size_t)n * a.ld_dy;
     const int t0 = threadIdx.x % TPT * 8;
-    Raw<D> d[U];
-    Raw<__bf16> x[2][U];
+    Raw<D, WHOLE> d[U];
+    Raw<__bf16, WHOLE> x[2][U];
     auto load = [&](auto& to, const auto* row, int c0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * TPT * 8, m = min(8, a.hidden - c);
-        to[u] = {};
-        if (m > 0) to[u].load(row + c, m, a.vec);
-      }
+      for (int u = 0; u < U; ++u) to[u].load(row, c0 + u * TPT * 8, a.hidden);
     };
     auto row_of = [&](int slot) { return static_cast<const __bf16*>(a.rows) + (size_t)__builtin_amdgcn_readlane(idx, slot) * a.ld_rows; };
     load(x[0], row_of(__builtin_ctzll(local)), t0);
@@ -167,7 +146,7 @@ __global__ void __launch_bounds__(256) moe_combine_backward_k(const CombineBackw
             dot = __builtin_fmaf(g[i], z[i], dot);
             g[i] *= w;
           }
-          if (m > 0) store8(drow + c, m, a.vec && m == 8, g);
+          if (m > 0) put8(drow + c, m, g);
         }
       }
 #pragma unroll
@@ -212,18 +191,21 @@ hipError_t launch_dispatch_rows(const RowsArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_combine_rows(const RowsArgs& a, const float* weights, bool bf16_out, hipStream_t s) {
-  const bool vec = (((uintptr_t)a.in | (uintptr_t)a.out | (uintptr_t)a.ld_in | (uintptr_t)a.ld_out) % 16) == 0;
   const int tokens = (int)(a.pairs / a.k);
   auto run = [&](auto tpt, auto pieces) {
     constexpr int T = decltype(tpt)::value, U = decltype(pieces)::value;
     const int grid = (tokens + 256 / T - 1) / (256 / T);
-    if (weights) {
-      if (bf16_out) moe_combine_rows_k<true, T, U, true><<<grid, 256, 0, s>>>(a, weights, vec, tokens);
-      else moe_combine_rows_k<false, T, U, true><<<grid, 256, 0, s>>>(a, weights, vec, tokens);
-    } else {
-      if (bf16_out) moe_combine_rows_k<true, T, U, false><<<grid, 256, 0, s>>>(a, nullptr, vec, tokens);
-      else moe_combine_rows_k<false, T, U, false><<<grid, 256, 0, s>>>(a, nullptr, vec, tokens);
-    }
+    auto go = [&](auto bf16, auto whole) {
+      constexpr bool B = decltype(bf16)::value, W = decltype(whole)::value;
+      if (weights) moe_combine_rows_k<B, T, U, true, W><<<grid, 256, 0, s>>>(a, weights, tokens);
+      else moe_combine_rows_k<B, T, U, false, W><<<grid, 256, 0, s>>>(a, nullptr, tokens);
+    };
+    auto type = [&](auto whole) {
+      if (bf16_out) go(std::true_type{}, whole);
+      else go(std::false_type{}, whole);
+    };
+    if (a.hidden % 8 == 0) type(std::true_type{});
+    else type(std::false_type{});
     return hipGetLastError();
   };
   using std::integral_constant;
@@ -244,8 +226,13 @@ hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t s) 
   auto run = [&](auto tpt, auto pieces) {
     constexpr int T = decltype(tpt)::value, U = decltype(pieces)::value;
     const int grid = (a.tokens + 256 / T - 1) / (256 / T);
-    if (a.dy_fp32) moe_combine_backward_k<float, T, U><<<grid, 256, 0, s>>>(a);
-    else moe_combine_backward_k<__bf16, T, U><<<grid, 256, 0, s>>>(a);
+    auto go = [&](auto whole) {
+      constexpr bool W = decltype(whole)::value;
+      if (a.dy_fp32) moe_combine_backward_k<float, T, U, W><<<grid, 256, 0, s>>>(a);
+      else moe_combine_backward_k<__bf16, T, U, W><<<grid, 256, 0, s>>>(a);
+    };
+    if (a.hidden % 8 == 0) go(std::true_type{});
+    else go(std::false_type{});
     return hipGetLastError();
   };
   using std::integral_constant;

@@ -112,7 +112,7 @@ __device__ __forceinline__ int chunk_in(int r, int p) {
   }
 }
 
-template <class C>
+template <class C, bool EVEN>
 struct TileM {
   const char *fbase, *tbase, *wsbase, *xsbase;
   uint32_t fv[C::NIF], tv[C::NIT];
@@ -177,25 +177,22 @@ struct TileM {
     });
   }
 
-  // 16 bytes at `src` of which `n` e4m3 bytes (PACKED: e2m1 codes) exist
+  // 16 bytes at `src` of which `n` e4m3 bytes (PACKED: e2m1 codes) exist; a short loop,
+  // since a longer body slows every short call by its size (unrolled over words: 1 x 7170
+  // x 4096 8.6 to 9.6 us)
   template <bool PACKED>
   __device__ __forceinline__ static uint4 partial(const char* src, int n) {
+    uint64_t v[2] = {0, 0};
     const int bytes = PACKED ? (n + 1) / 2 : n;
-    uint32_t v[4];
-    // whole words, then the bytes behind them: all on their way at once
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = 4 * i + 4 <= bytes ? reinterpret_cast<const uint32_t*>(src)[i] : 0u;
-    uint32_t last = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if ((bytes & ~3) + i < bytes) last |= (uint32_t)(uint8_t)src[(bytes & ~3) + i] << (8 * i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i == bytes / 4) v[i] = last;
-      // an odd row's last byte holds one code
-      if (PACKED && (n & 1) && i == (bytes - 1) / 4) v[i] &= ~(0xf0u << (8 * ((bytes - 1) & 3)));
+#pragma unroll 1
+    for (int b = 0; b < bytes; ++b) {
+      uint64_t x = (uint8_t)src[b];
+      if (PACKED && 2 * b + 1 == n) x &= 0x0f;
+      x <<= 8 * (b & 7);
+      if (b < 8) v[0] |= x;
+      else v[1] |= x;
     }
-    return uint4{v[0], v[1], v[2], v[3]};
+    return uint4{(uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32)};
   }
 
   template <int copy>
@@ -323,7 +320,7 @@ struct TileM {
     each<C::NG>([&](auto i) { issue_group<i>(0, (uint32_t)(uintptr_t)lds); });
     if (k >= C::KS) {
       each<C::NI>([&](auto i) { issue<i>(0, (uint32_t)(uintptr_t)lds); });
-    } else {
+    } else if constexpr (!EVEN) {
       issue_tail(0, k, lds);
     }
   }
@@ -337,7 +334,7 @@ struct TileM {
 #pragma unroll
       for (int j = 0; j < C::TB; ++j) acc[i][j] = f32x4{};
     const uint32_t ring = (uint32_t)(uintptr_t)lds;
-    const int full = k / C::KS, left = k % C::KS, nk = full + (left != 0);
+    const int full = k / C::KS, left = EVEN ? 0 : k % C::KS, nk = full + (left != 0);
     // without stores since the first stage's copies (fresh) all stages are on
     // their way at once, and counted below
     if (!fresh) wait_first(stores);
@@ -351,8 +348,8 @@ struct TileM {
         if (s < nk) issue_scales(s, ring);
         if (s < full) {
           each<NI>([&](auto i) { issue<i>(s, ring + s * C::STAGE); });
-        } else if (s < nk) {
-          issue_tail(s, left, lds);
+        } else if constexpr (!EVEN) {
+          if (s < nk) issue_tail(s, left, lds);
         }
       }
     }
@@ -372,9 +369,11 @@ struct TileM {
       } else if (left) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       else vm_wait_ahead<NI, C::NS - 2>(nk - 1 - s);
       if constexpr (C::KW == 1) lds_barrier();
-      if (left && s + C::NS - 1 == full) {
-        issue_scales(full, ring);
-        issue_tail(full, left, lds);
+      if constexpr (!EVEN) {
+        if (left && s + C::NS - 1 == full) {
+          issue_scales(full, ring);
+          issue_tail(full, left, lds);
+        }
       }
       compute<false, NTP>(lds, s, lds + slot * C::STAGE, wf, wt, 0);
       slot = slot + 1 == C::NS ? 0 : slot + 1;
@@ -512,8 +511,10 @@ struct Work {
   char* out;
 };
 
-// Workgroups walk the tiles as the bf16 kernel's do.
-template <class C>
+// Workgroups walk the tiles as the bf16 kernel's do. EVEN: the sum is whole stages
+// long; short calls take longer by the size of the code that ends it otherwise (1 x 7168
+// x 4096 W4A8: 5 KB 6.5 us, 18 KB 7.5), so it is built for tiles of few rows.
+template <class C, bool EVEN>
 __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_gemm_mx(const GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   const int wave = uni((int)(threadIdx.x >> 6)), kw = C::KW == 1 ? 0 : wave;
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
   const GroupScan<C::TM> scan(a.row_offset, grouped ? a.L : 0, a.rows);
   const int ti = grouped ? scan.total : (a.rows + C::TM - 1) / C::TM;
   const int tiles = ti * tj, total = tiles * a.splits;
-  TileM<C> g;
+  TileM<C, EVEN> g;
 
   auto start = [&](int b, Work& wk) {
     int tile = xcd_tile(b, total);
@@ -564,26 +565,29 @@ __global__ void __launch_bounds__(C::THREADS, (C::THREADS / 256) * C::OCC) moe_g
     return true;
   };
 
-  Work cur, next;
+  Work cur;
   int b = blockIdx.x;
-  int stores = 0;   // of the previous tile, possibly in flight
-  bool more = start(b, cur), fresh = true;
-  while (more) {
-    g.multiply(ring, cur.ni - cur.i0, wf, wt, stores, fresh);
-    fresh = C::KW > 1;   // split wavefronts store before they copy
-    stores = 0;
-    b += gridDim.x;
-    if constexpr (C::KW == 1) {
+  if constexpr (C::KW > 1) {   // the next tile's copies wait for the stores: the rings hold the sums
+    for (; start(b, cur); b += gridDim.x) {
+      g.multiply(ring, cur.ni - cur.i0, wf, wt, 0, true);
+      g.store_split(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, kw, a.out_bf16, a.vec_out);
+      __syncthreads();   // the joined sums are read
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  } else {
+    Work next;
+    int stores = 0;   // of the previous tile, possibly in flight
+    bool more = start(b, cur), fresh = true;
+    while (more) {
+      g.multiply(ring, cur.ni - cur.i0, wf, wt, stores, fresh);
+      fresh = false;
+      b += gridDim.x;
       lds_barrier();   // every wavefront is done with the ring
       more = start(b, next);
       stores = g.write(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, wf, wt, a.out_bf16, a.vec_out);
-    } else {
-      g.store_split(lds, cur.out, a.ld_y, cur.i0, cur.ni, cur.j0, a.n, kw, a.out_bf16, a.vec_out);
-      __syncthreads();   // the joined sums are read
-      more = start(b, next);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      cur = next;
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    cur = next;
   }
 }
 
@@ -609,7 +613,13 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
   const long long tiles = nj * mi * a.splits;
   if (tiles >= INT_MAX / 2) return launch_gemm_mx_any(a, s);   // the kernel counts tiles in int
   const long long grid = tiles > kCus ? kCus * C::OCC : (tiles + 7) / 8 * 8;
-  moe_gemm_mx<C><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
+  if constexpr (C::TM <= 32) {
+    if (a.k % C::KS == 0) {
+      moe_gemm_mx<C, true><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  moe_gemm_mx<C, false><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -654,9 +654,9 @@ constexpr GemmTile timed(double a, double c, double b, double o, bool once = fal
 
 const GemmTile kMxTiles[2][kMxGemmTiles] = {
     {timed<Large<false>>(0.36, 1.33, 1.33, 7.1), timed<Wide<false>>(0.47, 1.05, 1.05, 6.4), timed<Medium<false>>(0.49, 0.74, 0.74, 5.9),
-     GemmTile{}, timed<Deep<false>>(0.31, 0.43, 0.43, 5.0, true), timed<Split>(0.35, 0.35, 0.35, 4.0),
-     timed<Split64<false>>(0.39, 0.39, 0.39, 4.6), timed<Few<false>>(0.127, 0.127, 0.127, 4.55), timed<Thin<false>>(0.185, 0.23, 0.138, 4.5),
-     timed<Thin16>(0.16, 0.21, 0.11, 4.36)},
+     GemmTile{}, timed<Deep<false>>(0.31, 0.43, 0.43, 5.0, true), timed<Split>(0.405, 0.405, 0.405, 4.03),
+     timed<Split64<false>>(0.45, 0.45, 0.45, 4.09), timed<Few<false>>(0.214, 0.214, 0.214, 4.17), timed<Thin<false>>(0.177, 0.25, 0.206, 4.37),
+     timed<Thin16>(0.169, 0.20, 0.134, 4.08)},
     {timed<Large<true>>(0.55, 1.89, 1.89, 6.6), timed<Wide<true>>(0.73, 1.51, 1.51, 6.1), timed<Medium<true>>(0.58, 1.08, 1.08, 5.6),
      timed<Small>(0.31, 0.44, 0.36, 4.76), timed<Deep<true>>(0.29, 0.55, 0.55, 5.5, true), GemmTile{},
      timed<Split64<true>>(0.59, 0.59, 0.59, 4.1), timed<Few<true>>(0.455, 0.455, 0.455, 4.1), timed<Thin<true>>(0.33, 0.50, 0.26, 4.4),

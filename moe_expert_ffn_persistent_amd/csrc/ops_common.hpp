@@ -169,9 +169,10 @@ typedef uint32_t u32u __attribute__((aligned(1), may_alias));
 // waits in half the registers (bf16); those past its end read as zero. Rows of any
 // alignment, since element by element they took twice as long (combination of 3318
 // rows of 2692 bf16, which are on 8 bytes: 16.4 us, so 7.2). WHOLE: rows of whole
-// eights. At the end of others the last eight are read and moved down, which waits
-// for them: kernels are built for both, since a branch between the two makes every
-// load wait (combination of 16384 tokens x 7168: 103 us, 90 without).
+// eights. The end of others is read in pieces, and of no element twice: a call that
+// writes over its input may have written what other lanes hold. Kernels are built for
+// both, since a branch between the two makes every load wait (combination of 16384
+// tokens x 7168: 103 us, 90 without).
 template <class T, bool WHOLE>
 struct Raw {
   static constexpr int N = sizeof(T) / 2;   // of 16 bytes
@@ -188,40 +189,47 @@ struct Raw {
     }
   }
 
+  // the 1 to 7 elements from c on, as a four, a two and a one
   __device__ __forceinline__ void end(const T* row, int c, int cols) {
+    const int n = cols - c;
+    const T* p = row + c;
     uint32_t w[4 * N] = {};
-    if (cols >= 8) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const u32x4u x = reinterpret_cast<const u32x4u*>(row + cols - 8)[i];
-        w[4 * i] = x.x;
-        w[4 * i + 1] = x.y;
-        w[4 * i + 2] = x.z;
-        w[4 * i + 3] = x.w;
+    if constexpr (sizeof(T) == 4) {
+      if (n & 4) {
+        const u32x4u x = *reinterpret_cast<const u32x4u*>(p);
+        w[0] = x.x;
+        w[1] = x.y;
+        w[2] = x.z;
+        w[3] = x.w;
       }
-      const int by = c + 8 - cols;   // elements to move: 1 .. 7
-      int steps = by;
-      if constexpr (sizeof(T) == 2) {
-        steps = by >> 1;
-        if (by & 1) {
-#pragma unroll
-          for (int i = 0; i < 4 * N; ++i) w[i] = w[i] >> 16 | (i + 1 < 4 * N ? w[i + 1] << 16 : 0u);
-        }
+      if (n & 2) {
+        const u32x2u x = *reinterpret_cast<const u32x2u*>(p + (n & 4));
+        if (n & 4) w[4] = x.x, w[5] = x.y;
+        else w[0] = x.x, w[1] = x.y;
       }
+      if (n & 1) {
+        const uint32_t x = __float_as_uint(p[n & 6]);
 #pragma unroll
-      for (int s = 1; s < 4 * N; s *= 2) {
-        if (steps & s) {
-#pragma unroll
-          for (int i = 0; i < 4 * N; ++i) w[i] = i + s < 4 * N ? w[i + s] : 0u;
-        }
+        for (int i = 0; i < 8; i += 2)
+          if (i == (n & 6)) w[i] = x;
       }
-    } else {   // c is 0
+    } else {
+      if (n & 4) {
+        const u32x2u x = *reinterpret_cast<const u32x2u*>(p);
+        w[0] = x.x;
+        w[1] = x.y;
+      }
+      if (n & 2) {
+        const uint32_t x = *reinterpret_cast<const u32u*>(p + (n & 4));
+        if (n & 4) w[2] = x;
+        else w[0] = x;
+      }
+      if (n & 1) {
+        const uint32_t x = __builtin_bit_cast(uint16_t, p[n & 6]);
 #pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (i < cols) {
-          if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(row[i]);
-          else w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, row[i]) << (16 * (i & 1));
-        }
+        for (int i = 0; i < 4; ++i)
+          if (i == (n & 6) / 2) w[i] = x;
+      }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = u32x4u{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};

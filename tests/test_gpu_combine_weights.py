@@ -85,6 +85,20 @@ def test_weighted_combine_backward(N, k, E, L, H, dy_dtype):
     assert over is both and torch.equal(over[up(r)], got[up(r)]) and torch.equal(dwo, dw)
 
 
+@pytest.mark.parametrize("N", [40, 1200])
+@pytest.mark.parametrize("H", [515, 1027, 2051, 4099, 8195])
+def test_rows_whose_end_is_a_wavefronts_first_piece_in_place(H, N):
+    # a wavefront may be done with its part of the row before another has read the end of it
+    rows, weights, pair_row, here, dy = case(N, 2, 8, 8, H)
+    weights = torch.nan_to_num(weights)
+    out = up(torch.zeros_like(rows))
+    want, dw = moe.combine_rows_backward(up(dy), up(rows), up(pair_row), up(weights), out=out)
+    both = up(rows)
+    got, dwo = moe.combine_rows_backward(up(dy), both, up(pair_row), up(weights), out=both)
+    r = up(pair_row.long()[here.view(-1)])
+    assert torch.equal(got[r], want[r]) and torch.equal(dwo, dw)
+
+
 def test_infinities_stay_in_their_rows():
     N, k, H = 6, 2, 72
     rows, weights, dy = normal(gen(1), 12, H), torch.rand(N, k, generator=gen(2)), normal(gen(3), N, H)

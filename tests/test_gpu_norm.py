@@ -116,6 +116,26 @@ def test_in_place_and_rows_apart():
     assert torch.equal(moe.rms_norm(d, out=d), want)
 
 
+@pytest.mark.parametrize("H", [515, 1027, 2051, 4099, 8195, 16387, 33283])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_rows_whose_end_is_a_wavefronts_first_piece_in_place(dtype, H):
+    # a wavefront may be done with its part of the row before another has read the end of it
+    R = 600 if H < 16000 else 60
+    x, res, w, g = inputs(R, H, dtype, H)
+    dy, dx, dr = up(normal(g, R, H, dtype=dtype)), up(x), up(res)
+    say(f"in place {R} x {H} {dtype}")
+    y, s = moe.rms_norm(up(x), up(w), residual=dr)
+    got, stream = moe.rms_norm(dx, up(w), residual=dr, residual_out=dx)
+    assert torch.equal(got, y) and torch.equal(stream, s)
+    want, dw = moe.rms_norm_backward(dy, s, up(w), dresidual=dr)
+    for over in (0, 1, 2):
+        t = [dy.clone(), s.clone(), dr.clone()]
+        got, dwo = moe.rms_norm_backward(t[0], t[1], up(w), dresidual=t[2], out=t[over])
+        assert torch.equal(got, want) and torch.equal(dwo, dw)
+    d = s.clone()
+    assert torch.equal(moe.rms_norm(d, up(w), out=d, out_dtype=dtype), moe.rms_norm(s, up(w), out_dtype=dtype))
+
+
 def test_zero_infinite_and_large_rows():
     H = 264
     x = normal(gen(9), 6, H, dtype=F32)

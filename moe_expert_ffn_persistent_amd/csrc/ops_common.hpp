@@ -168,7 +168,7 @@ typedef uint32_t u32u __attribute__((aligned(1), may_alias));
 // Columns c .. c+7 of a row of `cols` elements as they lie in memory, so that a row
 // waits in half the registers (bf16); those past its end read as zero. Rows of any
 // alignment, since element by element they took twice as long (combination of 3318
-// rows of 2692 bf16, which are on 8 bytes: 16.4 us, so 7.2). WHOLE: rows of whole
+// rows of 2692 bf16, which are on 8 bytes: 16.4 us, so 6.5). WHOLE: rows of whole
 // eights. The end of others is read in pieces, and of no element twice: a call that
 // writes over its input may have written what other lanes hold. Kernels are built for
 // both, since a branch between the two makes every load wait (combination of 16384

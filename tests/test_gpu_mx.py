@@ -216,6 +216,14 @@ def test_mx_strides_and_alignment(counts, R, K, n, pad, lead, element):
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("pad,lead", [(3, 0), (5, 3)])
+@pytest.mark.parametrize("element", FORMATS)
+@pytest.mark.parametrize("counts,R,K,n", [([300, 0, 249, 150, 1], 700, 206, 2601), (None, 700, 384, 2600), (None, 513, 34, 3001)], ids=["grouped", "dense", "short"])
+def test_many_rows_of_any_alignment(counts, R, K, n, pad, lead, element, out_dtype):
+    run_mx(counts, R, K, n, element, out_dtype, pad=pad, lead=lead, behind=3 if counts else 0)
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("tile", range(1, 11))
 @pytest.mark.parametrize("element", FORMATS)
 @pytest.mark.parametrize("counts,R,K,n", [([0, 33, 290, 1], 324, 272, 328), (None, 300, 64, 8), ([3, 0, 200], 203, 34, 65),

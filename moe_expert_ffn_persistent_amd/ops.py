@@ -308,11 +308,14 @@ def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
     """Rows of the local experts: ``out[r] = x[row_pair[r] // top_k]`` for r in
     row_offset[0] .. row_offset[L]-1 (a layout's arrays). x [N, H] of 1-, 2- or
     4-byte elements; out [rows, H], allocated with one row for every entry of
-    row_pair when not given. The gradient of combine_rows."""
+    row_pair when not given: back to back, or as far apart as those of x where
+    these are bytes with less than 16 of padding (MX codes and scales, which
+    mx_matmul's tile kernels take so). The gradient of combine_rows."""
     if out is None:
         _, H = _sizes(x, "x", 2)
         _indices(row_pair, "row_pair")
-        out = _empty((row_pair.numel(), H), x.dtype, x.device, stream)
+        apart = x.stride(0) if x.element_size() == 1 and 0 < x.stride(0) - H < 16 else H
+        out = _empty((row_pair.numel(), apart), x.dtype, x.device, stream)[:, :H]
     _call("moe_dispatch_rows", check_dispatch_inputs, (x, row_pair, row_offset, top_k, out), (top_k,),
           (x, row_pair, row_offset, out), 0b1000, stream)
     return out

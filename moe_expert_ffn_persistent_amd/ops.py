@@ -321,7 +321,7 @@ def dispatch_rows(x, row_pair, row_offset, top_k, out=None, stream=None):
     return out
 
 
-class _MoreTokens(Exception):
+class _MoreTokens(ValueError):
     """Inputs that are in order but for more tokens than one call takes."""
 
 
@@ -390,8 +390,9 @@ def check_combine_backward_inputs(dy, rows, pair_row, weights, drows, dweights):
     if rows.shape[1] != H or drows.shape != rows.shape:
         raise ValueError(f"shapes do not fit: dy {tuple(dy.shape)}, rows {tuple(rows.shape)}, out {tuple(drows.shape)}")
     _at_most(rows.shape[0], "rows", _MAX_ROWS)
-    _at_most(N, "tokens", _MAX_TOKENS)
     _on(dy.device, ("dy", dy), ("rows", rows), ("pair_row", pair_row), ("weights", weights), ("out", drows), ("dweights", dweights))
+    if N > _MAX_TOKENS:
+        raise _MoreTokens
     return MoeCombineBackwardParams(N, rows.shape[0], k, H, _OUT[dy.dtype], ldy, ldr, ldd)
 
 
@@ -401,13 +402,20 @@ def combine_rows_backward(dy, rows, pair_row, weights, out=None, dweights=None, 
     weights[n, j] * dy[n]`` and ``dweights[n, j] = dy[n] . rows[pair_row[n, j]]``,
     0 for slots whose pair_row is negative (or no row). Rows that no slot names
     keep what ``out`` held. Each row belongs to one slot, as in a layout. ``out``
-    may be rows itself. At most 2^23 tokens."""
+    may be rows itself."""
     if out is None:
         out = _empty(_sizes(rows, "rows", 2), torch.bfloat16, rows.device, stream)
     if dweights is None:
         dweights = _empty(_sizes(weights, "weights", 2), torch.float32, weights.device, stream)
-    _call("moe_combine_rows_backward", check_combine_backward_inputs, (dy, rows, pair_row, weights, out, dweights), (),
-          (dy, rows, pair_row, weights, out, dweights), 0b110000, stream)
+    try:
+        _call("moe_combine_rows_backward", check_combine_backward_inputs, (dy, rows, pair_row, weights, out, dweights), (),
+              (dy, rows, pair_row, weights, out, dweights), 0b110000, stream)
+    except _MoreTokens:   # a row has one slot, so it is read and written by one piece
+        pairs, k = pair_row.view(-1), weights.shape[1]
+        for n in range(0, dy.shape[0], _MAX_TOKENS):
+            some = slice(n, n + _MAX_TOKENS)
+            combine_rows_backward(dy[some], rows, pairs[n * k:(n + _MAX_TOKENS) * k], weights[some], out=out, dweights=dweights[some],
+                                  stream=stream)
     return out, dweights
 
 

@@ -520,7 +520,8 @@ int32_t moe_grouped_matmul(const moe_grouped_params* p, const int32_t* row_offse
  * long sum may add up ranges of the sum side by side, in fp32, and join them in
  * their order: results do not depend on timing. moe_grouped_workspace_bytes
  * says what it takes to do so, 0 where the call gains nothing; with less it is
- * cut into fewer ranges or none (workspace NULL: none). */
+ * cut into fewer ranges or none (workspace NULL: none). Ranges asked for that
+ * make 2^30 output tiles or more are MOE_ERR_UNSUPPORTED. */
 int64_t moe_grouped_workspace_bytes(const moe_grouped_params* p);
 int32_t moe_grouped_matmul_split(const moe_grouped_params* p, const int32_t* row_offset, void* x, void* w,
                                  void* y, void* workspace, void* stream);

@@ -19,7 +19,6 @@
 // per stage. A ragged end (the last c of a row, or of an expert's rows in
 // wgrad) is zeros in LDS: lanes past the end write a zero instead of copying.
 // Rows i past an expert's end repeat its last row and are not stored.
-#include <climits>
 
 #include "internal.hpp"
 #include "ops_common.hpp"
@@ -515,11 +514,8 @@ constexpr GemmTile timed(double a, double c, double b, double o, bool once = fal
 
 template <class C, int OP>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
-  const long long nj = ((OP == MOE_GROUPED_FORWARD ? a.n : a.k) + C::TN - 1) / C::TN;
-  const long long mi = OP == MOE_GROUPED_WGRAD ? (long long)a.L * ((a.n + C::TM - 1) / C::TM)
-                                               : ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM;
-  const long long tiles = nj * mi * a.splits;
-  if (tiles >= INT_MAX / 2) return launch_gemm_any(a, false, s);   // the kernel counts tiles in int
+  const long long tiles = gemm_tiles(a, C::TM, C::TN);
+  if (tiles >= kMostTiles) return launch_gemm_any(a, false, s);   // only whole sums (ops_api.cpp)
   // A workgroup for each place on the GPU; a multiple of 8 keeps one on its XCD.
   // Past a tile for every compute unit all places get one, since the tile order
   // is dealt in runs: with a workgroup for each of 288 to 320 tiles, places for

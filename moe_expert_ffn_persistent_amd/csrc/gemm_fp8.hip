@@ -22,7 +22,6 @@
 // scales come along as four-byte copies, and the weight scales by a wavefront
 // that has no rows left to fetch scales for (a load to registers would wait for
 // every copy and store in flight). A ragged last block is zeros in LDS.
-#include <climits>
 
 #include "internal.hpp"
 #include "ops_common.hpp"
@@ -453,10 +452,8 @@ constexpr GemmTile timed(double a, double c, double b, double o, bool once = fal
 
 template <class C>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
-  const long long nj = (a.n + C::TN - 1) / C::TN;
-  const long long mi = a.row_offset ? ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM : (a.rows + C::TM - 1) / C::TM;
-  const long long tiles = nj * mi * a.splits;
-  if (tiles >= INT_MAX / 2) return launch_gemm_any(a, true, s);   // the kernel counts tiles in int
+  const long long tiles = gemm_tiles(a, C::TM, C::TN);
+  if (tiles >= kMostTiles) return launch_gemm_any(a, true, s);   // only whole sums (ops_api.cpp)
   const long long grid = tiles > kCus ? kCus * C::OCC : (tiles + 7) / 8 * 8;
   moe_gemm_fp8<C><<<(unsigned)grid, C::THREADS, 0, s>>>(a);
   return hipGetLastError();

@@ -18,7 +18,6 @@
 // copy then touches 16 rows. Copied with each stage, 128 k of 64 rows at a time,
 // their scattered lines were the kernel's bound (8192 x 7168 x 4096 e4m3 203 us
 // where the same copies from one line took 169, e2m1 145 and 108).
-#include <climits>
 #include <type_traits>
 #include <utility>
 
@@ -608,10 +607,8 @@ using Thin16 = CfgM<false, 2, 16, 128, 1, 4, 3, 4, 2, 4>;                       
 
 template <class C>
 hipError_t launch(const GemmArgs& a, hipStream_t s) {
-  const long long nj = (a.n + C::TN - 1) / C::TN;
-  const long long mi = a.row_offset ? ((long long)a.rows + (long long)a.L * (C::TM - 1)) / C::TM : (a.rows + C::TM - 1) / C::TM;
-  const long long tiles = nj * mi * a.splits;
-  if (tiles >= INT_MAX / 2) return launch_gemm_mx_any(a, s);   // the kernel counts tiles in int
+  const long long tiles = gemm_tiles(a, C::TM, C::TN);
+  if (tiles >= kMostTiles) return launch_gemm_mx_any(a, s);   // only whole sums (ops_api.cpp)
   const long long grid = tiles > kCus ? kCus * C::OCC : (tiles + 7) / 8 * 8;
   if constexpr (C::TM <= 32) {
     if (a.k % C::KS == 0) {

@@ -220,6 +220,15 @@ struct GemmTile {
   bool once;             // only for calls that give no compute unit a second tile
 };
 extern const GemmTile kBf16GemmTileTable[], kDgradTiles[], kWgradTiles[], kFp8GemmTileTable[];   // id - 1
+// Most output tiles of tm x tn that a call has, over all ranges of its sum. The tile
+// kernels count them in int, and the kernels of any size, which take over from
+// kMostTiles on, add up no ranges.
+constexpr long long kMostTiles = 1ll << 30;
+inline long long gemm_tiles(const GemmArgs& a, int tm, int tn) {
+  const long long nj = ((a.op == MOE_GROUPED_FORWARD ? a.n : a.k) + tn - 1) / tn;
+  const long long mi = a.op == MOE_GROUPED_WGRAD ? (long long)a.L * ((a.n + tm - 1) / tm) : (a.rows + (long long)a.L * (tm - 1)) / tm;
+  return nj * mi * a.splits;
+}
 // The same call with its sum cut into a.splits ranges, written to `ws` (fp32, one
 // output's elements a range), and the joining of them into a's output
 GemmArgs split_args(const GemmArgs& a, float* ws);

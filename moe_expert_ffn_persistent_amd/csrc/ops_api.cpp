@@ -120,10 +120,11 @@ bool split_ok(int32_t splits, int64_t bytes) { return splits >= 0 && splits <= k
 
 // One product: whole, or in ranges joined afterwards
 template <class Launch>
-int32_t run(const GemmArgs& a, Choice c, float* ws, hipStream_t s, Launch launch) {
+int32_t run(const GemmTile* tiles, const GemmArgs& a, Choice c, float* ws, hipStream_t s, Launch launch) {
   if (c.splits == 1) return done(launch(c.tile, a, s));
   GemmArgs b = a;
   b.splits = c.splits;
+  if (gemm_tiles(b, tiles[c.tile - 1].tm, tiles[c.tile - 1].tn) >= kMostTiles) return MOE_ERR_UNSUPPORTED;
   b.vec_out = true;   // the workspace's rows
   const hipError_t e = launch(c.tile, split_args(b, ws), s);
   return e != hipSuccess ? done(e) : done(launch_join_splits(b, ws, s));
@@ -197,7 +198,7 @@ int32_t grouped(const moe_grouped_params* p, const int32_t* row_offset, void* x,
   if (!fast) return done(launch_gemm_any(a, false, stream));
   const long long room = workspace ? bytes / 4 : 0;
   if (splits > 1 && splits * split_args(a, nullptr).part > room) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  return run(a, choose(grouped_tiles(p), kBf16GemmTiles, a, 64, 2, p->tile, splits, room), static_cast<float*>(workspace),
+  return run(grouped_tiles(p), a, choose(grouped_tiles(p), kBf16GemmTiles, a, 64, 2, p->tile, splits, room), static_cast<float*>(workspace),
              stream, launch_gemm_bf16);
 }
 
@@ -252,7 +253,7 @@ int32_t fp8(const moe_fp8_params* p, const int32_t* row_offset, const void* x, c
   if (!fast) return done(launch_gemm_any(a, true, stream));
   const long long room = workspace ? bytes / 4 : 0;
   if (splits > 1 && splits * split_args(a, nullptr).part > room) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  return run(a, choose(kFp8GemmTileTable, kFp8GemmTiles, a, 128, 1, p->tile, splits, room), static_cast<float*>(workspace),
+  return run(kFp8GemmTileTable, a, choose(kFp8GemmTileTable, kFp8GemmTiles, a, 128, 1, p->tile, splits, room), static_cast<float*>(workspace),
              stream, launch_gemm_fp8);
 }
 
@@ -472,7 +473,7 @@ int32_t moe_mx_matmul(const moe_mx_params* p, const int32_t* row_offset, const v
   const long long room = workspace && ranges ? p->workspace_bytes / 4 : 0;
   if (p->splits > 1 && !ranges) return MOE_ERR_UNSUPPORTED;
   if (p->splits > 1 && p->splits * split_args(a, nullptr).part > room) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  return run(a, mx_choice(p, a, room), static_cast<float*>(workspace), (hipStream_t)stream, launch_gemm_mx);
+  return run(kMxTiles[a.x_e2m1], a, mx_choice(p, a, room), static_cast<float*>(workspace), (hipStream_t)stream, launch_gemm_mx);
 }
 
 int32_t moe_dispatch_rows(const moe_rows_params* p, const void* x, const int32_t* row_pair,

@@ -25,7 +25,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 import struct
 import warnings
 
@@ -710,7 +709,7 @@ def _mx_blocks(n: int) -> int:
 
 
 def _element(element):
-    if element not in _MX:
+    if not isinstance(element, str) or element not in _MX:
         raise ValueError(f"element: need 'e4m3' or 'e2m1', got {element!r}")
     return _MX[element]
 
@@ -851,11 +850,20 @@ def mx_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=tor
 # ---- RMS norm of the residual stream -------------------------------------------------
 
 @functools.lru_cache(maxsize=64)
+def _fp32_bits(v):
+    return struct.unpack("<i", struct.pack("<f", float(v)))[0]
+
+
 def _bits(eps):
     """The fp32 bits of eps, by which a call is remembered."""
-    if not isinstance(eps, (int, float)) or not 0.0 < ctypes.c_float(eps).value < math.inf:
-        raise ValueError(f"eps: need a positive number, got {eps!r}")
-    return struct.unpack("<i", struct.pack("<f", eps))[0]
+    if isinstance(eps, (int, float)):
+        try:
+            bits = _fp32_bits(eps)
+        except OverflowError:
+            bits = 0
+        if 0 < bits < 0x7f800000:   # above 0 and below infinity, no NaN
+            return bits
+    raise ValueError(f"eps: need a positive number, got {eps!r}")
 
 
 def _eps(bits):

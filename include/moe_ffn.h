@@ -701,7 +701,9 @@ int32_t moe_quantize_mx(const moe_mx_quantize_params* p, const void* x, const in
  *   w [num_experts, n, ceil(k/2) bytes] e2m1, w_scales [num_experts, n,
  *   ceil(k/32)]; y bf16 or fp32 [rows, n]
  * Products and scales are exact and the sums fp32, but for the matrix cores' own
- * addition (see moe_fp8_matmul). A scale of 255 makes NaN of what it scales.
+ * addition (see moe_fp8_matmul). A partial sum past fp32's largest value is
+ * infinite, also where the whole sum would not be, and one below fp32's normal
+ * numbers a multiple of 2^-149. A scale of 255 makes NaN of what it scales.
  * The tile kernels take x, w and their strides in whole 16 bytes and the scales'
  * in whole four (as moe_quantize_mx's outputs are when allocated so), a slower
  * kernel anything else; k and n are any size in both.

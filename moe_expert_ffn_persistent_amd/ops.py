@@ -834,7 +834,8 @@ def mx_matmul(x, x_scales, w, w_scales, row_offset=None, out=None, out_dtype=tor
     ``tile`` and ``splits`` as for grouped_matmul.
 
     Scales are the matrix cores' own and exact; sums are fp32 but for the bits that
-    the matrix cores drop (see fp8_matmul). Operands off their 16 bytes (scales off
+    the matrix cores drop (see fp8_matmul): a partial sum past fp32's largest value
+    is infinite, also where the whole sum would not be. Operands off their 16 bytes (scales off
     four), or with such strides, take a slower kernel; what quantize_mx allocates
     is on them for any k."""
     if out is None:

@@ -1,8 +1,9 @@
 """RMS norm and its gradients with several rows to a workgroup, for every shape in
-which a row is held: one and two pieces a thread, 256, 512 and 1024 threads, rows
-side by side, whole eights and not. Each workgroup then walks its rows with the next
-one on its way and its reduction buffers in turn, which few rows never show. Against
-64 bits, with test_gpu_norm's bars. And tensors of more than 2^31 elements."""
+which a row is held (one and two pieces a thread, 256, 512 and 1024 threads, rows
+side by side, whole eights and not) and for rows past what is held. Each workgroup
+then walks its rows with the next one on its way and its reduction buffers in turn,
+which few rows never show. Against 64 bits, with test_gpu_norm's bars. And tensors
+of more than 2^31 elements."""
 import pytest
 import torch
 
@@ -12,9 +13,9 @@ from test_gpu_operators import BF, F32, gen, normal, say, up
 
 pytestmark = pytest.mark.gpu
 
-# rows, hidden: three times the rows that the largest grid takes at once, or more
+# rows, hidden: more than the largest grid takes at once, mostly twice or three times
 MANY = [(70000, 64), (70001, 61), (20000, 500), (9001, 1000), (5000, 2048), (5001, 2047), (3300, 4096), (3301, 4095), (3100, 7168), (3101, 7167),
-        (1600, 8200), (1601, 8199), (1100, 16384)]
+        (1600, 8200), (1601, 8199), (1100, 16384), (1200, 16500)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])

@@ -49,7 +49,7 @@ _E8M0 = tuple(t for t in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) i
 _NORM = {None: MOE_NORM_BF16, "fp8": MOE_NORM_FP8, "mx_e4m3": MOE_NORM_MX_E4M3, "mx_e2m1": MOE_NORM_MX_E2M1}
 # the C entry points' limits
 _MAX_ROWS, _MAX_COLS, _MAX_STRIDE, _MAX_MATRIX = 1 << 28, 1 << 20, 1 << 32, 1 << 52
-_MAX_TOKENS = 1 << 23    # of one moe_combine_rows
+_MAX_TOKENS = 1 << 23    # of one moe_combine_rows, weighted or not, or moe_combine_rows_backward
 _MAX_BATCH, _MAX_BLOCKS = 65535, (1 << 23) - 1   # quantisation: matrices; 128 x 128 blocks of one
 _MAX_SPLITS = 64
 
